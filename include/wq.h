@@ -23,6 +23,10 @@
  *           LUT[q] * S (NF4-style, wq_gemm_w4a16_lut).
  *   W2A16   2-bit codes, four per byte along K, (q - 2) * S (wq_gemm_w2a16).
  *
+ * Between the projections of an attention layer: norms and rotation of queries and
+ * keys (wq_qk_norm_rope), a paged key / value cache held in 4 bits (wq_kv4_write,
+ * wq_kv4_read) and attention over it (wq_attn_kv4).
+ *
  * Conventions for every entry point:
  *   - All arrays are row-major and live in device memory unless stated.  The
  *     caller allocates and owns every buffer; the library never allocates,
@@ -72,7 +76,8 @@ typedef enum {
     WQ_ERR_WORKSPACE = 6,           /* workspace missing or smaller than required */
     WQ_ERR_UNSUPPORTED_DEVICE = 7,  /* current device is not compute capability 10.3 */
     WQ_ERR_CUDA = 8,                /* a CUDA runtime call failed */
-    WQ_ERR_TIMEOUT = 9              /* a kernel gave up on a bounded wait (device status) */
+    WQ_ERR_TIMEOUT = 9,             /* a kernel gave up on a bounded wait (device status) */
+    WQ_ERR_INDEX = 10               /* a kernel met a slot, page or position out of range (device status) */
 } wq_status;
 
 /* Human-readable name of a status. */
@@ -297,6 +302,110 @@ wq_status wq_gemm_bf16_fp4(const void* A, const uint8_t* w_e2m1, const uint8_t* 
                            int64_t M, int64_t N, int64_t K, void* out, void* ws, size_t ws_bytes,
                            wq_stream_t stream);
 
+/* ------------------------------------------------------------------ queries and keys */
+
+/* Norms of queries and keys for each head and their rotation by position, in one pass
+ * over q [T][Hq][D] and k [T][Hkv][D].  For each row x of D values, in fp32 with one
+ * rounding at the end:
+ *     y = x * rsqrt(mean(x^2) + eps) * w        (w = q_weight or k_weight, [D] of `dtype`;
+ *                                                a NULL weight leaves that tensor unnormed)
+ *     out = y with its first `rot` values rotated in pairs (a, b) by the token's angles:
+ *           (a cos_i - b sin_i, b cos_i + a sin_i),  i = 0 .. rot / 2 - 1
+ * interleaved == 0: pair i is (y[i], y[i + rot / 2]); 1: (y[2 i], y[2 i + 1]).
+ * cos_sin: fp32 [max_pos][rot], a row holds the rot / 2 cosines, then the rot / 2 sines.
+ * positions: int64 [T], the row of each token.  A position outside [0, max_pos) sets the
+ * index bit of the device status and leaves that token's outputs unwritten.
+ * q_stride, k_stride and the output strides are elements from token to token (heads of a
+ * token are contiguous), so q and k may be slices of one packed projection.  An output may
+ * be its own input (same pointer and stride); any other overlap is undefined.
+ * Requirements: T >= 0, Hq >= 1, Hkv >= 1, D % 8 == 0, 8 <= D <= 256, rot % 8 == 0,
+ * 8 <= rot <= D, eps >= 0, strides >= heads * D and multiples of 4; pointers 8-byte
+ * aligned, cos_sin 16-byte aligned. */
+wq_status wq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, wq_dtype dtype,
+                          int64_t T, int32_t Hq, int32_t Hkv, int32_t D, const void* q_weight, const void* k_weight,
+                          float eps, const int64_t* positions, const float* cos_sin, int64_t max_pos, int32_t rot,
+                          int32_t interleaved, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                          wq_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit cache */
+
+/* A paged key / value cache held in 4 bits.  pages: uint8 [num_pages][kv_heads][block],
+ * one block for each page of P = page_size tokens and each head, holding in this order
+ *     key codes    uint8 [P][D / 2]           (even d in the low nibble)
+ *     value codes  uint8 [P][D / 2]
+ *     key pairs    dtype [P][D / G][2]        (s, lo) of each group of G values
+ *     value pairs  dtype [P][D / G][2]
+ * (P (D + 8 D / G) bytes).  Code q of a group stands for the 16-bit number
+ *     value = RN(lo + q * s)                  (one rounding to dtype)
+ * and it is these values that wq_kv4_read returns and wq_attn_kv4 attends to. */
+typedef struct {
+    int64_t num_pages;
+    int32_t kv_heads;    /* >= 1 */
+    int32_t head_dim;    /* D: 64 or 128 */
+    int32_t group;       /* G: 32, 64 or 128, at most D */
+    int32_t page_size;   /* P: 16, 32, 64 or 128 tokens */
+    int32_t dtype;       /* wq_dtype of keys, values and pairs */
+} wq_kv4_layout;
+
+/* Bytes of one page (all heads); the cache is num_pages times that.  Host only. */
+wq_status wq_kv4_page_bytes(const wq_kv4_layout* layout, size_t* bytes);
+
+/* Quantises the keys and values of T tokens into their slots.  k, v: dtype, heads of a
+ * token contiguous, k_stride / v_stride elements from token to token.  slots: int64 [T],
+ * page * P + place in the page.  A negative slot skips its token; a slot past the cache
+ * sets the index bit of the device status and skips it; of tokens that share a slot any
+ * may win.  For each group of G values:
+ *     lo = min,  s = RN((max - lo) / 15),  q = nearest integer to (x - lo) / s in 0..15
+ * (half to even; q = 0 where s is 0), decided on fp32 differences; where lo + 15 s would
+ * overflow the type, s is the next number below.  A group that holds an
+ * infinity or a NaN, or whose range overflows fp32, is stored as NaN throughout and
+ * touches no other group.
+ * Requirements: T >= 0, strides >= kv_heads * D and multiples of 8; k, v and pages
+ * 16-byte aligned, slots 8-byte aligned. */
+wq_status wq_kv4_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
+                       int64_t T, const wq_kv4_layout* layout, uint8_t* pages, wq_stream_t stream);
+
+/* The values that the cache holds in T slots, to k and v (as for wq_kv4_write).  A slot
+ * that is negative or past the cache gives zeros; the latter also sets the index bit of
+ * the device status. */
+wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const int64_t* slots, int64_t T, void* k,
+                      int64_t k_stride, void* v, int64_t v_stride, wq_stream_t stream);
+
+/* Attention of the new tokens of B sequences over their cached keys and values.
+ * Sequence b has kv_lens[b] = L tokens in the cache, its new ones (already written) among
+ * them, in the pages block_table[b][0], block_table[b][1], ...; its n = cu_q[b + 1] -
+ * cu_q[b] queries are rows cu_q[b] .. of q [T][q_heads][D] and stand at positions
+ * L - n .. L - 1.  cu_q NULL: one query for each sequence (T = B).  Query head h reads
+ * key head h / (q_heads / kv_heads).  With the visible tokens j of a query at position p
+ * (j < L; causal: j <= p; window > 0: also j > p - window):
+ *     out = sum_j softmax_j(scale * q . K_j) V_j
+ *     lse = log sum_j exp(scale * q . K_j)          (fp32 [T][q_heads], may be NULL)
+ * accumulated in fp32, one rounding of out; the probabilities are rounded to dtype as
+ * operands of the tensor cores.  A query that sees nothing gets out = 0, lse = -inf.
+ * What pages hold past a sequence's length, NaN included, has no effect, and a NaN among
+ * a sequence's keys or values only reaches the queries that see it: a key makes all of
+ * their out NaN, a value at least the places where it stands.
+ * kv_lens, cu_q and block_table are read on the device: a CUDA graph that captured the
+ * call replays with new lengths.  max_q bounds n for the choice of kernel (a larger n is
+ * still right).  Lengths are cut to table_stride * P (a longer one sets the index bit of
+ * the device status), decreasing cu_q counts as n = 0, rows past T do not exist, and a
+ * page outside the cache sets the index bit (page 0 is read in its place).
+ * q_stride / out_stride: elements from token to token.  Results do not change from run to
+ * run.  ws: at least wq_attn_kv4_workspace_bytes bytes, 16-byte aligned; its first 16 KiB
+ * hold arrival counters: zero-fill them once, every call leaves them zero; calls that
+ * share a workspace must not overlap on the GPU.
+ * Requirements: B >= 0, T >= 0, q_heads a multiple of kv_heads, window >= 0 and 0 unless
+ * causal, scale finite, 1 <= max_q, strides >= q_heads * D and multiples of 8; q, out
+ * and pages 16-byte aligned, the int32 arrays and lse 4-byte aligned. */
+wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const int32_t* cu_q, int64_t B, int64_t T,
+                      int64_t max_q, const uint8_t* pages, const wq_kv4_layout* layout, const int32_t* block_table,
+                      int64_t table_stride, const int32_t* kv_lens, float scale, int32_t causal, int32_t window,
+                      void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes, wq_stream_t stream);
+
+/* Workspace bytes of wq_attn_kv4 on the current device for these heads and max_q, whatever
+ * the lengths, the number of sequences and the cache's size.  Host only. */
+wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_heads, int64_t max_q, size_t* bytes);
+
 /* ------------------------------------------------------------------ planning */
 
 /* The launch plan the library picks for a problem (deterministic in the
@@ -393,8 +502,9 @@ wq_status wq_gemm_w4a16_noalloc(const void* A, wq_dtype a_dtype, const uint8_t* 
 
 /* Reads the current device's status word: bit 0..3 = a bounded wait timed out in
  * the producer / MMA / transform / epilogue role, bit 4 = draining after a
- * timeout timed out, bit 5 = the wait probe timed out.  Synchronous (copies one
- * word); returns WQ_ERR_TIMEOUT when any bit is set. */
+ * timeout timed out, bit 5 = the wait probe timed out, bit 6 = a slot, page, length or
+ * position out of range.  Synchronous (copies one word); returns WQ_ERR_TIMEOUT when any
+ * of bits 0..5 is set, WQ_ERR_INDEX when only bit 6 is. */
 wq_status wq_device_status(uint32_t* bits);
 
 /* Clears the current device's status word (synchronous). */

@@ -4,7 +4,18 @@ out[M, N] = A[M, K] . dequant(W)[N, K]^T with fp16/bf16 activations, fp32
 accumulation, and INT4 (group-scaled, symmetric, zero-point or codebook), INT2
 (group-scaled), FP8-e4m3 (per-tensor scale) or FP4-e2m1 (block-scaled) weights.  The computation runs in hand-written CUDA kernels in
 libwq.so (C ABI: include/wq.h); this package only binds it.
+
+Between the projections of an attention layer: norm + rotation of queries and keys, a
+paged key / value cache held in 4 bits, and attention over it.
 """
+from ._attn import (  # noqa: F401
+    wq_attn_kv4,
+    wq_kv4_page_bytes,
+    wq_kv4_pages,
+    wq_kv4_read,
+    wq_kv4_write,
+    wq_qk_norm_rope,
+)
 from ._lib import (  # noqa: F401
     WQError,
     get_plan,

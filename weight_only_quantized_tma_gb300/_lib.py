@@ -24,7 +24,7 @@ WQ_KERNEL_TILE, WQ_KERNEL_DECODE, WQ_KERNEL_TILE_PAIR = 0, 1, 2
 STATUS_NAMES = {
     0: "WQ_OK", 1: "WQ_ERR_NULL", 2: "WQ_ERR_SHAPE", 3: "WQ_ERR_GROUP", 4: "WQ_ERR_MISALIGNED",
     5: "WQ_ERR_DTYPE", 6: "WQ_ERR_WORKSPACE", 7: "WQ_ERR_UNSUPPORTED_DEVICE", 8: "WQ_ERR_CUDA",
-    9: "WQ_ERR_TIMEOUT",
+    9: "WQ_ERR_TIMEOUT", 10: "WQ_ERR_INDEX",
 }
 
 _lock = threading.Lock()
@@ -84,6 +84,14 @@ _SIGNATURES = {
     "wq_clear_device_status": (ctypes.c_int, []),
     "wq_debug_wait_probe": (ctypes.c_int, [_i64, _vp]),
     "wq_gemm_w4a16_noalloc": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "wq_qk_norm_rope": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i32, _i32, _i32, _vp, _vp,
+                                       ctypes.c_float, _vp, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "wq_kv4_page_bytes": (ctypes.c_int, [_vp, ctypes.POINTER(_sz)]),
+    "wq_kv4_write": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "wq_kv4_read": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "wq_attn_kv4": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, ctypes.c_float,
+                                   _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "wq_attn_kv4_workspace_bytes": (ctypes.c_int, [_vp, _i32, _i64, ctypes.POINTER(_sz)]),
     "wq_debug_fastdiv": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_uint32, _vp, _i64, _vp, ctypes.POINTER(_i32)]),
 }
 
@@ -473,7 +481,7 @@ def wq_gemm_bf16_fp4(A: torch.Tensor, w: torch.Tensor, sf_kernel: torch.Tensor, 
 def wq_device_status() -> int:
     bits = ctypes.c_uint32(0)
     st = lib().wq_device_status(ctypes.byref(bits))
-    if st not in (0, 9):
+    if st not in (0, 9, 10):
         raise WQError(st, "wq_device_status")
     return bits.value
 

@@ -466,6 +466,15 @@ wq_status finish_launch(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ER
 const int64_t kMaxDim = (1LL << 31) - 1;
 
 }  // namespace
+
+int current_device_state(DeviceState* out) {
+    DeviceInfo* d = nullptr;
+    const wq_status st = device_info(&d);
+    if (st != WQ_OK) return st;
+    *out = DeviceState{d->sms, d->status, kTimeoutNs};
+    return WQ_OK;
+}
+
 }  // namespace wq
 
 using namespace wq;
@@ -484,6 +493,7 @@ const char* wq_status_string(wq_status s) {
         case WQ_ERR_UNSUPPORTED_DEVICE: return "WQ_ERR_UNSUPPORTED_DEVICE: requires compute capability 10.3";
         case WQ_ERR_CUDA: return "WQ_ERR_CUDA: CUDA runtime error";
         case WQ_ERR_TIMEOUT: return "WQ_ERR_TIMEOUT: a kernel gave up on a bounded wait";
+        case WQ_ERR_INDEX: return "WQ_ERR_INDEX: a kernel met a slot, page, length or position out of range";
     }
     return "unknown wq_status";
 }
@@ -907,7 +917,8 @@ wq_status wq_device_status(uint32_t* bits) {
     wq_status st = device_info(&d);
     if (st != WQ_OK) return st;
     if (cudaMemcpy(bits, d->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess) return WQ_ERR_CUDA;
-    return *bits ? WQ_ERR_TIMEOUT : WQ_OK;
+    if (*bits & ~DEVICE_INDEX) return WQ_ERR_TIMEOUT;
+    return *bits ? WQ_ERR_INDEX : WQ_OK;
 }
 
 wq_status wq_clear_device_status(void) {

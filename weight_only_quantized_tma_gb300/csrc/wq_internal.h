@@ -127,6 +127,7 @@ constexpr uint32_t DEVICE_TIMEOUT_MMA = 1u << 1;
 constexpr uint32_t DEVICE_TIMEOUT_TRANSFORM = 1u << 2;
 constexpr uint32_t DEVICE_TIMEOUT_EPILOGUE = 1u << 3;
 constexpr uint32_t DEVICE_TIMEOUT_DRAIN = 1u << 4;
+constexpr uint32_t DEVICE_INDEX = 1u << 6;   // a slot, page, length or position out of range
 
 // Largest split-K cluster of the decode kernel (non-portable cluster size).
 constexpr int kMaxDecodeCluster = 16;
@@ -221,6 +222,75 @@ cudaError_t launch_dequant_fp4(const uint8_t* w, const uint8_t* sfk, int64_t N, 
                                cudaStream_t st);
 cudaError_t launch_dequant_fp8(const uint8_t* w, int64_t N, int64_t K, bool bf16, float* out, cudaStream_t st);
 cudaError_t launch_wait_probe(uint32_t* status, long long timeout_ns, cudaStream_t st);
+
+// What an entry point outside wq_api.cu needs of the current device; returns a wq_status.
+struct DeviceState {
+    int sms;
+    uint32_t* status;
+    long long timeout_ns;
+};
+int current_device_state(DeviceState* out);
+
+// The 4-bit cache (wq_kv4_layout in include/wq.h) as the kernels see it.
+struct Kv4View {
+    uint8_t* pages;
+    int64_t num_pages;
+    int64_t page_bytes;   // all heads
+    int32_t block_bytes;  // one head: P (D + 8 D / G)
+    int32_t heads;
+    int32_t D, G, P;
+    int32_t p_shift, g_shift;
+};
+
+struct RopeParams {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;   // elements
+    const void* q_weight;
+    const void* k_weight;
+    const int64_t* positions;
+    const float* cos_sin;
+    int64_t T, max_pos;
+    int Hq, Hkv, D, rot, interleaved;
+    float eps;
+    uint32_t* status;
+};
+cudaError_t launch_qk_norm_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st);   // wq_rope.cu
+
+struct Kv4RowsParams {   // write and read
+    Kv4View c;
+    const void* k;       // read: the outputs
+    const void* v;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+    int64_t T;
+    uint32_t* status;
+};
+cudaError_t launch_kv4_write(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);   // wq_kv4.cu
+cudaError_t launch_kv4_read(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);
+
+struct AttnParams {
+    Kv4View c;
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_stride, out_stride;   // elements
+    const int32_t* cu_q;            // null: one query for each sequence
+    const int32_t* table;
+    const int32_t* lens;
+    int64_t table_stride;
+    int64_t B, T;
+    int Hq, group;                  // query heads, query heads for each key head
+    int causal, window;
+    float scale;
+    uint32_t* ws_count;
+    float* ws_part;
+    uint32_t* status;
+    long long timeout_ns;
+};
+cudaError_t launch_attn_kv4_simple(const AttnParams& p, bool bf16, int sms, cudaStream_t st);   // wq_attn_simple.cu
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 

@@ -1,0 +1,105 @@
+// wq_kv4.cuh -- device helpers for the 4-bit key / value cache (include/wq.h,
+// wq_kv4_layout): 16-bit arithmetic in the cache's type, the unpack of code words and
+// addressing inside a page block.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sm103_ptx.cuh"
+#include "wq_internal.h"
+
+namespace wq {
+
+// Two values of the cache's type in a register.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (BF16) return ptx::f32x2_to_bf16x2(lo, hi);
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+    if (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// a * b + c on both halves, one rounding each (subnormals kept).
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    if (BF16)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16)
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Smaller / larger of both halves; a NaN in either operand gives NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16)
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Codes to numbers.  A code OR-ed into the low mantissa bits of a constant gives
+// base + q (fp16: 1024 + q at bits 0-3, 64 + q at bits 4-7; bf16: 128 + q at bits
+// 0-3); subtracting the base is exact, and one fma gives RN(lo + q * s).
+template <bool BF16>
+struct Codes {
+    static constexpr uint32_t kMagic = BF16 ? 0x43004300u : 0x64006400u;
+    // codes in bits 0-3 and 16-19 of x
+    static __device__ __forceinline__ uint32_t low(uint32_t x) {
+        return sub2<BF16>(ptx::lop3_and_or(x, 0x000F000Fu, kMagic), kMagic);
+    }
+    // codes in bits 4-7 and 20-23
+    static __device__ __forceinline__ uint32_t high(uint32_t x) {
+        if (BF16) return low(x >> 4);
+        return sub2<false>(ptx::lop3_and_or(x, 0x00F000F0u, 0x54005400u), 0x54005400u);
+    }
+};
+
+// Eight codes of one word to the values of d = 0..7 in order, as four pairs.
+// s2, lo2: the group's s and lo in both halves.
+template <bool BF16>
+__device__ __forceinline__ uint4 word_values(uint32_t w, uint32_t s2, uint32_t lo2) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = (w >> (8 * i)) & 0xFFu;
+        o[i] = fma2<BF16>(Codes<BF16>::low(b | (b << 12)), s2, lo2);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Offsets inside a page block.
+__device__ __forceinline__ int kv4_codes_at(const Kv4View& c, int which, int place) {
+    return (which * c.P + place) * (c.D >> 1);
+}
+__device__ __forceinline__ int kv4_pairs_at(const Kv4View& c, int which, int place) {
+    return c.P * c.D + (which * c.P + place) * ((c.D >> c.g_shift) * 4);
+}
+
+}  // namespace wq
