@@ -1,6 +1,7 @@
 // wq_attn_api.cu -- C entry points between the projections of an attention layer
 // (include/wq.h): norm + rotation, the 4-bit cache, attention over it.  Argument
 // validation and launches; host code only.
+#include <algorithm>
 #include <cmath>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -151,7 +152,7 @@ wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_hea
     if (q_heads < 1 || q_heads > 65535 || q_heads % v.heads != 0 || max_q < 1) return WQ_ERR_SHAPE;
     DeviceState d{};
     if ((st = (wq_status)current_device_state(&d)) != WQ_OK) return st;
-    *bytes = 0;
+    *bytes = attn_kv4_decode_ws(v, layout->dtype == WQ_BF16, max_q * (q_heads / v.heads), d.sms);
     return WQ_OK;
 }
 
@@ -195,7 +196,13 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
     p.scale = scale;
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
-    return finish_launch(launch_attn_kv4_simple(p, layout->dtype == WQ_BF16, d.sms, (cudaStream_t)stream));
+    const bool bf16 = layout->dtype == WQ_BF16;
+    const int64_t rows = std::min<int64_t>(max_q, T) * p.group;
+    const size_t need = attn_kv4_decode_ws(p.c, bf16, rows, d.sms);
+    if (!ws || ws_bytes < need) return WQ_ERR_WORKSPACE;
+    p.ws_count = static_cast<uint32_t*>(ws);
+    p.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
+    return finish_launch(launch_attn_kv4_decode(p, bf16, rows, d.sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,511 @@
+// wq_attn_decode.cuh -- attention of few query rows over the 4-bit cache.
+//
+//   S^T = K Q^T,  P = exp2(scale' S - m),  O^T += V^T P^T,  out = O / sum P
+//
+// Bound by the bytes of the cache (D + 8 D / G for each token and key head), so the
+// kernel streams them once, with the fewest instructions for each code:
+//   * cached tokens are the M dimension of the mma.sync m16n8k16 tiles (16 tokens x 8 query
+//     rows), so the 8 rows of a group of heads fill a tile that single tokens leave empty
+//     the other way round, and a lane's K operand is consecutive codes of one token;
+//   * the order of d inside a product is free: lane c of a quad takes codes c D / 4 ..
+//     (c + 1) D / 4 of its token, all in one group (G >= 32 >= D / 4), so one pair (s, lo)
+//     serves it; Q is loaded in the same order.  V^T: lane g takes codes g D / 8 .. of four
+//     tokens; two tokens' words are merged with byte permutes, since a pair of the V^T
+//     operand is two tokens of one d;
+//   * code -> number is one LOP3 (magic number), one exact subtraction and one fma,
+//     RN(lo + q s): the value that the cache stands for, in every kernel;
+//   * the running maximum moves only when a score passes it by more than 2^8, so most
+//     tiles pay one vote in place of a reduction.
+// Warps 0-3 each take 16 of the 64 tokens of a tile with their own maximum, sum and O and
+// meet once for each item; warp 4 copies page blocks into a ring with bulk copies.
+#pragma once
+
+#include "wq_attn_sched.cuh"
+#include "wq_common.cuh"
+
+namespace wq {
+
+constexpr int kDecodeTN = 64;      // tokens of a tile
+constexpr int kDecodeStages = 4;
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+template <int D, int NT>
+struct DecodeCfg {
+    static constexpr int R = 8 * NT;
+    static constexpr int KS = D / 16;              // k steps of Q K^T = m tiles of V^T
+    static constexpr bool Q_SMEM = NT > 1;         // Q operands: registers, or shared memory
+    static constexpr int REGS = KS * NT * 4 + 4 * NT;                     // a lane's O, m and l
+    static constexpr int OFF_EX = 0;                                      // two warps' results
+    static constexpr int EX_BYTES = 2 * REGS * 32 * 4;
+    static constexpr int OFF_Q = OFF_EX + EX_BYTES;
+    static constexpr int Q_BYTES = Q_SMEM ? KS * NT * 32 * 8 : 0;
+    static constexpr int OFF_W = OFF_Q + Q_BYTES;                         // merge weights
+    static constexpr int W_BYTES = R * 33 * 4;
+    static constexpr int OFF_BAR = (OFF_W + W_BYTES + 15) / 16 * 16;
+    static constexpr int OFF_MISC = OFF_BAR + 2 * kDecodeStages * 8;
+    static constexpr int OFF_RING = (OFF_MISC + 16 + 127) / 128 * 128;
+    static constexpr int MIN_BLOCKS = NT == 1 ? 3 : 2;
+};
+
+// The token of row r (0..15) of a 16-token tile: neighbours differ in parity (K rows of a
+// quad pair fall on both halves of the banks) and so do a quad's rows 0, 2, 4, 6 (V).
+__device__ __forceinline__ int token_of_row(int r) { return r ^ ((r >> 1) & 1); }
+
+template <bool BF16, int D, int NT>
+__global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_decode_kernel(const AttnParams p,
+                                                                                          const int stage_bytes) {
+    using C = DecodeCfg<D, NT>;
+    constexpr int R = C::R, KS = C::KS, TN = kDecodeTN, ST = kDecodeStages;
+    constexpr int WK = D / 32;        // words of codes of a lane and token: K
+    constexpr int WV = D / 64;        // V
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto full_bar = [&](int s) { return sbase + C::OFF_BAR + 8u * s; };
+    auto empty_bar = [&](int s) { return sbase + C::OFF_BAR + 8u * (ST + s); };
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 4);
+        }
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    __syncthreads();
+    // every input may come from the kernel before
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    Walk w;
+    int used;
+    const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
+    const int vp = min(p.c.P, TN);                              // tokens of a page inside a tile
+    const int pair_row = 4 * (D >> p.c.g_shift);                // bytes of a token's pairs
+    const int vblock = vp * (D + 2 * pair_row);                 // a (part of a) page block in the ring
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        const uint64_t pol = ptx::policy_evict_first();
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        uint32_t issued = 0;
+        for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
+            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > (p.table_stride << p.c.p_shift))
+                atomicOr(p.status, DEVICE_INDEX);
+            const int tb = w.v.t0 + (int)(w.u - w.item0), te = w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0);
+            for (int t = tb; t < te && ok; ++t) {
+                const int tok = t * TN;
+                // the tile's pages that hold a token to be seen: [skip, pages)
+                const int pages = min((w.v.hi - tok + vp - 1) / vp, TN / vp);
+                const int skip = max(w.v.lo - tok, 0) / vp;
+                int64_t page = 0;
+                const bool parted = p.c.P > TN;
+                if (parted ? (lane < 4 && pages > 0) : (lane >= skip && lane < pages))
+                    page = safe_page(p, w.b, (tok >> p.c.p_shift) + (parted ? 0 : lane));
+                ok = bounded_wait(empty_bar(s), ph ^ 1u, abort_flag, p.status, DEVICE_TIMEOUT_PRODUCER, p.timeout_ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (pages > 0)
+                        ptx::mbar_arrive_expect_tx(full_bar(s), (uint32_t)((pages - skip) * vblock));
+                    else
+                        ptx::mbar_arrive(full_bar(s));
+                }
+                __syncwarp();
+                const uint32_t dst = sbase + C::OFF_RING + s * stage_bytes;
+                const uint8_t* block = p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes;
+                if (!parted) {
+                    if (lane >= skip && lane < pages) ptx::bulk_load(dst + lane * vblock, block, vblock, full_bar(s), pol);
+                } else if (lane < 4 && pages > 0) {
+                    // half of a page of 128: four pieces (codes and pairs of keys and of values)
+                    const int place = tok & (p.c.P - 1);
+                    const int which = lane & 1;
+                    if (lane < 2)
+                        ptx::bulk_load(dst + which * vp * (D / 2), block + kv4_codes_at(p.c, which, place), vp * (D / 2),
+                                       full_bar(s), pol);
+                    else
+                        ptx::bulk_load(dst + vp * D + which * vp * pair_row, block + kv4_pairs_at(p.c, which, place),
+                                       vp * pair_row, full_bar(s), pol);
+                }
+                issued |= 1u << s;
+                if (++s == ST) s = 0, ph ^= 1u;
+            }
+        }
+        if (!ok) {
+            // given up: let the copies in flight land before the block may end.  A stage
+            // passed in this lap was filled with parity ph, the others in the lap before.
+            for (int i = 0; i < ST; ++i)
+                if (issued >> i & 1u) drain_wait(full_bar(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- compute warps
+    const int g = lane >> 2, c = lane & 3;
+    const float sl2 = p.scale * 1.4426950408889634f;
+    float* ex = reinterpret_cast<float*>(smem + C::OFF_EX);
+    uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
+    // this warp's 16 tokens inside a tile (fixed: pages hold a multiple of 16)
+    const int in_page = (16 * warp) & (vp - 1);
+    const uint32_t page_at = (uint32_t)((16 * warp) / vp * vblock);
+    const int row_k[2] = {token_of_row(g), token_of_row(g) + 8};
+    const int row_v[4] = {token_of_row(2 * c), token_of_row(2 * c + 1), token_of_row(2 * c) + 8,
+                          token_of_row(2 * c + 1) + 8};
+    const uint32_t k_codes = page_at + in_page * (D / 2), v_codes = page_at + (vp + in_page) * (D / 2);
+    const uint32_t k_pairs = page_at + vp * D + in_page * pair_row, v_pairs = k_pairs + vp * pair_row;
+    const int k_group = ((c * (D / 4)) >> p.c.g_shift) * 4, v_group = ((g * (D / 8)) >> p.c.g_shift) * 4;
+
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    uint32_t qr[C::Q_SMEM ? 1 : KS][2];
+
+    for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
+        const int rows = (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R);
+        // ---- Q operands of the item, in the order of the codes
+        auto load_q = [&](int nt, uint32_t (&q)[KS][2]) {
+            const int r = nt * 8 + g;
+            uint32_t raw[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
+            if (r < rows) {
+                const int64_t row = (int64_t)w.rt * R + r;
+                const int64_t t = w.s.q0 + row / p.group;
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + t * p.q_stride +
+                                      (int64_t)(w.head * p.group + (int)(row % p.group)) * D + c * (D / 4);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
+                    raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < WK; ++j) {   // values 8j .. 8j + 7: pairs (0,4) (1,5) (2,6) (3,7)
+                q[2 * j][0] = __byte_perm(raw[4 * j], raw[4 * j + 2], 0x5410);
+                q[2 * j][1] = __byte_perm(raw[4 * j], raw[4 * j + 2], 0x7632);
+                q[2 * j + 1][0] = __byte_perm(raw[4 * j + 1], raw[4 * j + 3], 0x5410);
+                q[2 * j + 1][1] = __byte_perm(raw[4 * j + 1], raw[4 * j + 3], 0x7632);
+            }
+        };
+        if constexpr (C::Q_SMEM) {
+            ptx::named_barrier_sync(1, 128);
+            for (int nt = warp; nt < NT; nt += 4) {
+                uint32_t q[KS][2];
+                load_q(nt, q);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) qs[(k * NT + nt) * 32 + lane] = make_uint2(q[k][0], q[k][1]);
+            }
+            ptx::named_barrier_sync(1, 128);
+        } else {
+            load_q(0, qr);
+        }
+        // tokens that each of this lane's rows sees: [lo, hi)
+        int lo[NT][2], hi[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t row = (int64_t)w.rt * R + nt * 8 + 2 * c + i;
+                const int pos = w.s.L - w.s.n + (int)(row / p.group);
+                hi[nt][i] = p.causal ? min(w.s.L, pos + 1) : w.s.L;
+                lo[nt][i] = p.window > 0 ? pos + 1 - p.window : 0;
+            }
+        // tokens that every row sees
+        const int pos0 = w.s.L - w.s.n + (int)((int64_t)w.rt * R / p.group);
+        const int pos1 = w.s.L - w.s.n + (int)(((int64_t)w.rt * R + rows - 1) / p.group);
+        const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
+        const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
+
+        float o[KS][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[k][nt][i] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+
+        const int tb = w.v.t0 + (int)(w.u - w.item0), te = w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0);
+        for (int t = tb; t < te; ++t) {
+            if (ok) ok = __all_sync(0xffffffffu, bounded_wait(full_bar(s), ph, abort_flag, p.status,
+                                                              DEVICE_TIMEOUT_TRANSFORM, p.timeout_ns));
+            const int tok = t * TN + 16 * warp;
+            if (ok && tok < w.v.hi && tok + 16 > w.v.lo) {
+                const uint8_t* st = smem + C::OFF_RING + s * stage_bytes;
+                const bool masked = tok < all_lo || tok + 16 > all_hi;
+                // ---- S^T: 16 tokens x R rows
+                uint32_t kw[2][WK], kp[2], vw[4][WV], vpair[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* src = st + k_codes + row_k[i] * (D / 2) + c * (D / 8);
+                    if constexpr (WK == 4) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src);
+                        kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(src);
+                        kw[i][0] = v.x, kw[i][1] = v.y;
+                    }
+                    kp[i] = *reinterpret_cast<const uint32_t*>(st + k_pairs + row_k[i] * pair_row + k_group);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* src = st + v_codes + row_v[i] * (D / 2) + g * (D / 16);
+                    if constexpr (WV == 2) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(src);
+                        vw[i][0] = v.x, vw[i][1] = v.y;
+                    } else {
+                        vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                    }
+                    vpair[i] = *reinterpret_cast<const uint32_t*>(st + v_pairs + row_v[i] * pair_row + v_group);
+                }
+                if (masked) {
+                    // What a row does not see must not reach it as 0 * NaN: values that
+                    // nobody sees are cleared, and a NaN among a seen token's values moves
+                    // to its key, where the mask of each row applies.
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t z = 0;
+                        for (int j = 0; j < pair_row; j += 4)
+                            z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(st + v_pairs + row_k[i] * pair_row + j), 0u, z);
+                        if (z & 0x7FFF7FFFu) kp[i] = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tt = tok + row_v[i];
+                        if (tt < w.v.lo || tt >= w.v.hi || (fma2<BF16>(vpair[i], 0u, 0u) & 0x7FFF7FFFu)) vpair[i] = 0u;
+                    }
+                }
+                float sc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+                const uint32_t ks0 = __byte_perm(kp[0], 0, 0x1010), kl0 = __byte_perm(kp[0], 0, 0x3232);
+                const uint32_t ks1 = __byte_perm(kp[1], 0, 0x1010), kl1 = __byte_perm(kp[1], 0, 0x3232);
+#pragma unroll
+                for (int j = 0; j < WK; ++j) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x0 = h ? kw[0][j] >> 8 : kw[0][j], x1 = h ? kw[1][j] >> 8 : kw[1][j];
+                        const uint32_t a[4] = {fma2<BF16>(Codes<BF16>::low(x0), ks0, kl0),
+                                               fma2<BF16>(Codes<BF16>::low(x1), ks1, kl1),
+                                               fma2<BF16>(Codes<BF16>::high(x0), ks0, kl0),
+                                               fma2<BF16>(Codes<BF16>::high(x1), ks1, kl1)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (C::Q_SMEM) {
+                                const uint2 q = qs[((2 * j + h) * NT + nt) * 32 + lane];
+                                mma16816<BF16>(sc[nt], a, q.x, q.y);
+                            } else {
+                                mma16816<BF16>(sc[nt], a, qr[2 * j + h][0], qr[2 * j + h][1]);
+                            }
+                        }
+                    }
+                }
+                // ---- probabilities (scores in units of log2)
+                bool grow = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x0 = sc[nt][i] * sl2, x1 = sc[nt][2 + i] * sl2;
+                        if (masked) {
+                            const int t0 = tok + row_k[0], t1 = tok + row_k[1];
+                            if (t0 < lo[nt][i] || t0 >= hi[nt][i]) x0 = -INFINITY;
+                            if (t1 < lo[nt][i] || t1 >= hi[nt][i]) x1 = -INFINITY;
+                        }
+                        sc[nt][i] = x0, sc[nt][2 + i] = x1;
+                        grow |= fmaxf(x0, x1) > m[nt][i] + 8.f;
+                    }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = fmaxf(sc[nt][i], sc[nt][2 + i]);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, m[nt][i]);
+                            f[i] = part_weight(m[nt][i], x);
+                            m[nt][i] = x;
+                            l[nt][i] *= f[i];
+                        }
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+                            o[k][nt][0] *= f[0], o[k][nt][2] *= f[0], o[k][nt][1] *= f[1], o[k][nt][3] *= f[1];
+                    }
+                }
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                    const float p0 = ex2(sc[nt][0] - m0), p1 = ex2(sc[nt][1] - m1), p2 = ex2(sc[nt][2] - m0),
+                                p3 = ex2(sc[nt][3] - m1);
+                    l[nt][0] += p0 + p2;
+                    l[nt][1] += p1 + p3;
+                    pb[nt][0] = transpose8x8(pack2<BF16>(p0, p1));
+                    pb[nt][1] = transpose8x8(pack2<BF16>(p2, p3));
+                }
+                // ---- O^T += V^T P^T
+                const uint32_t sab = __byte_perm(vpair[0], vpair[1], 0x5410), lab = __byte_perm(vpair[0], vpair[1], 0x7632);
+                const uint32_t scd = __byte_perm(vpair[2], vpair[3], 0x5410), lcd = __byte_perm(vpair[2], vpair[3], 0x7632);
+#pragma unroll
+                for (int j = 0; j < WV; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t sel = 0x4400u + 0x1111u * i;
+                        const uint32_t xab = __byte_perm(vw[0][j], vw[1][j], sel), xcd = __byte_perm(vw[2][j], vw[3][j], sel);
+                        const uint32_t a[4] = {fma2<BF16>(Codes<BF16>::low(xab), sab, lab),
+                                               fma2<BF16>(Codes<BF16>::high(xab), sab, lab),
+                                               fma2<BF16>(Codes<BF16>::low(xcd), scd, lcd),
+                                               fma2<BF16>(Codes<BF16>::high(xcd), scd, lcd)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[4 * j + i][nt], a, pb[nt][0], pb[nt][1]);
+                    }
+            }
+            __syncwarp();
+            if (ok && lane == 0) ptx::mbar_arrive(empty_bar(s));
+            if (++s == ST) s = 0, ph ^= 1u;
+        }
+
+        // ---- the four warps' results, pairwise
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+            }
+        auto put = [&](int slot) {
+            float* e = ex + slot * C::REGS * 32 + lane;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[((k * NT + nt) * 4 + i) * 32] = o[k][nt][i];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    e[(KS * NT * 4 + nt * 4 + i) * 32] = m[nt][i];
+                    e[(KS * NT * 4 + nt * 4 + 2 + i) * 32] = l[nt][i];
+                }
+            }
+        };
+        auto add = [&](int slot) {
+            const float* e = ex + slot * C::REGS * 32 + lane;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float f[2], h[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float m2 = e[(KS * NT * 4 + nt * 4 + i) * 32], l2 = e[(KS * NT * 4 + nt * 4 + 2 + i) * 32];
+                    const float M = fmaxf(m[nt][i], m2);
+                    f[i] = part_weight(m[nt][i], M), h[i] = part_weight(m2, M);
+                    m[nt][i] = M;
+                    l[nt][i] = l[nt][i] * f[i] + l2 * h[i];
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[k][nt][i] = o[k][nt][i] * f[i & 1] + e[((k * NT + nt) * 4 + i) * 32] * h[i & 1];
+            }
+        };
+        ptx::named_barrier_sync(1, 128);   // the slots are free
+        if (warp >= 2) put(warp - 2);
+        ptx::named_barrier_sync(1, 128);
+        if (warp < 2) add(warp);
+        if (warp == 1) put(1);
+        ptx::named_barrier_sync(1, 128);
+        const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
+        const int b_first = whole ? 0 : block_of(w.item0, total, used);
+        const int parts = whole ? 1 : block_of(w.item0 + w.units - 1, total, used) - b_first + 1;
+        if (warp == 0) {
+            add(1);
+            if (whole && ok) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = nt * 8 + 2 * c + i;
+                        if (r >= rows) continue;
+                        const int64_t row = (int64_t)w.rt * R + r;
+                        const int64_t t = w.s.q0 + row / p.group;
+                        const int head = w.head * p.group + (int)(row % p.group);
+                        const float inv = l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i];
+                        uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride + (int64_t)head * D + g * (D / 8);
+#pragma unroll
+                        for (int k = 0; k < KS; k += 4)
+                            *reinterpret_cast<uint4*>(out + 2 * k) = make_uint4(
+                                pack2<BF16>(o[k][nt][i] * inv, o[k][nt][2 + i] * inv),
+                                pack2<BF16>(o[k + 1][nt][i] * inv, o[k + 1][nt][2 + i] * inv),
+                                pack2<BF16>(o[k + 2][nt][i] * inv, o[k + 2][nt][2 + i] * inv),
+                                pack2<BF16>(o[k + 3][nt][i] * inv, o[k + 3][nt][2 + i] * inv));
+                        if (p.lse != nullptr && g == 0)
+                            p.lse[t * p.Hq + head] =
+                                l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + log2f(l[nt][i])) * 0.6931471805599453f;
+                    }
+            } else if (ok) {
+                float* slot = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = nt * 8 + 2 * c + i;
+                        if (r >= rows) continue;
+#pragma unroll
+                        for (int k = 0; k < KS; k += 2)
+                            __stcg(reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 2 * k),
+                                   make_float4(o[k][nt][i], o[k][nt][2 + i], o[k + 1][nt][i], o[k + 1][nt][2 + i]));
+                        if (g == 0)
+                            __stcg(reinterpret_cast<float2*>(slot + R * D) + r, make_float2(m[nt][i], l[nt][i]));
+                    }
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t before = atomicAdd(p.ws_count + b_first, 1u);
+                    const int last = before + 1 == (uint32_t)parts;
+                    if (last) p.ws_count[b_first] = 0u;
+                    __threadfence();
+                    *last_flag = last;
+                }
+            } else if (lane == 0) {
+                *last_flag = 0;
+            }
+        }
+        if (!whole) {
+            ptx::named_barrier_sync(1, 128);
+            if (*last_flag) {
+                __threadfence();
+                merge_parts<BF16, D, R, 128>(p, w, b_first, parts, reinterpret_cast<float*>(smem + C::OFF_W),
+                                             threadIdx.x, 1);
+            }
+        }
+    }
+}
+
+}  // namespace wq

@@ -271,6 +271,9 @@ struct Kv4RowsParams {   // write and read
 cudaError_t launch_kv4_write(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);   // wq_kv4.cu
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);
 
+// Workspace of the attention kernels: arrival counters first (wq_attn_sched.cuh).
+constexpr int kAttnCounterBytes = 16384;
+
 struct AttnParams {
     Kv4View c;
     const void* q;
@@ -290,7 +293,9 @@ struct AttnParams {
     uint32_t* status;
     long long timeout_ns;
 };
-cudaError_t launch_attn_kv4_simple(const AttnParams& p, bool bf16, int sms, cudaStream_t st);   // wq_attn_simple.cu
+// Few rows for each key head (wq_attn_decode.cu); `rows`: query tokens times heads of a group, an upper bound.
+cudaError_t launch_attn_kv4_decode(const AttnParams& p, bool bf16, int64_t rows, int sms, cudaStream_t st);
+size_t attn_kv4_decode_ws(const Kv4View& c, bool bf16, int64_t rows, int sms);
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
