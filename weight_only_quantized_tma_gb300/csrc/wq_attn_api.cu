@@ -48,6 +48,13 @@ bool stride_ok(int64_t stride, int64_t row, int64_t step) {
     return stride >= row && stride <= kMaxStride && stride % step == 0;
 }
 
+// The few-row kernel's tiles hold 8 to 32 rows, the many-row kernel's 128.
+bool many_rows(int64_t rows) { return rows > 32; }
+
+size_t attn_ws(const Kv4View& c, bool bf16, int64_t rows, int sms) {
+    return many_rows(rows) ? attn_kv4_prompt_ws(c, sms) : attn_kv4_decode_ws(c, bf16, rows, sms);
+}
+
 wq_status rows_call(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots, int64_t T,
                     const wq_kv4_layout* layout, uint8_t* pages, wq_stream_t stream, bool write) {
     Kv4RowsParams p{};
@@ -152,7 +159,7 @@ wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_hea
     if (q_heads < 1 || q_heads > 65535 || q_heads % v.heads != 0 || max_q < 1) return WQ_ERR_SHAPE;
     DeviceState d{};
     if ((st = (wq_status)current_device_state(&d)) != WQ_OK) return st;
-    *bytes = attn_kv4_decode_ws(v, layout->dtype == WQ_BF16, max_q * (q_heads / v.heads), d.sms);
+    *bytes = attn_ws(v, layout->dtype == WQ_BF16, std::min(max_q, kMaxTokens) * (q_heads / v.heads), d.sms);
     return WQ_OK;
 }
 
@@ -197,11 +204,11 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
     p.status = d.status;
     p.timeout_ns = d.timeout_ns;
     const bool bf16 = layout->dtype == WQ_BF16;
-    const int64_t rows = std::min<int64_t>(max_q, T) * p.group;
-    const size_t need = attn_kv4_decode_ws(p.c, bf16, rows, d.sms);
-    if (!ws || ws_bytes < need) return WQ_ERR_WORKSPACE;
+    const int64_t rows = std::min(max_q, kMaxTokens) * p.group;
+    if (!ws || ws_bytes < attn_ws(p.c, bf16, rows, d.sms)) return WQ_ERR_WORKSPACE;
     p.ws_count = static_cast<uint32_t*>(ws);
     p.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounterBytes);
+    if (many_rows(rows)) return finish_launch(launch_attn_kv4_prompt(p, bf16, d.sms, (cudaStream_t)stream));
     return finish_launch(launch_attn_kv4_decode(p, bf16, rows, d.sms, (cudaStream_t)stream));
 }
 

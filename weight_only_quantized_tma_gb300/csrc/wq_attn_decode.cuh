@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
             ptx::named_barrier_sync(1, 128);
             if (*last_flag) {
                 __threadfence();
-                merge_parts<BF16, D, R, 128>(p, w, b_first, parts, reinterpret_cast<float*>(smem + C::OFF_W),
+                merge_parts<BF16, D, R, R, 128>(p, w, b_first, parts, reinterpret_cast<float*>(smem + C::OFF_W),
                                              threadIdx.x, 1);
             }
         }

@@ -1,0 +1,480 @@
+// wq_attn_prompt.cuh -- attention of many query rows (prompts and long drafts) over the
+// 4-bit cache on the tcgen05 tensor cores.
+//
+//   S = Q K^T,  P = exp2(scale' S - m),  O += P V,  out = O / sum P
+//
+// An item is 256 rows (query tokens x heads of a group, so a key head's codes are unpacked
+// once for all of them) as two 128-row tiles; cached tokens come in tiles of 128.  Bound by
+// the tensor cores: 4 products of 128 x 128 x D for each tile of tokens, so one row tile's
+// products run while the other's softmax does:
+//   warps 0-3 / 4-7   softmax of row tile 0 / 1, a thread for each row: S from tensor memory
+//                     (twice: maximum, then exponentials), P back over S, O rescaled only
+//                     when a row's maximum grows by more than 2^8; at the end O -> out;
+//   warps 8-11        unpack: a thread for each token, codes -> RN(lo + q s) into a
+//                     three-slot ring of swizzled shared-memory tiles, K and V in turn;
+//   warp 12           issues the MMAs: S0 S1 | PV0 S0' PV1 S1' | ...;
+//   warp 13           copies page blocks into a two-stage ring with bulk copies.
+// Both operand tiles have the same image [D / 64][128 tokens][128 B]: K is read K-major, V
+// MN-major, so V is never transposed.  Eight codes of a word land in the order 0 4 1 5 2 6
+// 3 7 that the unpack gives; Q is stored in the same order and O is read back through it.
+#pragma once
+
+#include "wq_attn_sched.cuh"
+#include "wq_common.cuh"
+
+namespace wq {
+
+constexpr int kPromptTN = 128;
+constexpr int kPromptRows = 256;
+constexpr int kPromptThreads = 448;
+
+template <int D>
+struct PromptCfg {
+    static constexpr int TILE = 128 * D * 2;               // a 16-bit operand tile: 128 rows of D
+    static constexpr int HALF = 128 * 128;                 // its part of 64 columns
+    static constexpr int KV_SLOTS = 3;
+    static constexpr int RAW_STAGES = 2;
+    static constexpr int OFF_Q = 0;                        // two row tiles
+    static constexpr int OFF_KV = OFF_Q + 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + KV_SLOTS * TILE;
+    static constexpr int NBARS = 2 * RAW_STAGES + 2 * KV_SLOTS + 11;
+    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
+    static constexpr int OFF_RAW = (OFF_MISC + 16 + 127) / 128 * 128;
+    static constexpr int MERGE_ROWS = 32;                  // merge weights live in the Q tiles
+    // tensor memory columns
+    static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i, O_i at 256 + 128 i; P_i over S_i
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const AttnParams p, const int stage_bytes) {
+    using C = PromptCfg<D>;
+    constexpr int R = kPromptRows, TN = kPromptTN, KS = D / 16, RS = C::RAW_STAGES, NS = C::KV_SLOTS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t bar0 = sbase + C::OFF_BAR;
+    auto raw_full = [&](int i) { return bar0 + 8u * i; };
+    auto raw_empty = [&](int i) { return bar0 + 8u * (RS + i); };
+    auto kv_full = [&](int i) { return bar0 + 8u * (2 * RS + i); };
+    auto kv_empty = [&](int i) { return bar0 + 8u * (2 * RS + NS + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * RS + 2 * NS);
+    auto q_full = [&](int i) { return bar1 + 8u * i; };
+    auto s_full = [&](int i) { return bar1 + 8u * (2 + i); };
+    auto p_full = [&](int i) { return bar1 + 8u * (4 + i); };
+    auto o_full = [&](int i) { return bar1 + 8u * (6 + i); };
+    auto o_empty = [&](int i) { return bar1 + 8u * (8 + i); };
+    const uint32_t final_bar = bar1 + 80u;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RS; ++i) ptx::mbar_init(raw_full(i), 1), ptx::mbar_init(raw_empty(i), 4);
+        for (int i = 0; i < NS; ++i) ptx::mbar_init(kv_full(i), 4), ptx::mbar_init(kv_empty(i), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(q_full(i), 4);
+            ptx::mbar_init(s_full(i), 1);
+            ptx::mbar_init(p_full(i), 4);
+            ptx::mbar_init(o_full(i), 1);
+            ptx::mbar_init(o_empty(i), 4);
+        }
+        ptx::mbar_init(final_bar, 1);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 12) {
+        ptx::tmem_alloc<1>(sbase + C::OFF_MISC, 512);
+        ptx::tmem_relinquish<1>();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    Walk w;
+    int used;
+    const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
+    const int pair_row = 4 * (D >> p.c.g_shift);
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
+        if (ok) ok = bounded_wait(bar, parity, abort_flag, p.status, code, p.timeout_ns);
+        return ok;
+    };
+    auto item_rows = [&]() { return (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R); };
+    auto tile_begin = [&]() { return w.v.t0 + (int)(w.u - w.item0); };
+    auto tile_end = [&]() { return w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0); };
+
+    if (warp == 13) {
+        // ------------------------------------------------------------ producer
+        const uint64_t pol = ptx::policy_evict_last();
+        int s = 0;
+        uint32_t ph = 0, issued = 0;
+        for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
+            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > (p.table_stride << p.c.p_shift))
+                atomicOr(p.status, DEVICE_INDEX);
+            const int te = tile_end();
+            for (int t = tile_begin(); t < te; ++t) {
+                const int tok = t * TN;
+                // the tile's pages that hold a token to be seen: [skip, pages)
+                const int pages = min((w.v.hi - tok + p.c.P - 1) >> p.c.p_shift, TN >> p.c.p_shift);
+                const int skip = max(w.v.lo - tok, 0) >> p.c.p_shift;
+                const bool mine = lane >= skip && lane < pages;
+                const int64_t page = mine ? safe_page(p, w.b, (tok >> p.c.p_shift) + lane) : 0;
+                ok = __all_sync(0xffffffffu, wait(raw_empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER));
+                if (!ok) break;
+                if (lane == 0) {
+                    if (pages > skip)
+                        ptx::mbar_arrive_expect_tx(raw_full(s), (uint32_t)((pages - skip) * p.c.block_bytes));
+                    else
+                        ptx::mbar_arrive(raw_full(s));
+                }
+                __syncwarp();
+                if (mine)
+                    ptx::bulk_load(sbase + C::OFF_RAW + s * stage_bytes + lane * p.c.block_bytes,
+                                   p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes,
+                                   p.c.block_bytes, raw_full(s), pol);
+                issued |= 1u << s;
+                if (++s == RS) s = 0, ph ^= 1u;
+            }
+        }
+        if (!ok)   // given up: copies in flight land before the block may end
+            for (int i = 0; i < RS; ++i)
+                if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
+    } else if (warp == 12) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 128);
+            const uint32_t id_o = ptx::make_idesc_f16(BF16, 128, D) | ptx::kIdescBTransposed;
+            int slot = 0;
+            uint32_t slot_ph = 0;
+            uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, o_ph[2] = {1, 1};   // of each row tile's own barriers
+            auto next_slot = [&]() {
+                if (++slot == NS) slot = 0, slot_ph ^= 1u;
+            };
+            auto qk = [&](int i, int k_slot) {
+                const uint32_t a = sbase + C::OFF_Q + i * C::TILE, b = sbase + C::OFF_KV + k_slot * C::TILE;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint32_t off = (k >> 2) * C::HALF + (k & 3) * 32;
+                    ptx::mma_f16_ss(tmem + C::S_COL + 128 * i, ptx::make_sdesc_sw128(a + off),
+                                    ptx::make_sdesc_sw128(b + off), id_s, k > 0);
+                }
+                ptx::mma_commit(s_full(i));
+            };
+            auto pv = [&](int i, int v_slot, bool first) {
+                const uint32_t b = sbase + C::OFF_KV + v_slot * C::TILE;
+#pragma unroll
+                for (int k = 0; k < TN / 16; ++k)
+                    ptx::mma_f16_ts(tmem + C::O_COL + 128 * i, tmem + C::S_COL + 128 * i + 8 * k,
+                                    ptx::make_sdesc_sw128_mn(b + k * 2048, C::HALF), id_o, !(first && k == 0));
+            };
+            for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
+                const int tb = tile_begin(), te = tile_end();
+                const int nq = item_rows() > 128 ? 2 : 1;   // row tiles in use
+                for (int i = 0; i < nq; ++i) {
+                    wait(q_full(i), q_ph[i], DEVICE_TIMEOUT_MMA);
+                    q_ph[i] ^= 1u;
+                }
+                if (!wait(kv_full(slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
+                ptx::tc_fence_after();
+                for (int i = 0; i < nq; ++i) qk(i, slot);
+                ptx::mma_commit(kv_empty(slot));
+                next_slot();
+                for (int t = tb; t < te && ok; ++t) {
+                    const int v_slot = slot;
+                    if (!wait(kv_full(slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
+                    next_slot();
+                    const int k_slot = slot;
+                    const bool more = t + 1 < te;
+                    for (int i = 0; i < nq && ok; ++i) {
+                        if (t == tb) {
+                            wait(o_empty(i), o_ph[i], DEVICE_TIMEOUT_MMA);
+                            o_ph[i] ^= 1u;
+                        }
+                        if (!wait(p_full(i), p_ph[i], DEVICE_TIMEOUT_MMA)) break;
+                        p_ph[i] ^= 1u;
+                        ptx::tc_fence_after();
+                        pv(i, v_slot, t == tb);
+                        if (i == nq - 1) ptx::mma_commit(kv_empty(v_slot));
+                        if (more) {
+                            if (i == 0 && !wait(kv_full(k_slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
+                            if (i == 0) ptx::tc_fence_after();
+                            qk(i, k_slot);
+                            if (i == nq - 1) ptx::mma_commit(kv_empty(k_slot));
+                        } else {
+                            ptx::mma_commit(o_full(i));
+                        }
+                    }
+                    if (more) next_slot();
+                }
+            }
+            if (!ok) {
+                // given up: the MMAs in flight end before tensor memory is freed
+                ptx::mma_commit(final_bar);
+                drain_wait(final_bar, 0u, p.timeout_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ unpack
+        const int tt = threadIdx.x - 256;          // the token of the tile
+        const int pg = tt >> p.c.p_shift, place = tt & (p.c.P - 1);
+        int s = 0, slot = 0;
+        uint32_t ph = 0, slot_ph = 0;
+        for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
+            const int rows = item_rows(), te = tile_end();
+            const int pos0 = w.s.L - w.s.n + (int)((int64_t)w.rt * R / p.group);
+            const int pos1 = w.s.L - w.s.n + (int)(((int64_t)w.rt * R + rows - 1) / p.group);
+            const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
+            const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
+            for (int t = tile_begin(); t < te; ++t) {
+                const int tok = t * TN;
+                const bool masked = tok < all_lo || tok + TN > all_hi;
+                ok = __all_sync(0xffffffffu, wait(raw_full(s), ph, DEVICE_TIMEOUT_TRANSFORM));
+                const uint8_t* block = smem + C::OFF_RAW + s * stage_bytes + pg * p.c.block_bytes;
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    ok = __all_sync(0xffffffffu, wait(kv_empty(slot), slot_ph ^ 1u, DEVICE_TIMEOUT_TRANSFORM));
+                    if (ok) {
+                        const uint8_t* codes = block + kv4_codes_at(p.c, which, place);
+                        const uint8_t* pairs = block + kv4_pairs_at(p.c, which, place);
+                        uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + tt * 128;
+                        bool clear = false, spoil = false;
+                        if (masked) {
+                            // 0 * NaN must not reach rows that do not see a token: values
+                            // nobody sees are cleared, and a NaN among a seen token's
+                            // values moves to its key, where each row's mask applies
+                            const uint8_t* vp = block + kv4_pairs_at(p.c, 1, place);
+                            uint32_t z = 0;
+                            for (int j = 0; j < pair_row; j += 4)
+                                z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(vp + j), 0u, z);
+                            spoil = (z & 0x7FFF7FFFu) != 0;
+                            clear = which == 1 && (spoil || tok + tt < w.v.lo || tok + tt >= w.v.hi);
+                        }
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            // 32 codes; the rotation spreads a quarter warp over the banks
+                            const int ch = (i + (lane >> (D == 128 ? 1 : 2))) & (D / 32 - 1);
+                            const uint4 cw = *reinterpret_cast<const uint4*>(codes + ch * 16);
+                            uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + ((ch * 32) >> p.c.g_shift) * 4);
+                            if (clear) pair = 0u;
+                            if (which == 0 && spoil) pair = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                            const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
+                            const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t x = words[j], y = x >> 8;
+                                const int chunk = ch * 4 + j;
+                                *reinterpret_cast<uint4*>(dst + (chunk >> 3) * C::HALF +
+                                                          (((chunk & 7) ^ (tt & 7)) << 4)) =
+                                    make_uint4(fma2<BF16>(Codes<BF16>::low(x), s2, l2), fma2<BF16>(Codes<BF16>::high(x), s2, l2),
+                                               fma2<BF16>(Codes<BF16>::low(y), s2, l2), fma2<BF16>(Codes<BF16>::high(y), s2, l2));
+                            }
+                        }
+                        ptx::fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (ok && lane == 0) {
+                        ptx::mbar_arrive(kv_full(slot));
+                        if (which == 1) ptx::mbar_arrive(raw_empty(s));
+                    }
+                    if (++slot == NS) slot = 0, slot_ph ^= 1u;
+                }
+                if (++s == RS) s = 0, ph ^= 1u;
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int i = warp >> 2;                     // row tile
+        const int r = threadIdx.x;                   // row of the item
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i, o_tm = tmem + lanes + C::O_COL + 128 * i;
+        // a zero scale becomes a tiny one, so that a masked -inf stays -inf; a negative
+        // one moves its sign to Q
+        const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+        uint32_t s_ph = 0, o_ph = 0;
+        for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
+            const int rows = item_rows();
+            const bool idle = 128 * i >= rows;       // no rows in this tile
+            const int64_t row = (int64_t)w.rt * R + min(r, rows - 1);
+            const int qt = (int)(row / p.group);
+            const int64_t tq = w.s.q0 + qt;
+            const int head = w.head * p.group + (int)(row % p.group);
+            const int pos = w.s.L - w.s.n + qt;
+            const int hi = p.causal ? min(w.s.L, pos + 1) : w.s.L;
+            const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+            if (!idle) {
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + tq * p.q_stride + (int64_t)head * D;
+                uint8_t* dst = smem + C::OFF_Q + i * C::TILE + (r & 127) * 128;
+#pragma unroll 4
+                for (int ch = 0; ch < D / 8; ++ch) {
+                    uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
+                    if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
+                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::HALF + (((ch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                   __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(q_full(i));
+            }
+            const int tb = tile_begin(), te = tile_end();
+            float m = -INFINITY, l = 0.f;
+            if (!idle) {
+                for (int t = tb; t < te; ++t) {
+                    ok = __all_sync(0xffffffffu, wait(s_full(i), s_ph, DEVICE_TIMEOUT_EPILOGUE));
+                    s_ph ^= 1u;
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const int h = hi - t * TN, b = lo - t * TN;      // this row sees columns [b, h)
+                    const bool masked = __any_sync(0xffffffffu, b > 0 || h < TN);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        ptx::tmem_ld32(s_tm + 32 * c, v);
+                        ptx::tmem_wait_ld();
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * c + k < b || 32 * c + k >= h) v[k] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    }
+                    mx *= sl2;
+                    const bool grow = mx > m + 8.f;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float m1 = grow ? mx : m, f = grow ? part_weight(m, m1) : 1.f;
+                        m = m1;
+                        l *= f;
+                        if (t > tb) {
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t v[16];
+                                ptx::tmem_ld16(o_tm + 16 * c, v);
+                                ptx::tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                                ptx::tmem_st16(o_tm + 16 * c, v);
+                            }
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32], o[16];
+                        ptx::tmem_ld32(s_tm + 32 * c, v);
+                        ptx::tmem_wait_ld();
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * c + k < b || 32 * c + k >= h) v[k] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), sl2, -mm));
+                            const float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl2, -mm));
+                            l0 += e0, l1 += e1;
+                            o[k] = pack2<BF16>(e0, e1);
+                        }
+                        ptx::tmem_st16(s_tm + 16 * c, o);
+                    }
+                    l += l0 + l1;
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(p_full(i));
+                }
+                if (ok) ok = __all_sync(0xffffffffu, wait(o_full(i), o_ph, DEVICE_TIMEOUT_EPILOGUE));
+                ptx::tc_fence_after();
+                o_ph ^= 1u;
+            }
+            // ---- the item's result, or this block's part of it
+            const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
+            const int b_first = whole ? 0 : block_of(w.item0, total, used);
+            const int parts = whole ? 1 : block_of(w.item0 + w.units - 1, total, used) - b_first + 1;
+            float* part = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
+            if (!idle && ok) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D;
+#pragma unroll 2
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t v[16];
+                    ptx::tmem_ld16(o_tm + 16 * c, v);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        // columns hold d = 0 4 1 5 2 6 3 7 of each eight
+                        float d[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) d[(k >> 1) + 4 * (k & 1)] = __uint_as_float(v[8 * j + k]);
+                        if (r < rows) {
+                            if (whole) {
+                                *reinterpret_cast<uint4*>(out + 16 * c + 8 * j) =
+                                    make_uint4(pack2<BF16>(d[0] * inv, d[1] * inv), pack2<BF16>(d[2] * inv, d[3] * inv),
+                                               pack2<BF16>(d[4] * inv, d[5] * inv), pack2<BF16>(d[6] * inv, d[7] * inv));
+                            } else {
+                                float4* dst = reinterpret_cast<float4*>(part + (size_t)r * D + 16 * c + 8 * j);
+                                __stcg(dst, make_float4(d[0], d[1], d[2], d[3]));
+                                __stcg(dst + 1, make_float4(d[4], d[5], d[6], d[7]));
+                            }
+                        }
+                    }
+                }
+                if (r < rows) {
+                    if (!whole)
+                        __stcg(reinterpret_cast<float2*>(part + R * D) + r, make_float2(m, l));
+                    else if (p.lse != nullptr)
+                        p.lse[tq * p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                }
+            }
+            if (!idle) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(o_empty(i));
+            }
+            if (!whole) {
+                __threadfence();
+                ptx::named_barrier_sync(1, 256);
+                if (threadIdx.x == 0) {
+                    int last = 0;
+                    if (ok) {
+                        const uint32_t before = atomicAdd(p.ws_count + b_first, 1u);
+                        last = before + 1 == (uint32_t)parts;
+                        if (last) p.ws_count[b_first] = 0u;
+                        __threadfence();
+                    }
+                    *last_flag = last;
+                }
+                ptx::named_barrier_sync(1, 256);
+                if (*last_flag) {
+                    __threadfence();
+                    merge_parts<BF16, D, R, C::MERGE_ROWS, 256>(p, w, b_first, parts,
+                                                                reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 1);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc<1>(tmem, 512);
+    }
+}
+
+}  // namespace wq

@@ -173,89 +173,96 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float part_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2(m - M); }
 
 // Adds the partial results of an item, in the order of its tiles, and writes out and lse.
-// Executed by NTHR threads (warps 0 .. NTHR / 32 - 1) of the last block to arrive.
-// weights: shared, R * 33 floats.
-template <bool BF16, int D, int R, int NTHR>
+// Executed by NTHR threads (warps 0 .. NTHR / 32 - 1) of the last block to arrive, RB rows
+// of the item's R at a time.  weights: shared, RB * 33 floats.
+template <bool BF16, int D, int R, int RB, int NTHR>
 __device__ __forceinline__ void merge_parts(const AttnParams& p, const Walk& w, int first_block, int parts,
                                             float* weights, int tid, uint32_t barrier) {
     constexpr int CH = D / 4;                       // float4 chunks of a row
-    constexpr int PER = (R * CH + NTHR - 1) / NTHR;
-    const int rows = (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R);
+    constexpr int PER = (RB * CH + NTHR - 1) / NTHR;
+    constexpr int NW = NTHR / 32, RW = (RB + NW - 1) / NW;
+    const int all = (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R);
     const int warp = tid >> 5, lane = tid & 31;
-    float4 acc[PER];
-    float lsum[(R + NTHR / 32 - 1) / (NTHR / 32)], mrun[(R + NTHR / 32 - 1) / (NTHR / 32)];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (auto& x : lsum) x = 0.f;
-#pragma unroll
-    for (auto& x : mrun) x = -INFINITY;
-    auto slot = [&](int j) {   // the first part is what its block left unfinished, the others what theirs continued
+    // the first part is what its block left unfinished, the others what theirs continued
+    auto slot = [&](int j) {
         return p.ws_part + (size_t)(2 * (first_block + j) + (j == 0 ? 1 : 0)) * attn_slot_floats(R, D);
     };
-    for (int j0 = 0; j0 < parts; j0 += 32) {
-        const int cnt = min(32, parts - j0);
-        int k = 0;
+    for (int r0 = 0; r0 < all; r0 += RB) {
+        const int rows = min(RB, all - r0);
+        float4 acc[PER];
+        float lsum[RW], mrun[RW];
 #pragma unroll
-        for (int r = warp; r < R; r += NTHR / 32, ++k) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (lane < cnt && r < rows) ml = __ldcg(reinterpret_cast<const float2*>(slot(j0 + lane) + R * D) + r);
-            float M = fmaxf(ml.x, mrun[k]);
+        for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            const float f = part_weight(mrun[k], M), wt = part_weight(ml.x, M);
-            float l = wt * ml.y;
+        for (int k = 0; k < RW; ++k) lsum[k] = 0.f, mrun[k] = -INFINITY;
+        for (int j0 = 0; j0 < parts; j0 += 32) {
+            const int cnt = min(32, parts - j0);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-            lsum[k] = lsum[k] * f + l;
-            mrun[k] = M;
-            weights[r * 33 + lane] = wt;
-            if (lane == 0) weights[r * 33 + 32] = f;
+            for (int k = 0; k < RW; ++k) {
+                const int r = warp + k * NW;
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (lane < cnt && r < rows)
+                    ml = __ldcg(reinterpret_cast<const float2*>(slot(j0 + lane) + R * D) + r0 + r);
+                float M = fmaxf(ml.x, mrun[k]);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                const float f = part_weight(mrun[k], M), wt = part_weight(ml.x, M);
+                float l = wt * ml.y;
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                lsum[k] = lsum[k] * f + l;
+                mrun[k] = M;
+                if (r < RB) {
+                    weights[r * 33 + lane] = wt;
+                    if (lane == 0) weights[r * 33 + 32] = f;
+                }
+            }
+            ptx::named_barrier_sync(barrier, NTHR);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int idx = tid + i * NTHR, r = idx / CH, ch = idx % CH;
+                if (r >= rows) continue;
+                const float f = weights[r * 33 + 32];
+                acc[i].x *= f, acc[i].y *= f, acc[i].z *= f, acc[i].w *= f;
+#pragma unroll 8
+                for (int j = 0; j < cnt; ++j) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(j0 + j)) + (r0 + r) * CH + ch);
+                    const float wt = weights[r * 33 + j];
+                    if (wt != 0.f) {   // a part that saw nothing holds nothing
+                        acc[i].x += wt * v.x, acc[i].y += wt * v.y, acc[i].z += wt * v.z, acc[i].w += wt * v.w;
+                    }
+                }
+            }
+            ptx::named_barrier_sync(barrier, NTHR);
+        }
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+            const int r = warp + k * NW;
+            if (lane == 0 && r < rows) {
+                weights[r * 33] = lsum[k];
+                if (p.lse != nullptr) {
+                    const int64_t row = (int64_t)w.rt * R + r0 + r;
+                    const int64_t t = w.s.q0 + row / p.group;
+                    p.lse[t * p.Hq + w.head * p.group + (int)(row % p.group)] =
+                        lsum[k] == 0.f ? -INFINITY : (mrun[k] + log2f(lsum[k])) * 0.6931471805599453f;
+                }
+            }
         }
         ptx::named_barrier_sync(barrier, NTHR);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int idx = tid + i * NTHR, r = idx / CH, ch = idx % CH;
             if (r >= rows) continue;
-            const float f = weights[r * 33 + 32];
-            acc[i].x *= f, acc[i].y *= f, acc[i].z *= f, acc[i].w *= f;
-#pragma unroll 8
-            for (int j = 0; j < cnt; ++j) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(j0 + j)) + r * CH + ch);
-                const float wt = weights[r * 33 + j];
-                if (wt != 0.f) {   // a part that saw nothing holds nothing
-                    acc[i].x += wt * v.x, acc[i].y += wt * v.y, acc[i].z += wt * v.z, acc[i].w += wt * v.w;
-                }
-            }
+            const float l = weights[r * 33], inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t row = (int64_t)w.rt * R + r0 + r;
+            const int64_t t = w.s.q0 + row / p.group;
+            uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride +
+                            (int64_t)(w.head * p.group + (int)(row % p.group)) * D + ch * 4;
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(acc[i].x * inv, acc[i].y * inv),
+                                                        pack2<BF16>(acc[i].z * inv, acc[i].w * inv));
         }
-        ptx::named_barrier_sync(barrier, NTHR);
+        ptx::named_barrier_sync(barrier, NTHR);   // the weights may be written again
     }
-    int k = 0;
-#pragma unroll
-    for (int r = warp; r < R; r += NTHR / 32, ++k)
-        if (lane == 0 && r < rows) {
-            weights[r * 33] = lsum[k];
-            if (p.lse != nullptr) {
-                const int64_t row = (int64_t)w.rt * R + r;
-                const int64_t t = w.s.q0 + row / p.group;
-                p.lse[t * p.Hq + w.head * p.group + (int)(row % p.group)] =
-                    lsum[k] == 0.f ? -INFINITY : (mrun[k] + log2f(lsum[k])) * 0.6931471805599453f;
-            }
-        }
-    ptx::named_barrier_sync(barrier, NTHR);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int idx = tid + i * NTHR, r = idx / CH, ch = idx % CH;
-        if (r >= rows) continue;
-        const float l = weights[r * 33], inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t row = (int64_t)w.rt * R + r;
-        const int64_t t = w.s.q0 + row / p.group;
-        uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride +
-                        (int64_t)(w.head * p.group + (int)(row % p.group)) * D + ch * 4;
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(acc[i].x * inv, acc[i].y * inv),
-                                                    pack2<BF16>(acc[i].z * inv, acc[i].w * inv));
-    }
-    ptx::named_barrier_sync(barrier, NTHR);   // the weights may be written again
 }
 
 }  // namespace wq

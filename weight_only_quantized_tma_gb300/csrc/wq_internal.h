@@ -296,6 +296,9 @@ struct AttnParams {
 // Few rows for each key head (wq_attn_decode.cu); `rows`: query tokens times heads of a group, an upper bound.
 cudaError_t launch_attn_kv4_decode(const AttnParams& p, bool bf16, int64_t rows, int sms, cudaStream_t st);
 size_t attn_kv4_decode_ws(const Kv4View& c, bool bf16, int64_t rows, int sms);
+// Many rows (wq_attn_prompt.cu).
+cudaError_t launch_attn_kv4_prompt(const AttnParams& p, bool bf16, int sms, cudaStream_t st);
+size_t attn_kv4_prompt_ws(const Kv4View& c, int sms);
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
