@@ -7,13 +7,16 @@
 // once for all of them) as two 128-row tiles; cached tokens come in tiles of 128.  Bound by
 // the tensor cores: 4 products of 128 x 128 x D for each tile of tokens, so one row tile's
 // products run while the other's softmax does:
-//   warps 0-3 / 4-7   softmax of row tile 0 / 1, a thread for each row: S from tensor memory
-//                     (twice: maximum, then exponentials), P back over S, O rescaled only
-//                     when a row's maximum grows by more than 2^8; at the end O -> out;
-//   warps 8-11        unpack: a thread for each token, codes -> RN(lo + q s) into a
-//                     three-slot ring of swizzled shared-memory tiles, K and V in turn;
-//   warp 12           issues the MMAs: S0 S1 | PV0 S0' PV1 S1' | ...;
-//   warp 13           copies page blocks into a two-stage ring with bulk copies.
+//   warps 0-7 / 8-15  softmax of row tile 0 / 1: two threads for each row, 64 columns each.
+//                     S from tensor memory, the row's maximum through shared memory, P back
+//                     over S; O is rescaled only when a row's maximum grows by more than
+//                     2^8; at the end O -> out;
+//   warps 16-19, 20-23  unpack keys / values: a thread for each token, codes -> RN(lo + q s)
+//                     into a three-slot ring of swizzled shared-memory tiles, K and V in turn;
+//   warps 24, 25      issue the MMAs of row tile 0 / 1 (PV, then the next S): the queue before
+//                     the tensor core is short, so while one warp waits the other's products run;
+//   warp 26           copies page blocks into a two-stage ring with bulk copies (warp 27 only
+//                     fills the warpgroup, which hands its registers on).
 // Both operand tiles have the same image [D / 64][128 tokens][128 B]: K is read K-major, V
 // MN-major, so V is never transposed.  Eight codes of a word land in the order 0 4 1 5 2 6
 // 3 7 that the unpack gives; Q is stored in the same order and O is read back through it.
@@ -26,7 +29,11 @@ namespace wq {
 
 constexpr int kPromptTN = 128;
 constexpr int kPromptRows = 256;
-constexpr int kPromptThreads = 448;
+constexpr int kPromptThreads = 896;
+// Registers of a thread by role; a block is launched with 72 for each, and the seven
+// warpgroups' shares add up to no more than the same 504.
+constexpr int kRegsSoftmax = 80, kRegsUnpack = 64, kRegsIssue = 40;
+static_assert(4 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 7 * 72, "register split");
 
 template <int D>
 struct PromptCfg {
@@ -39,12 +46,34 @@ struct PromptCfg {
     static constexpr int OFF_BAR = OFF_KV + KV_SLOTS * TILE;
     static constexpr int NBARS = 2 * RAW_STAGES + 2 * KV_SLOTS + 11;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
-    static constexpr int OFF_RAW = (OFF_MISC + 16 + 127) / 128 * 128;
+    static constexpr int OFF_EX = (OFF_MISC + 16 + 15) / 16 * 16;     // a row's two halves: maximum, sum
+    static constexpr int OFF_RAW = (OFF_EX + 2 * 2 * 128 * 4 + 127) / 128 * 128;
     static constexpr int MERGE_ROWS = 32;                  // merge weights live in the Q tiles
     // tensor memory columns
     static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i, O_i at 256 + 128 i; P_i over S_i
 };
 
+// Two fp32 values in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 un2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -76,32 +105,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < RS; ++i) ptx::mbar_init(raw_full(i), 1), ptx::mbar_init(raw_empty(i), 4);
-        for (int i = 0; i < NS; ++i) ptx::mbar_init(kv_full(i), 4), ptx::mbar_init(kv_empty(i), 1);
+        for (int i = 0; i < RS; ++i) ptx::mbar_init(raw_full(i), 1), ptx::mbar_init(raw_empty(i), 8);
+        for (int i = 0; i < NS; ++i) ptx::mbar_init(kv_full(i), 4), ptx::mbar_init(kv_empty(i), 2);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(q_full(i), 4);
+            ptx::mbar_init(q_full(i), 8);
             ptx::mbar_init(s_full(i), 1);
-            ptx::mbar_init(p_full(i), 4);
+            ptx::mbar_init(p_full(i), 8);
             ptx::mbar_init(o_full(i), 1);
-            ptx::mbar_init(o_empty(i), 4);
+            ptx::mbar_init(o_empty(i), 8);
         }
-        ptx::mbar_init(final_bar, 1);
+        ptx::mbar_init(final_bar, 2);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
-    if (warp == 12) {
+    if (warp == 24) {
         ptx::tmem_alloc<1>(sbase + C::OFF_MISC, 512);
         ptx::tmem_relinquish<1>();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = 0;   // all 512 columns are allocated: they start at column 0
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
 
-    Walk w;
+    Walk w{};
     int used;
     const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
     const int pair_row = 4 * (D >> p.c.g_shift);
@@ -114,7 +143,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     auto tile_begin = [&]() { return w.v.t0 + (int)(w.u - w.item0); };
     auto tile_end = [&]() { return w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0); };
 
-    if (warp == 13) {
+    if (warp >= 24) {
+    ptx::regs_dec<kRegsIssue>();
+    if (warp == 26) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = ptx::policy_evict_last();
         int s = 0;
@@ -150,86 +181,101 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         if (!ok)   // given up: copies in flight land before the block may end
             for (int i = 0; i < RS; ++i)
                 if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
-    } else if (warp == 12) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp < 26) {
+        // ------------------------------------------------------------ MMA issuers
+        // One lane for each row tile, and as few instructions between products as can be:
+        // a product of 128 x 128 x 16 takes 64 cycles, so address arithmetic and waits here
+        // leave the tensor core idle.  The products of a tile are unrolled with constant
+        // offsets, and the whole of tensor memory is ours, so its addresses are constants.
+        const int i = warp - 24;
         if (lane == 0) {
-            const uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 128);
-            const uint32_t id_o = ptx::make_idesc_f16(BF16, 128, D) | ptx::kIdescBTransposed;
+            constexpr uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 128);
+            constexpr uint32_t id_o = ptx::make_idesc_f16(BF16, 128, D) | ptx::kIdescBTransposed;
+            const uint32_t q_lo = ptx::sdesc_lo(sbase + C::OFF_Q + i * C::TILE);
+            const uint32_t k_lo = ptx::sdesc_lo(sbase + C::OFF_KV), v_lo = ptx::sdesc_lo_mn(sbase + C::OFF_KV, C::HALF);
+            const uint32_t s_tm = C::S_COL + 128 * i, o_tm = C::O_COL + 128 * i;
+            const uint32_t b_q = q_full(i), b_s = s_full(i), b_p = p_full(i), b_of = o_full(i), b_oe = o_empty(i);
             int slot = 0;
-            uint32_t slot_ph = 0;
-            uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, o_ph[2] = {1, 1};   // of each row tile's own barriers
+            uint32_t slot_ph = 0, q_ph = 0, p_ph = 0, o_ph = 1;
             auto next_slot = [&]() {
                 if (++slot == NS) slot = 0, slot_ph ^= 1u;
             };
-            auto qk = [&](int i, int k_slot) {
-                const uint32_t a = sbase + C::OFF_Q + i * C::TILE, b = sbase + C::OFF_KV + k_slot * C::TILE;
+            auto ready = [&](uint32_t bar, uint32_t parity) {
+                if (!ptx::mbar_try_wait(bar, parity)) wait(bar, parity, DEVICE_TIMEOUT_MMA);
+            };
+            auto qk = [&](int k_slot) {      // S_i = Q_i K^T
+                const uint32_t b = k_lo + k_slot * (C::TILE >> 4);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    const uint32_t off = (k >> 2) * C::HALF + (k & 3) * 32;
-                    ptx::mma_f16_ss(tmem + C::S_COL + 128 * i, ptx::make_sdesc_sw128(a + off),
-                                    ptx::make_sdesc_sw128(b + off), id_s, k > 0);
+                    const uint32_t off = (k >> 2) * (C::HALF >> 4) + (k & 3) * 2;
+                    ptx::mma_f16_ss(s_tm, q_lo + off, ptx::kSdescHi, b + off, ptx::kSdescHi, id_s, k > 0);
                 }
-                ptx::mma_commit(s_full(i));
-            };
-            auto pv = [&](int i, int v_slot, bool first) {
-                const uint32_t b = sbase + C::OFF_KV + v_slot * C::TILE;
-#pragma unroll
-                for (int k = 0; k < TN / 16; ++k)
-                    ptx::mma_f16_ts(tmem + C::O_COL + 128 * i, tmem + C::S_COL + 128 * i + 8 * k,
-                                    ptx::make_sdesc_sw128_mn(b + k * 2048, C::HALF), id_o, !(first && k == 0));
+                ptx::mma_commit(b_s);
+                ptx::mma_commit(kv_empty(k_slot));
             };
             for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
-                const int tb = tile_begin(), te = tile_end();
-                const int nq = item_rows() > 128 ? 2 : 1;   // row tiles in use
-                for (int i = 0; i < nq; ++i) {
-                    wait(q_full(i), q_ph[i], DEVICE_TIMEOUT_MMA);
-                    q_ph[i] ^= 1u;
-                }
-                if (!wait(kv_full(slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
-                ptx::tc_fence_after();
-                for (int i = 0; i < nq; ++i) qk(i, slot);
-                ptx::mma_commit(kv_empty(slot));
-                next_slot();
-                for (int t = tb; t < te && ok; ++t) {
-                    const int v_slot = slot;
-                    if (!wait(kv_full(slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
-                    next_slot();
-                    const int k_slot = slot;
-                    const bool more = t + 1 < te;
-                    for (int i = 0; i < nq && ok; ++i) {
-                        if (t == tb) {
-                            wait(o_empty(i), o_ph[i], DEVICE_TIMEOUT_MMA);
-                            o_ph[i] ^= 1u;
-                        }
-                        if (!wait(p_full(i), p_ph[i], DEVICE_TIMEOUT_MMA)) break;
-                        p_ph[i] ^= 1u;
-                        ptx::tc_fence_after();
-                        pv(i, v_slot, t == tb);
-                        if (i == nq - 1) ptx::mma_commit(kv_empty(v_slot));
-                        if (more) {
-                            if (i == 0 && !wait(kv_full(k_slot), slot_ph, DEVICE_TIMEOUT_MMA)) break;
-                            if (i == 0) ptx::tc_fence_after();
-                            qk(i, k_slot);
-                            if (i == nq - 1) ptx::mma_commit(kv_empty(k_slot));
-                        } else {
-                            ptx::mma_commit(o_full(i));
-                        }
+                const int tiles = tile_end() - tile_begin();
+                if (i == 1 && item_rows() <= 128) {
+                    // no rows in this tile: only hand the slots on
+                    for (int t = 0; t < 2 * tiles && ok; ++t) {
+                        ready(kv_full(slot), slot_ph);
+                        ptx::mbar_arrive(kv_empty(slot));
+                        next_slot();
                     }
-                    if (more) next_slot();
+                    continue;
+                }
+                ready(b_q, q_ph);
+                q_ph ^= 1u;
+                ready(kv_full(slot), slot_ph);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                qk(slot);
+                next_slot();
+                for (int t = 0; t < tiles; ++t) {
+                    const int v_slot = slot;
+                    ready(kv_full(v_slot), slot_ph);
+                    next_slot();
+                    if (t == 0) {
+                        ready(b_oe, o_ph);
+                        o_ph ^= 1u;
+                    }
+                    ready(b_p, p_ph);
+                    p_ph ^= 1u;
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t b = v_lo + v_slot * (C::TILE >> 4);   // O_i (+)= P_i V
+#pragma unroll
+                    for (int k = 0; k < TN / 16; ++k)
+                        ptx::mma_f16_ts(o_tm, s_tm + 64 * (k >> 2) + 8 * (k & 3), b + k * (2048 >> 4), ptx::kSdescHi, id_o, k > 0 || t > 0);
+                    ptx::mma_commit(kv_empty(v_slot));
+                    if (t + 1 < tiles) {
+                        ready(kv_full(slot), slot_ph);
+                        if (!ok) break;
+                        qk(slot);
+                        next_slot();
+                    } else {
+                        ptx::mma_commit(b_of);
+                    }
                 }
             }
-            if (!ok) {
-                // given up: the MMAs in flight end before tensor memory is freed
+            // given up (either warp): the MMAs in flight end before tensor memory is freed
+            if (*abort_flag) {
                 ptx::mma_commit(final_bar);
                 drain_wait(final_bar, 0u, p.timeout_ns);
             }
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    }
+    } else if (warp >= 16) {
+        ptx::regs_dec<kRegsUnpack>();
         // ------------------------------------------------------------ unpack
-        const int tt = threadIdx.x - 256;          // the token of the tile
+        const int which = (warp - 16) >> 2;        // keys, values
+        const int tt = threadIdx.x & 127;          // the token of the tile
         const int pg = tt >> p.c.p_shift, place = tt & (p.c.P - 1);
-        int s = 0, slot = 0;
+        const int codes_at = pg * p.c.block_bytes + kv4_codes_at(p.c, which, place);
+        const int pairs_at = pg * p.c.block_bytes + kv4_pairs_at(p.c, which, place);
+        const int vpairs_at = pg * p.c.block_bytes + kv4_pairs_at(p.c, 1, place);
+        int s = 0, slot = which;
         uint32_t ph = 0, slot_ph = 0;
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows(), te = tile_end();
@@ -239,66 +285,67 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
             for (int t = tile_begin(); t < te; ++t) {
                 const int tok = t * TN;
-                const bool masked = tok < all_lo || tok + TN > all_hi;
                 ok = __all_sync(0xffffffffu, wait(raw_full(s), ph, DEVICE_TIMEOUT_TRANSFORM));
-                const uint8_t* block = smem + C::OFF_RAW + s * stage_bytes + pg * p.c.block_bytes;
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    ok = __all_sync(0xffffffffu, wait(kv_empty(slot), slot_ph ^ 1u, DEVICE_TIMEOUT_TRANSFORM));
-                    if (ok) {
-                        const uint8_t* codes = block + kv4_codes_at(p.c, which, place);
-                        const uint8_t* pairs = block + kv4_pairs_at(p.c, which, place);
-                        uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + tt * 128;
-                        bool clear = false, spoil = false;
-                        if (masked) {
-                            // 0 * NaN must not reach rows that do not see a token: values
-                            // nobody sees are cleared, and a NaN among a seen token's
-                            // values moves to its key, where each row's mask applies
-                            const uint8_t* vp = block + kv4_pairs_at(p.c, 1, place);
-                            uint32_t z = 0;
-                            for (int j = 0; j < pair_row; j += 4)
-                                z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(vp + j), 0u, z);
-                            spoil = (z & 0x7FFF7FFFu) != 0;
-                            clear = which == 1 && (spoil || tok + tt < w.v.lo || tok + tt >= w.v.hi);
-                        }
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            // 32 codes; the rotation spreads a quarter warp over the banks
-                            const int ch = (i + (lane >> (D == 128 ? 1 : 2))) & (D / 32 - 1);
-                            const uint4 cw = *reinterpret_cast<const uint4*>(codes + ch * 16);
-                            uint32_t pair = *reinterpret_cast<const uint32_t*>(pairs + ((ch * 32) >> p.c.g_shift) * 4);
-                            if (clear) pair = 0u;
-                            if (which == 0 && spoil) pair = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
-                            const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
-                            const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t x = words[j], y = x >> 8;
-                                const int chunk = ch * 4 + j;
-                                *reinterpret_cast<uint4*>(dst + (chunk >> 3) * C::HALF +
-                                                          (((chunk & 7) ^ (tt & 7)) << 4)) =
-                                    make_uint4(fma2<BF16>(Codes<BF16>::low(x), s2, l2), fma2<BF16>(Codes<BF16>::high(x), s2, l2),
-                                               fma2<BF16>(Codes<BF16>::low(y), s2, l2), fma2<BF16>(Codes<BF16>::high(y), s2, l2));
-                            }
-                        }
-                        ptx::fence_proxy_async_smem();
+                ok = __all_sync(0xffffffffu, wait(kv_empty(slot), slot_ph ^ 1u, DEVICE_TIMEOUT_TRANSFORM));
+                if (ok) {
+                    const uint8_t* st = smem + C::OFF_RAW + s * stage_bytes;
+                    uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + tt * 128;
+                    bool clear = false, spoil = false;
+                    if (tok < all_lo || tok + TN > all_hi) {
+                        // 0 * NaN must not reach rows that do not see a token: values
+                        // nobody sees are cleared, and a NaN among a seen token's
+                        // values moves to its key, where each row's mask applies
+                        uint32_t z = 0;
+                        for (int j = 0; j < pair_row; j += 4)
+                            z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(st + vpairs_at + j), 0u, z);
+                        spoil = (z & 0x7FFF7FFFu) != 0;
+                        clear = which == 1 && (spoil || tok + tt < w.v.lo || tok + tt >= w.v.hi);
+                        spoil = which == 0 && spoil;
                     }
-                    __syncwarp();
-                    if (ok && lane == 0) {
-                        ptx::mbar_arrive(kv_full(slot));
-                        if (which == 1) ptx::mbar_arrive(raw_empty(s));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        // 32 codes; the rotation spreads a quarter warp over the banks
+                        const int ch = (i + (lane >> (D == 128 ? 1 : 2))) & (D / 32 - 1);
+                        const uint4 cw = *reinterpret_cast<const uint4*>(st + codes_at + ch * 16);
+                        uint32_t pair = *reinterpret_cast<const uint32_t*>(st + pairs_at + ((ch * 32) >> p.c.g_shift) * 4);
+                        if (clear) pair = 0u;
+                        if (spoil) pair = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                        const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
+                        const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t x = words[j], y = x >> 8;
+                            const int chunk = ch * 4 + j;
+                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * C::HALF + (((chunk & 7) ^ (tt & 7)) << 4)) =
+                                make_uint4(fma2<BF16>(Codes<BF16>::low(x), s2, l2), fma2<BF16>(Codes<BF16>::high(x), s2, l2),
+                                           fma2<BF16>(Codes<BF16>::low(y), s2, l2), fma2<BF16>(Codes<BF16>::high(y), s2, l2));
+                        }
                     }
-                    if (++slot == NS) slot = 0, slot_ph ^= 1u;
+                    ptx::fence_proxy_async_smem();
                 }
+                __syncwarp();
+                if (ok && lane == 0) {
+                    ptx::mbar_arrive(kv_full(slot));
+                    ptx::mbar_arrive(raw_empty(s));
+                }
+                slot += 2;                          // the other warpgroup fills every other slot
+                if (slot >= NS) slot -= NS, slot_ph ^= 1u;
                 if (++s == RS) s = 0, ph ^= 1u;
             }
         }
     } else {
+        ptx::regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------------ softmax
-        const int i = warp >> 2;                     // row tile
-        const int r = threadIdx.x;                   // row of the item
+        const int i = warp >> 3;                     // row tile
+        const int half = (warp >> 2) & 1;            // columns 64 half ..
+        const int r1 = (warp & 3) * 32 + lane;       // row of the tile
+        const int r = 128 * i + r1;                  // row of the item
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i, o_tm = tmem + lanes + C::O_COL + 128 * i;
+        const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i + 64 * half;
+        const uint32_t o_tm = tmem + lanes + C::O_COL + 128 * i + (D / 2) * half;
+        float* ex_mine = reinterpret_cast<float*>(smem + C::OFF_EX) + (2 * i + half) * 128 + r1;
+        float* ex_other = reinterpret_cast<float*>(smem + C::OFF_EX) + (2 * i + (half ^ 1)) * 128 + r1;
+        const uint32_t pair_bar = 1 + 4 * i + (warp & 3);     // this warp and the one with the other half
         // a zero scale becomes a tiny one, so that a masked -inf stays -inf; a negative
         // one moves its sign to Q
         const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
@@ -316,13 +363,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int lo = p.window > 0 ? pos + 1 - p.window : 0;
             if (!idle) {
                 const uint16_t* src = static_cast<const uint16_t*>(p.q) + tq * p.q_stride + (int64_t)head * D;
-                uint8_t* dst = smem + C::OFF_Q + i * C::TILE + (r & 127) * 128;
-#pragma unroll 4
-                for (int ch = 0; ch < D / 8; ++ch) {
+                uint8_t* dst = smem + C::OFF_Q + i * C::TILE + r1 * 128;
+#pragma unroll 2
+                for (int c = 0; c < D / 16; ++c) {
+                    const int ch = half * (D / 16) + c;
                     uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
                     if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
                     v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::HALF + (((ch & 7) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::HALF + (((ch & 7) ^ (r1 & 7)) << 4)) =
                         make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 }
@@ -334,66 +382,90 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             float m = -INFINITY, l = 0.f;
             if (!idle) {
                 for (int t = tb; t < te; ++t) {
-                    ok = __all_sync(0xffffffffu, wait(s_full(i), s_ph, DEVICE_TIMEOUT_EPILOGUE));
+                    if (ok) ok = __all_sync(0xffffffffu, wait(s_full(i), s_ph, DEVICE_TIMEOUT_EPILOGUE));
                     s_ph ^= 1u;
-                    if (!ok) break;
+                    if (!ok) {
+                        // given up: only keep the other half's warp from waiting for this one
+                        ptx::named_barrier_sync(pair_bar, 64);
+                        continue;
+                    }
                     ptx::tc_fence_after();
-                    const int h = hi - t * TN, b = lo - t * TN;      // this row sees columns [b, h)
-                    const bool masked = __any_sync(0xffffffffu, b > 0 || h < TN);
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        ptx::tmem_ld32(s_tm + 32 * c, v);
-                        ptx::tmem_wait_ld();
-                        if (masked) {
+                    const int h = hi - t * TN - 64 * half, b = lo - t * TN - 64 * half;   // this row sees columns [b, h)
+                    uint32_t v[32];
+                    if (__any_sync(0xffffffffu, b > 0 || h < 64)) {
+                        // the few tiles on a mask's edge: what the row does not see becomes -inf in place
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            ptx::tmem_ld32(s_tm + c, v);
+                            ptx::tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (32 * c + k < b || 32 * c + k >= h) v[k] = 0xFF800000u;
+                                if (c + k < b || c + k >= h) v[k] = 0xFF800000u;
+                            ptx::tmem_st32(s_tm + c, v);
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                        ptx::tmem_wait_st();
                     }
-                    mx *= sl2;
+                    float mx = -INFINITY, mx2 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        ptx::tmem_ld32(s_tm + 32 * c, v);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                            mx2 = max3(mx2, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                        }
+                    }
+                    mx = fmaxf(mx, mx2);
+                    *ex_mine = mx;
+                    ptx::named_barrier_sync(pair_bar, 64);
+                    mx = sl2 * fmaxf(mx, *ex_other);
                     const bool grow = mx > m + 8.f;
                     if (__any_sync(0xffffffffu, grow)) {
                         const float m1 = grow ? mx : m, f = grow ? part_weight(m, m1) : 1.f;
                         m = m1;
                         l *= f;
                         if (t > tb) {
-#pragma unroll
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t v[16];
-                                ptx::tmem_ld16(o_tm + 16 * c, v);
+#pragma unroll 1
+                            for (int c = 0; c < D / 2; c += 16) {
+                                uint32_t x[16];
+                                ptx::tmem_ld16(o_tm + c, x);
                                 ptx::tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                                ptx::tmem_st16(o_tm + 16 * c, v);
+                                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                                ptx::tmem_st16(o_tm + c, x);
                             }
+                            // v is loaded again: it need not outlive the rescale
+                            ptx::tmem_ld32(s_tm + 32, v);
+                            ptx::tmem_wait_ld();
                         }
                     }
+                    // columns 32-63 are still in registers, 0-31 are read again
                     const float mm = m == -INFINITY ? 0.f : m;
-                    float l0 = 0.f, l1 = 0.f;
+                    const uint64_t sl = f2(sl2, sl2), nm = f2(-mm, -mm);
+                    uint64_t la = 0, lb = 0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32], o[16];
-                        ptx::tmem_ld32(s_tm + 32 * c, v);
-                        ptx::tmem_wait_ld();
-                        if (masked) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (32 * c + k < b || 32 * c + k >= h) v[k] = 0xFF800000u;
-                        }
+                    for (int c = 1; c >= 0; --c) {
+                        uint32_t o[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float e0 = ex2(fmaf(__uint_as_float(v[2 * k]), sl2, -mm));
-                            const float e1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sl2, -mm));
-                            l0 += e0, l1 += e1;
-                            o[k] = pack2<BF16>(e0, e1);
+                            float2 e = un2(fma_f2(f2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl, nm));
+                            e.x = ex2(e.x), e.y = ex2(e.y);
+                            if (k & 1)
+                                lb = add_f2(lb, f2(e.x, e.y));
+                            else
+                                la = add_f2(la, f2(e.x, e.y));
+                            o[k] = pack2<BF16>(e.x, e.y);
+                        }
+                        // P's 32 columns cover S's first 32, so those are read before any of it is stored
+                        if (c == 1) {
+                            ptx::tmem_ld32(s_tm, v);
+                            ptx::tmem_wait_ld();
                         }
                         ptx::tmem_st16(s_tm + 16 * c, o);
                     }
-                    l += l0 + l1;
+                    const float2 ls = un2(add_f2(la, lb));
+                    l += ls.x + ls.y;
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -402,6 +474,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 if (ok) ok = __all_sync(0xffffffffu, wait(o_full(i), o_ph, DEVICE_TIMEOUT_EPILOGUE));
                 ptx::tc_fence_after();
                 o_ph ^= 1u;
+                // the row's sum: both halves
+                *ex_mine = l;
+                ptx::named_barrier_sync(pair_bar, 64);
+                l += *ex_other;
             }
             // ---- the item's result, or this block's part of it
             const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
@@ -410,11 +486,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             float* part = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
             if (!idle && ok) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D;
-#pragma unroll 2
-                for (int c = 0; c < D / 16; ++c) {
+                uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D + half * (D / 2);
+                float* po = part + (size_t)r * D + half * (D / 2);
+#pragma unroll 1
+                for (int c = 0; c < D / 2; c += 16) {
                     uint32_t v[16];
-                    ptx::tmem_ld16(o_tm + 16 * c, v);
+                    ptx::tmem_ld16(o_tm + c, v);
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -424,18 +501,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         for (int k = 0; k < 8; ++k) d[(k >> 1) + 4 * (k & 1)] = __uint_as_float(v[8 * j + k]);
                         if (r < rows) {
                             if (whole) {
-                                *reinterpret_cast<uint4*>(out + 16 * c + 8 * j) =
+                                *reinterpret_cast<uint4*>(out + c + 8 * j) =
                                     make_uint4(pack2<BF16>(d[0] * inv, d[1] * inv), pack2<BF16>(d[2] * inv, d[3] * inv),
                                                pack2<BF16>(d[4] * inv, d[5] * inv), pack2<BF16>(d[6] * inv, d[7] * inv));
                             } else {
-                                float4* dst = reinterpret_cast<float4*>(part + (size_t)r * D + 16 * c + 8 * j);
+                                float4* dst = reinterpret_cast<float4*>(po + c + 8 * j);
                                 __stcg(dst, make_float4(d[0], d[1], d[2], d[3]));
                                 __stcg(dst + 1, make_float4(d[4], d[5], d[6], d[7]));
                             }
                         }
                     }
                 }
-                if (r < rows) {
+                if (r < rows && half == 0) {
                     if (!whole)
                         __stcg(reinterpret_cast<float2*>(part + R * D) + r, make_float2(m, l));
                     else if (p.lse != nullptr)
@@ -449,7 +526,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             }
             if (!whole) {
                 __threadfence();
-                ptx::named_barrier_sync(1, 256);
+                ptx::named_barrier_sync(9, 512);
                 if (threadIdx.x == 0) {
                     int last = 0;
                     if (ok) {
@@ -460,20 +537,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                     }
                     *last_flag = last;
                 }
-                ptx::named_barrier_sync(1, 256);
+                ptx::named_barrier_sync(9, 512);
                 if (*last_flag) {
                     __threadfence();
-                    merge_parts<BF16, D, R, C::MERGE_ROWS, 256>(p, w, b_first, parts,
-                                                                reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 1);
+                    merge_parts<BF16, D, R, C::MERGE_ROWS, 512>(p, w, b_first, parts,
+                                                                reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 9);
                 }
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 24) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc<1>(tmem, 512);
+        ptx::tmem_dealloc<1>(*tmem_slot, 512);
     }
 }
 
