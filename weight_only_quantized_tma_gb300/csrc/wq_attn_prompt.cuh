@@ -4,18 +4,19 @@
 //   S = Q K^T,  P = exp2(scale' S - m),  O += P V,  out = O / sum P
 //
 // An item is 256 rows (query tokens x heads of a group, so a key head's codes are unpacked
-// once for all of them) as two 128-row tiles; cached tokens come in tiles of 128.  Bound by
-// the tensor cores: 4 products of 128 x 128 x D for each tile of tokens, so one row tile's
-// products run while the other's softmax does:
-//   warps 0-7 / 8-15  softmax of row tile 0 / 1: two threads for each row, 64 columns each.
-//                     S from tensor memory, the row's maximum through shared memory, P back
-//                     over S; O is rescaled only when a row's maximum grows by more than
-//                     2^8; at the end O -> out;
-//   warps 16-19, 20-23  unpack keys / values: a thread for each token, codes -> RN(lo + q s)
+// once for all of them) as two 128-row tiles; cached tokens come in tiles of 128, S and P in
+// halves of 64.  Bound by the tensor cores and the softmax between the products.  Each row
+// tile has two S buffers of 64 columns, so its softmax finds the next half ready when it has
+// signalled the last (with one buffer of 128, product, softmax and product followed one
+// another: 1087 us against DESIGN's figure for 4096 queries over 16384 tokens, 32 heads):
+//   warps 0-3 / 4-7   softmax of row tile 0 / 1, a thread for each row: S from tensor memory,
+//                     P back over it; O is rescaled only when a row's maximum grows by more
+//                     than 2^8; at the end O -> out;
+//   warps 8-11, 12-15 unpack keys / values: a thread for each token, codes -> RN(lo + q s)
 //                     into a three-slot ring of swizzled shared-memory tiles, K and V in turn;
-//   warps 24, 25      issue the MMAs of row tile 0 / 1 (PV, then the next S): the queue before
+//   warps 16, 17      issue the MMAs of row tile 0 / 1 (PV, then the next S): the queue before
 //                     the tensor core is short, so while one warp waits the other's products run;
-//   warp 26           copies page blocks into a two-stage ring with bulk copies (warp 27 only
+//   warp 18           copies page blocks into a two-stage ring with bulk copies (warp 19 only
 //                     fills the warpgroup, which hands its registers on).
 // Both operand tiles have the same image [D / 64][128 tokens][128 B]: K is read K-major, V
 // MN-major, so V is never transposed.  Eight codes of a word land in the order 0 4 1 5 2 6
@@ -29,11 +30,11 @@ namespace wq {
 
 constexpr int kPromptTN = 128;
 constexpr int kPromptRows = 256;
-constexpr int kPromptThreads = 896;
-// Registers of a thread by role; a block is launched with 72 for each, and the seven
-// warpgroups' shares add up to no more than the same 504.
-constexpr int kRegsSoftmax = 80, kRegsUnpack = 64, kRegsIssue = 40;
-static_assert(4 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 7 * 72, "register split");
+constexpr int kPromptThreads = 640;
+// Registers of a thread by role; a block is launched with 96 for each, and the five
+// warpgroups' shares add up to no more than the same 480.
+constexpr int kRegsSoftmax = 144, kRegsUnpack = 72, kRegsIssue = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 5 * 96, "register split");
 
 template <int D>
 struct PromptCfg {
@@ -44,13 +45,12 @@ struct PromptCfg {
     static constexpr int OFF_Q = 0;                        // two row tiles
     static constexpr int OFF_KV = OFF_Q + 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + KV_SLOTS * TILE;
-    static constexpr int NBARS = 2 * RAW_STAGES + 2 * KV_SLOTS + 11;
+    static constexpr int NBARS = 2 * RAW_STAGES + 2 * KV_SLOTS + 15;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
-    static constexpr int OFF_EX = (OFF_MISC + 16 + 15) / 16 * 16;     // a row's two halves: maximum, sum
-    static constexpr int OFF_RAW = (OFF_EX + 2 * 2 * 128 * 4 + 127) / 128 * 128;
+    static constexpr int OFF_RAW = (OFF_MISC + 16 + 127) / 128 * 128;
     static constexpr int MERGE_ROWS = 32;                  // merge weights live in the Q tiles
     // tensor memory columns
-    static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i, O_i at 256 + 128 i; P_i over S_i
+    static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i + 64 half, O_i at 256 + 128 i; P over S
 };
 
 // Two fp32 values in a 64-bit register: one instruction for both.
@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     auto kv_empty = [&](int i) { return bar0 + 8u * (2 * RS + NS + i); };
     const uint32_t bar1 = bar0 + 8u * (2 * RS + 2 * NS);
     auto q_full = [&](int i) { return bar1 + 8u * i; };
-    auto s_full = [&](int i) { return bar1 + 8u * (2 + i); };
-    auto p_full = [&](int i) { return bar1 + 8u * (4 + i); };
-    auto o_full = [&](int i) { return bar1 + 8u * (6 + i); };
-    auto o_empty = [&](int i) { return bar1 + 8u * (8 + i); };
-    const uint32_t final_bar = bar1 + 80u;
+    auto o_empty = [&](int i) { return bar1 + 8u * (2 + i); };
+    auto o_done = [&](int i) { return bar1 + 8u * (4 + i); };                 // a PV of row tile i has ended
+    auto s_full = [&](int i, int h) { return bar1 + 8u * (6 + 2 * i + h); };
+    auto p_full = [&](int i, int h) { return bar1 + 8u * (10 + 2 * i + h); };
+    const uint32_t final_bar = bar1 + 8u * 14;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -108,18 +108,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         for (int i = 0; i < RS; ++i) ptx::mbar_init(raw_full(i), 1), ptx::mbar_init(raw_empty(i), 8);
         for (int i = 0; i < NS; ++i) ptx::mbar_init(kv_full(i), 4), ptx::mbar_init(kv_empty(i), 2);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(q_full(i), 8);
-            ptx::mbar_init(s_full(i), 1);
-            ptx::mbar_init(p_full(i), 8);
-            ptx::mbar_init(o_full(i), 1);
-            ptx::mbar_init(o_empty(i), 8);
+            ptx::mbar_init(q_full(i), 4);
+            ptx::mbar_init(o_empty(i), 4);
+            ptx::mbar_init(o_done(i), 1);
+            for (int h = 0; h < 2; ++h) ptx::mbar_init(s_full(i, h), 1), ptx::mbar_init(p_full(i, h), 4);
         }
         ptx::mbar_init(final_bar, 2);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
     }
-    if (warp == 24) {
+    if (warp == 16) {
         ptx::tmem_alloc<1>(sbase + C::OFF_MISC, 512);
         ptx::tmem_relinquish<1>();
     }
@@ -143,9 +142,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     auto tile_begin = [&]() { return w.v.t0 + (int)(w.u - w.item0); };
     auto tile_end = [&]() { return w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0); };
 
-    if (warp >= 24) {
+    if (warp >= 16) {
     ptx::regs_dec<kRegsIssue>();
-    if (warp == 26) {
+    if (warp == 18) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = ptx::policy_evict_last();
         int s = 0;
@@ -181,20 +180,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         if (!ok)   // given up: copies in flight land before the block may end
             for (int i = 0; i < RS; ++i)
                 if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
-    } else if (warp < 26) {
+    } else if (warp < 18) {
         // ------------------------------------------------------------ MMA issuers
         // One lane for each row tile, and as few instructions between products as can be:
         // a product of 128 x 128 x 16 takes 64 cycles, so address arithmetic and waits here
         // leave the tensor core idle.  The products of a tile are unrolled with constant
         // offsets, and the whole of tensor memory is ours, so its addresses are constants.
-        const int i = warp - 24;
+        const int i = warp - 16;
         if (lane == 0) {
-            constexpr uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 128);
+            constexpr uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 64);
             constexpr uint32_t id_o = ptx::make_idesc_f16(BF16, 128, D) | ptx::kIdescBTransposed;
             const uint32_t q_lo = ptx::sdesc_lo(sbase + C::OFF_Q + i * C::TILE);
             const uint32_t k_lo = ptx::sdesc_lo(sbase + C::OFF_KV), v_lo = ptx::sdesc_lo_mn(sbase + C::OFF_KV, C::HALF);
             const uint32_t s_tm = C::S_COL + 128 * i, o_tm = C::O_COL + 128 * i;
-            const uint32_t b_q = q_full(i), b_s = s_full(i), b_p = p_full(i), b_of = o_full(i), b_oe = o_empty(i);
+            const uint32_t b_q = q_full(i), b_s = s_full(i, 0), b_p = p_full(i, 0), b_od = o_done(i), b_oe = o_empty(i);
             int slot = 0;
             uint32_t slot_ph = 0, q_ph = 0, p_ph = 0, o_ph = 1;
             auto next_slot = [&]() {
@@ -203,15 +202,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             auto ready = [&](uint32_t bar, uint32_t parity) {
                 if (!ptx::mbar_try_wait(bar, parity)) wait(bar, parity, DEVICE_TIMEOUT_MMA);
             };
-            auto qk = [&](int k_slot) {      // S_i = Q_i K^T
-                const uint32_t b = k_lo + k_slot * (C::TILE >> 4);
+            auto qk = [&](int h, int k_slot) {      // S_i = Q_i K^T of 64 tokens
+                const uint32_t b = k_lo + k_slot * (C::TILE >> 4) + h * (64 * 128 >> 4);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const uint32_t off = (k >> 2) * (C::HALF >> 4) + (k & 3) * 2;
-                    ptx::mma_f16_ss(s_tm, q_lo + off, ptx::kSdescHi, b + off, ptx::kSdescHi, id_s, k > 0);
+                    ptx::mma_f16_ss(s_tm + 64 * h, q_lo + off, ptx::kSdescHi, b + off, ptx::kSdescHi, id_s, k > 0);
                 }
-                ptx::mma_commit(b_s);
-                ptx::mma_commit(kv_empty(k_slot));
+                ptx::mma_commit(b_s + 8 * h);
+                if (h == 1) ptx::mma_commit(kv_empty(k_slot));
             };
             for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
                 const int tiles = tile_end() - tile_begin();
@@ -229,33 +228,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 ready(kv_full(slot), slot_ph);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                qk(slot);
+                qk(0, slot);
+                qk(1, slot);
                 next_slot();
-                for (int t = 0; t < tiles; ++t) {
+                ready(b_oe, o_ph);
+                o_ph ^= 1u;
+                for (int t = 0; t < tiles && ok; ++t) {
                     const int v_slot = slot;
                     ready(kv_full(v_slot), slot_ph);
                     next_slot();
-                    if (t == 0) {
-                        ready(b_oe, o_ph);
-                        o_ph ^= 1u;
-                    }
-                    ready(b_p, p_ph);
-                    p_ph ^= 1u;
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    const uint32_t b = v_lo + v_slot * (C::TILE >> 4);   // O_i (+)= P_i V
+                    const bool more = t + 1 < tiles;
+                    if (more) ready(kv_full(slot), slot_ph);
 #pragma unroll
-                    for (int k = 0; k < TN / 16; ++k)
-                        ptx::mma_f16_ts(o_tm, s_tm + 64 * (k >> 2) + 8 * (k & 3), b + k * (2048 >> 4), ptx::kSdescHi, id_o, k > 0 || t > 0);
-                    ptx::mma_commit(kv_empty(v_slot));
-                    if (t + 1 < tiles) {
-                        ready(kv_full(slot), slot_ph);
+                    for (int h = 0; h < 2; ++h) {
+                        ready(b_p + 8 * h, p_ph);
                         if (!ok) break;
-                        qk(slot);
-                        next_slot();
-                    } else {
-                        ptx::mma_commit(b_of);
+                        ptx::tc_fence_after();
+                        const uint32_t b = v_lo + v_slot * (C::TILE >> 4) + h * (64 * 128 >> 4);   // O_i (+)= P_i V
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_f16_ts(o_tm, s_tm + 64 * h + 8 * k, b + k * (2048 >> 4), ptx::kSdescHi, id_o,
+                                            k > 0 || h > 0 || t > 0);
+                        ptx::mma_commit(b_od);
+                        if (h == 1) ptx::mma_commit(kv_empty(v_slot));
+                        if (more) qk(h, slot);
                     }
+                    p_ph ^= 1u;
+                    if (more) next_slot();
                 }
             }
             // given up (either warp): the MMAs in flight end before tensor memory is freed
@@ -266,10 +265,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         }
         __syncwarp();
     }
-    } else if (warp >= 16) {
+    } else if (warp >= 8) {
         ptx::regs_dec<kRegsUnpack>();
         // ------------------------------------------------------------ unpack
-        const int which = (warp - 16) >> 2;        // keys, values
+        const int which = (warp - 8) >> 2;         // keys, values
         const int tt = threadIdx.x & 127;          // the token of the tile
         const int pg = tt >> p.c.p_shift, place = tt & (p.c.P - 1);
         const int codes_at = pg * p.c.block_bytes + kv4_codes_at(p.c, which, place);
@@ -336,21 +335,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     } else {
         ptx::regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------------ softmax
-        const int i = warp >> 3;                     // row tile
-        const int half = (warp >> 2) & 1;            // columns 64 half ..
-        const int r1 = (warp & 3) * 32 + lane;       // row of the tile
-        const int r = 128 * i + r1;                  // row of the item
+        const int i = warp >> 2;                     // row tile
+        const int r1 = threadIdx.x & 127;            // row of the tile
+        const int r = threadIdx.x;                   // row of the item
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i + 64 * half;
-        const uint32_t o_tm = tmem + lanes + C::O_COL + 128 * i + (D / 2) * half;
-        float* ex_mine = reinterpret_cast<float*>(smem + C::OFF_EX) + (2 * i + half) * 128 + r1;
-        float* ex_other = reinterpret_cast<float*>(smem + C::OFF_EX) + (2 * i + (half ^ 1)) * 128 + r1;
-        const uint32_t pair_bar = 1 + 4 * i + (warp & 3);     // this warp and the one with the other half
+        const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i, o_tm = tmem + lanes + C::O_COL + 128 * i;
         // a zero scale becomes a tiny one, so that a masked -inf stays -inf; a negative
         // one moves its sign to Q
         const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-        uint32_t s_ph = 0, o_ph = 0;
+        const uint64_t sl = f2(sl2, sl2);
+        uint32_t s_ph = 0, od_ph = 1;                // od_ph: parity of the last PV that this tile's P has started
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows();
             const bool idle = 128 * i >= rows;       // no rows in this tile
@@ -364,9 +359,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             if (!idle) {
                 const uint16_t* src = static_cast<const uint16_t*>(p.q) + tq * p.q_stride + (int64_t)head * D;
                 uint8_t* dst = smem + C::OFF_Q + i * C::TILE + r1 * 128;
-#pragma unroll 2
-                for (int c = 0; c < D / 16; ++c) {
-                    const int ch = half * (D / 16) + c;
+#pragma unroll 4
+                for (int ch = 0; ch < D / 8; ++ch) {
                     uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
                     if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
                     v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
@@ -381,53 +375,53 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int tb = tile_begin(), te = tile_end();
             float m = -INFINITY, l = 0.f;
             if (!idle) {
-                for (int t = tb; t < te; ++t) {
-                    if (ok) ok = __all_sync(0xffffffffu, wait(s_full(i), s_ph, DEVICE_TIMEOUT_EPILOGUE));
-                    s_ph ^= 1u;
-                    if (!ok) {
-                        // given up: only keep the other half's warp from waiting for this one
-                        ptx::named_barrier_sync(pair_bar, 64);
-                        continue;
-                    }
-                    ptx::tc_fence_after();
-                    const int h = hi - t * TN - 64 * half, b = lo - t * TN - 64 * half;   // this row sees columns [b, h)
-                    uint32_t v[32];
-                    if (__any_sync(0xffffffffu, b > 0 || h < 64)) {
-                        // the few tiles on a mask's edge: what the row does not see becomes -inf in place
+                const int first = tb * TN, end = te * TN;
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 32) {
-                            ptx::tmem_ld32(s_tm + c, v);
-                            ptx::tmem_wait_ld();
+                for (int tok = first; tok < end; tok += 64) {
+                    const int hf = tok >> 6 & 1;
+                    const uint32_t s_half = s_tm + 64 * hf;
+                    if (ok) ok = __all_sync(0xffffffffu, wait(s_full(i, hf), s_ph, DEVICE_TIMEOUT_EPILOGUE));
+                    if (!ok) break;
+                    s_ph ^= (uint32_t)hf;            // after the second half
+                    ptx::tc_fence_after();
+                    uint32_t v[2][32];
+                    ptx::tmem_ld32(s_half, v[0]);
+                    ptx::tmem_ld32(s_half + 32, v[1]);
+                    const int h = hi - tok, b = lo - tok;      // this row sees columns [b, h)
+                    const bool masked = __any_sync(0xffffffffu, b > 0 || h < 64);
+                    ptx::tmem_wait_ld();
+                    if (masked) {
+                        // the few tiles on a mask's edge: bit k of `see` is column k
+                        const uint64_t below = h >= 64 ? ~0ull : h <= 0 ? 0ull : (1ull << h) - 1;
+                        const uint64_t from = b <= 0 ? ~0ull : b >= 64 ? 0ull : ~((1ull << b) - 1);
+                        const uint32_t see[2] = {(uint32_t)(below & from), (uint32_t)((below & from) >> 32)};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (c + k < b || c + k >= h) v[k] = 0xFF800000u;
-                            ptx::tmem_st32(s_tm + c, v);
-                        }
-                        ptx::tmem_wait_st();
+                                if (!(see[c] >> k & 1u)) v[c][k] = 0xFF800000u;
                     }
-                    float mx = -INFINITY, mx2 = -INFINITY;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        ptx::tmem_ld32(s_tm + 32 * c, v);
-                        ptx::tmem_wait_ld();
+                    for (int k = 0; k < 32; k += 4)
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                            mx2 = max3(mx2, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+                        for (int c = 0; c < 2; ++c) {
+                            mx[c] = max3(mx[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
+                            mx[2 + c] = max3(mx[2 + c], __uint_as_float(v[c][k + 2]), __uint_as_float(v[c][k + 3]));
                         }
-                    }
-                    mx = fmaxf(mx, mx2);
-                    *ex_mine = mx;
-                    ptx::named_barrier_sync(pair_bar, 64);
-                    mx = sl2 * fmaxf(mx, *ex_other);
-                    const bool grow = mx > m + 8.f;
+                    const float top = sl2 * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    const bool grow = top > m + 8.f;
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float m1 = grow ? mx : m, f = grow ? part_weight(m, m1) : 1.f;
+                        const float m1 = grow ? top : m, f = grow ? part_weight(m, m1) : 1.f;
                         m = m1;
                         l *= f;
-                        if (t > tb) {
+                        if (tok > first) {
+                            // O is scaled between products: the last one has to have ended
+                            ok = __all_sync(0xffffffffu, wait(o_done(i), od_ph, DEVICE_TIMEOUT_EPILOGUE));
+                            if (!ok) break;
+                            ptx::tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D / 2; c += 16) {
+                            for (int c = 0; c < D; c += 16) {
                                 uint32_t x[16];
                                 ptx::tmem_ld16(o_tm + c, x);
                                 ptx::tmem_wait_ld();
@@ -435,21 +429,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                                 for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
                                 ptx::tmem_st16(o_tm + c, x);
                             }
-                            // v is loaded again: it need not outlive the rescale
-                            ptx::tmem_ld32(s_tm + 32, v);
-                            ptx::tmem_wait_ld();
                         }
                     }
-                    // columns 32-63 are still in registers, 0-31 are read again
                     const float mm = m == -INFINITY ? 0.f : m;
-                    const uint64_t sl = f2(sl2, sl2), nm = f2(-mm, -mm);
+                    const uint64_t nm = f2(-mm, -mm);
                     uint64_t la = 0, lb = 0;
 #pragma unroll
-                    for (int c = 1; c >= 0; --c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t o[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            float2 e = un2(fma_f2(f2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl, nm));
+                            float2 e = un2(fma_f2(f2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), sl, nm));
                             e.x = ex2(e.x), e.y = ex2(e.y);
                             if (k & 1)
                                 lb = add_f2(lb, f2(e.x, e.y));
@@ -457,27 +447,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                                 la = add_f2(la, f2(e.x, e.y));
                             o[k] = pack2<BF16>(e.x, e.y);
                         }
-                        // P's 32 columns cover S's first 32, so those are read before any of it is stored
-                        if (c == 1) {
-                            ptx::tmem_ld32(s_tm, v);
-                            ptx::tmem_wait_ld();
-                        }
-                        ptx::tmem_st16(s_tm + 16 * c, o);
+                        ptx::tmem_st16(s_half + 16 * c, o);
                     }
                     const float2 ls = un2(add_f2(la, lb));
                     l += ls.x + ls.y;
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(p_full(i));
+                    if (lane == 0) ptx::mbar_arrive(p_full(i, hf));
+                    od_ph ^= 1u;
                 }
-                if (ok) ok = __all_sync(0xffffffffu, wait(o_full(i), o_ph, DEVICE_TIMEOUT_EPILOGUE));
+                if (ok) ok = __all_sync(0xffffffffu, wait(o_done(i), od_ph, DEVICE_TIMEOUT_EPILOGUE));
                 ptx::tc_fence_after();
-                o_ph ^= 1u;
-                // the row's sum: both halves
-                *ex_mine = l;
-                ptx::named_barrier_sync(pair_bar, 64);
-                l += *ex_other;
             }
             // ---- the item's result, or this block's part of it
             const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
@@ -486,10 +467,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             float* part = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
             if (!idle && ok) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D + half * (D / 2);
-                float* po = part + (size_t)r * D + half * (D / 2);
+                uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D;
+                float* po = part + (size_t)r * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 16) {
+                for (int c = 0; c < D; c += 16) {
                     uint32_t v[16];
                     ptx::tmem_ld16(o_tm + c, v);
                     ptx::tmem_wait_ld();
@@ -512,7 +493,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         }
                     }
                 }
-                if (r < rows && half == 0) {
+                if (r < rows) {
                     if (!whole)
                         __stcg(reinterpret_cast<float2*>(part + R * D) + r, make_float2(m, l));
                     else if (p.lse != nullptr)
@@ -526,7 +507,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             }
             if (!whole) {
                 __threadfence();
-                ptx::named_barrier_sync(9, 512);
+                ptx::named_barrier_sync(1, 256);
                 if (threadIdx.x == 0) {
                     int last = 0;
                     if (ok) {
@@ -537,18 +518,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                     }
                     *last_flag = last;
                 }
-                ptx::named_barrier_sync(9, 512);
+                ptx::named_barrier_sync(1, 256);
                 if (*last_flag) {
                     __threadfence();
-                    merge_parts<BF16, D, R, C::MERGE_ROWS, 512>(p, w, b_first, parts,
-                                                                reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 9);
+                    merge_parts<BF16, D, R, C::MERGE_ROWS, 256>(p, w, b_first, parts,
+                                                                reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 1);
                 }
             }
         }
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 24) {
+    if (warp == 16) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc<1>(*tmem_slot, 512);
     }
