@@ -7,7 +7,7 @@ namespace {
 template <bool BF16, int D>
 cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
     using C = PromptCfg<D>;
-    const int stage = (p.c.block_bytes * (kPromptTN / p.c.P) + 127) / 128 * 128;
+    const int stage = (kPromptTN * (D + 8 * (D / p.c.G)) + 127) / 128 * 128;
     constexpr int most = 1024 + C::OFF_RAW + C::RAW_STAGES * kPromptTN * (D + 8 * (D / 32));
     static_assert(most <= 227 * 1024, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);

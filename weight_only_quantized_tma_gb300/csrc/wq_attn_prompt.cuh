@@ -4,21 +4,24 @@
 //   S = Q K^T,  P = exp2(scale' S - m),  O += P V,  out = O / sum P
 //
 // An item is 256 rows (query tokens x heads of a group, so a key head's codes are unpacked
-// once for all of them) as two 128-row tiles; cached tokens come in tiles of 128, S and P in
-// halves of 64.  Bound by the tensor cores and the softmax between the products.  Each row
-// tile has two S buffers of 64 columns, so its softmax finds the next half ready when it has
-// signalled the last (with one buffer of 128, product, softmax and product followed one
-// another: 1087 us against DESIGN's figure for 4096 queries over 16384 tokens, 32 heads):
+// once for all of them) as two 128-row tiles; cached tokens come in tiles of 64.  Bound by
+// the tensor cores and by the softmax between the products (a quarter of the exponentials'
+// unit and half of the issue slots).  What keeps them busy: each row tile has two S buffers,
+// so its softmax finds the next S ready when it has signalled the last P (with one, product,
+// softmax and product followed one another); four slots each of unpacked keys and values;
+// and as little as possible between two products.
 //   warps 0-3 / 4-7   softmax of row tile 0 / 1, a thread for each row: S from tensor memory,
-//                     P back over it; O is rescaled only when a row's maximum grows by more
-//                     than 2^8; at the end O -> out;
-//   warps 8-11, 12-15 unpack keys / values: a thread for each token, codes -> RN(lo + q s)
-//                     into a three-slot ring of swizzled shared-memory tiles, K and V in turn;
-//   warps 16, 17      issue the MMAs of row tile 0 / 1 (PV, then the next S): the queue before
-//                     the tensor core is short, so while one warp waits the other's products run;
-//   warp 18           copies page blocks into a two-stage ring with bulk copies (warp 19 only
-//                     fills the warpgroup, which hands its registers on).
-// Both operand tiles have the same image [D / 64][128 tokens][128 B]: K is read K-major, V
+//                     P back over it.  It runs under the row's maximum so far, and is
+//                     repeated under a new one (O rescaled) only where a sum shows that a
+//                     score passed that maximum by more than 2^8; at the end O -> out;
+//   warps 8-11, 12-15 unpack keys / values: two threads for each token, codes -> RN(lo + q s)
+//                     into swizzled shared-memory tiles;
+//   warps 16, 17      issue the MMAs of row tile 0 / 1 (PV, then the S after next): the queue
+//                     before the tensor core is short, so while one warp waits the other's
+//                     products run;
+//   warp 18           copies page blocks into a three-stage ring with bulk copies (warp 19
+//                     only fills the warpgroup, which hands its registers on).
+// Both operand tiles have the same image [D / 64][64 tokens][128 B]: K is read K-major, V
 // MN-major, so V is never transposed.  Eight codes of a word land in the order 0 4 1 5 2 6
 // 3 7 that the unpack gives; Q is stored in the same order and O is read back through it.
 #pragma once
@@ -28,7 +31,7 @@
 
 namespace wq {
 
-constexpr int kPromptTN = 128;
+constexpr int kPromptTN = 64;
 constexpr int kPromptRows = 256;
 constexpr int kPromptThreads = 640;
 // Registers of a thread by role; a block is launched with 96 for each, and the five
@@ -38,19 +41,22 @@ static_assert(2 * kRegsSoftmax + 2 * kRegsUnpack + kRegsIssue <= 5 * 96, "regist
 
 template <int D>
 struct PromptCfg {
-    static constexpr int TILE = 128 * D * 2;               // a 16-bit operand tile: 128 rows of D
-    static constexpr int HALF = 128 * 128;                 // its part of 64 columns
-    static constexpr int KV_SLOTS = 3;
-    static constexpr int RAW_STAGES = 2;
+    static constexpr int Q_TILE = 128 * D * 2;             // 128 rows of D
+    static constexpr int Q_HALF = 128 * 128;               // its part of 64 columns
+    static constexpr int KV_TILE = 64 * D * 2;             // 64 tokens of D
+    static constexpr int KV_HALF = 64 * 128;
+    static constexpr int SLOTS = 4;                        // of keys, and of values
+    static constexpr int RAW_STAGES = 3;
     static constexpr int OFF_Q = 0;                        // two row tiles
-    static constexpr int OFF_KV = OFF_Q + 2 * TILE;
-    static constexpr int OFF_BAR = OFF_KV + KV_SLOTS * TILE;
-    static constexpr int NBARS = 2 * RAW_STAGES + 2 * KV_SLOTS + 15;
+    static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
+    static constexpr int OFF_V = OFF_K + SLOTS * KV_TILE;
+    static constexpr int OFF_BAR = OFF_V + SLOTS * KV_TILE;
+    static constexpr int NBARS = 2 * RAW_STAGES + 4 * SLOTS + 15;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
     static constexpr int OFF_RAW = (OFF_MISC + 16 + 127) / 128 * 128;
     static constexpr int MERGE_ROWS = 32;                  // merge weights live in the Q tiles
     // tensor memory columns
-    static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i + 64 half, O_i at 256 + 128 i; P over S
+    static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i + 64 buffer, O_i at 256 + 128 i; P over S
 };
 
 // Two fp32 values in a 64-bit register: one instruction for both.
@@ -83,19 +89,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const AttnParams p, const int stage_bytes) {
     using C = PromptCfg<D>;
-    constexpr int R = kPromptRows, TN = kPromptTN, KS = D / 16, RS = C::RAW_STAGES, NS = C::KV_SLOTS;
+    constexpr int R = kPromptRows, TN = kPromptTN, KS = D / 16, RS = C::RAW_STAGES, NS = C::SLOTS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t bar0 = sbase + C::OFF_BAR;
     auto raw_full = [&](int i) { return bar0 + 8u * i; };
     auto raw_empty = [&](int i) { return bar0 + 8u * (RS + i); };
-    auto kv_full = [&](int i) { return bar0 + 8u * (2 * RS + i); };
-    auto kv_empty = [&](int i) { return bar0 + 8u * (2 * RS + NS + i); };
-    const uint32_t bar1 = bar0 + 8u * (2 * RS + 2 * NS);
+    // which: 0 keys, 1 values
+    auto kv_full = [&](int which, int i) { return bar0 + 8u * (2 * RS + 2 * NS * which + i); };
+    auto kv_empty = [&](int which, int i) { return bar0 + 8u * (2 * RS + 2 * NS * which + NS + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * RS + 4 * NS);
     auto q_full = [&](int i) { return bar1 + 8u * i; };
     auto o_empty = [&](int i) { return bar1 + 8u * (2 + i); };
     auto o_done = [&](int i) { return bar1 + 8u * (4 + i); };                 // a PV of row tile i has ended
+    // of row tile i and S buffer h
     auto s_full = [&](int i, int h) { return bar1 + 8u * (6 + 2 * i + h); };
     auto p_full = [&](int i, int h) { return bar1 + 8u * (10 + 2 * i + h); };
     const uint32_t final_bar = bar1 + 8u * 14;
@@ -106,7 +114,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < RS; ++i) ptx::mbar_init(raw_full(i), 1), ptx::mbar_init(raw_empty(i), 8);
-        for (int i = 0; i < NS; ++i) ptx::mbar_init(kv_full(i), 4), ptx::mbar_init(kv_empty(i), 2);
+        for (int i = 0; i < 2 * NS; ++i)
+            ptx::mbar_init(kv_full(i / NS, i % NS), 4), ptx::mbar_init(kv_empty(i / NS, i % NS), 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(q_full(i), 4);
             ptx::mbar_init(o_empty(i), 4);
@@ -147,6 +156,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     if (warp == 18) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = ptx::policy_evict_last();
+        const int vp = min(p.c.P, TN);                          // tokens of a page inside a tile
+        const int vblock = vp * (D + 2 * pair_row);
+        const bool parted = p.c.P > TN;                         // half of a page of 128: four pieces
         int s = 0;
         uint32_t ph = 0, issued = 0;
         for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
@@ -156,23 +168,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             for (int t = tile_begin(); t < te; ++t) {
                 const int tok = t * TN;
                 // the tile's pages that hold a token to be seen: [skip, pages)
-                const int pages = min((w.v.hi - tok + p.c.P - 1) >> p.c.p_shift, TN >> p.c.p_shift);
-                const int skip = max(w.v.lo - tok, 0) >> p.c.p_shift;
-                const bool mine = lane >= skip && lane < pages;
-                const int64_t page = mine ? safe_page(p, w.b, (tok >> p.c.p_shift) + lane) : 0;
+                const int pages = min((w.v.hi - tok + vp - 1) / vp, TN / vp);
+                const int skip = max(w.v.lo - tok, 0) / vp;
+                const bool mine = parted ? (lane < 4 && pages > 0) : (lane >= skip && lane < pages);
+                const int64_t page = mine ? safe_page(p, w.b, (tok >> p.c.p_shift) + (parted ? 0 : lane)) : 0;
                 ok = __all_sync(0xffffffffu, wait(raw_empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER));
                 if (!ok) break;
                 if (lane == 0) {
                     if (pages > skip)
-                        ptx::mbar_arrive_expect_tx(raw_full(s), (uint32_t)((pages - skip) * p.c.block_bytes));
+                        ptx::mbar_arrive_expect_tx(raw_full(s), (uint32_t)((pages - skip) * vblock));
                     else
                         ptx::mbar_arrive(raw_full(s));
                 }
                 __syncwarp();
-                if (mine)
-                    ptx::bulk_load(sbase + C::OFF_RAW + s * stage_bytes + lane * p.c.block_bytes,
-                                   p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes,
-                                   p.c.block_bytes, raw_full(s), pol);
+                const uint32_t dst = sbase + C::OFF_RAW + s * stage_bytes;
+                const uint8_t* block = p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes;
+                if (mine && !parted) ptx::bulk_load(dst + lane * vblock, block, vblock, raw_full(s), pol);
+                if (mine && parted) {
+                    const int place = tok & (p.c.P - 1), which = lane & 1;
+                    if (lane < 2)
+                        ptx::bulk_load(dst + which * vp * (D / 2), block + kv4_codes_at(p.c, which, place), vp * (D / 2),
+                                       raw_full(s), pol);
+                    else
+                        ptx::bulk_load(dst + vp * D + which * vp * pair_row, block + kv4_pairs_at(p.c, which, place),
+                                       vp * pair_row, raw_full(s), pol);
+                }
                 issued |= 1u << s;
                 if (++s == RS) s = 0, ph ^= 1u;
             }
@@ -188,73 +208,66 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         // offsets, and the whole of tensor memory is ours, so its addresses are constants.
         const int i = warp - 16;
         if (lane == 0) {
-            constexpr uint32_t id_s = ptx::make_idesc_f16(BF16, 128, 64);
+            constexpr uint32_t id_s = ptx::make_idesc_f16(BF16, 128, TN);
             constexpr uint32_t id_o = ptx::make_idesc_f16(BF16, 128, D) | ptx::kIdescBTransposed;
-            const uint32_t q_lo = ptx::sdesc_lo(sbase + C::OFF_Q + i * C::TILE);
-            const uint32_t k_lo = ptx::sdesc_lo(sbase + C::OFF_KV), v_lo = ptx::sdesc_lo_mn(sbase + C::OFF_KV, C::HALF);
+            const uint32_t q_lo = ptx::sdesc_lo(sbase + C::OFF_Q + i * C::Q_TILE);
+            const uint32_t k_lo = ptx::sdesc_lo(sbase + C::OFF_K), v_lo = ptx::sdesc_lo_mn(sbase + C::OFF_V, C::KV_HALF);
             const uint32_t s_tm = C::S_COL + 128 * i, o_tm = C::O_COL + 128 * i;
             const uint32_t b_q = q_full(i), b_s = s_full(i, 0), b_p = p_full(i, 0), b_od = o_done(i), b_oe = o_empty(i);
-            int slot = 0;
-            uint32_t slot_ph = 0, q_ph = 0, p_ph = 0, o_ph = 1;
-            auto next_slot = [&]() {
-                if (++slot == NS) slot = 0, slot_ph ^= 1u;
-            };
+            const uint32_t b_kf = kv_full(0, 0), b_ke = kv_empty(0, 0), b_vf = kv_full(1, 0), b_ve = kv_empty(1, 0);
+            uint32_t nk = 0, nv = 0;        // tiles of keys and of values so far: slot n % 4, lap n / 4
+            uint32_t ns = 0, np = 0;        // S and P of this row tile so far: buffer n % 2
+            uint32_t q_ph = 0, o_ph = 1;
             auto ready = [&](uint32_t bar, uint32_t parity) {
                 if (!ptx::mbar_try_wait(bar, parity)) wait(bar, parity, DEVICE_TIMEOUT_MMA);
             };
-            auto qk = [&](int h, int k_slot) {      // S_i = Q_i K^T of 64 tokens
-                const uint32_t b = k_lo + k_slot * (C::TILE >> 4) + h * (64 * 128 >> 4);
+            auto qk = [&]() {               // S = Q K^T of the next tile
+                const uint32_t slot = nk & (NS - 1), h = ns & 1u;
+                ready(b_kf + 8 * slot, nk / NS & 1u);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                const uint32_t b = k_lo + slot * (C::KV_TILE >> 4), d = s_tm + TN * h;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const uint32_t off = (k >> 2) * (C::HALF >> 4) + (k & 3) * 2;
-                    ptx::mma_f16_ss(s_tm + 64 * h, q_lo + off, ptx::kSdescHi, b + off, ptx::kSdescHi, id_s, k > 0);
-                }
+                for (int k = 0; k < KS; ++k)
+                    ptx::mma_f16_ss(d, q_lo + (k >> 2) * (C::Q_HALF >> 4) + (k & 3) * 2, ptx::kSdescHi,
+                                    b + (k >> 2) * (C::KV_HALF >> 4) + (k & 3) * 2, ptx::kSdescHi, id_s, k > 0);
                 ptx::mma_commit(b_s + 8 * h);
-                if (h == 1) ptx::mma_commit(kv_empty(k_slot));
+                ptx::mma_commit(b_ke + 8 * slot);
+                ++nk, ++ns;
             };
             for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
                 const int tiles = tile_end() - tile_begin();
                 if (i == 1 && item_rows() <= 128) {
                     // no rows in this tile: only hand the slots on
-                    for (int t = 0; t < 2 * tiles && ok; ++t) {
-                        ready(kv_full(slot), slot_ph);
-                        ptx::mbar_arrive(kv_empty(slot));
-                        next_slot();
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        ready(b_kf + 8 * (nk & (NS - 1)), nk / NS & 1u);
+                        ptx::mbar_arrive(b_ke + 8 * (nk & (NS - 1)));
+                        ready(b_vf + 8 * (nv & (NS - 1)), nv / NS & 1u);
+                        ptx::mbar_arrive(b_ve + 8 * (nv & (NS - 1)));
+                        ++nk, ++nv;
                     }
                     continue;
                 }
                 ready(b_q, q_ph);
                 q_ph ^= 1u;
-                ready(kv_full(slot), slot_ph);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                qk(0, slot);
-                qk(1, slot);
-                next_slot();
+                if (ok) qk();
+                if (ok && tiles > 1) qk();
                 ready(b_oe, o_ph);
                 o_ph ^= 1u;
                 for (int t = 0; t < tiles && ok; ++t) {
-                    const int v_slot = slot;
-                    ready(kv_full(v_slot), slot_ph);
-                    next_slot();
-                    const bool more = t + 1 < tiles;
-                    if (more) ready(kv_full(slot), slot_ph);
+                    const uint32_t slot = nv & (NS - 1), h = np & 1u;
+                    ready(b_vf + 8 * slot, nv / NS & 1u);
+                    ready(b_p + 8 * h, np >> 1 & 1u);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t b = v_lo + slot * (C::KV_TILE >> 4), a = s_tm + TN * h;   // O (+)= P V
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ready(b_p + 8 * h, p_ph);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const uint32_t b = v_lo + v_slot * (C::TILE >> 4) + h * (64 * 128 >> 4);   // O_i (+)= P_i V
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_f16_ts(o_tm, s_tm + 64 * h + 8 * k, b + k * (2048 >> 4), ptx::kSdescHi, id_o,
-                                            k > 0 || h > 0 || t > 0);
-                        ptx::mma_commit(b_od);
-                        if (h == 1) ptx::mma_commit(kv_empty(v_slot));
-                        if (more) qk(h, slot);
-                    }
-                    p_ph ^= 1u;
-                    if (more) next_slot();
+                    for (int k = 0; k < TN / 16; ++k)
+                        ptx::mma_f16_ts(o_tm, a + 8 * k, b + k * (2048 >> 4), ptx::kSdescHi, id_o, k > 0 || t > 0);
+                    ptx::mma_commit(b_od);
+                    ptx::mma_commit(b_ve + 8 * slot);
+                    ++nv, ++np;
+                    if (t + 2 < tiles) qk();
                 }
             }
             // given up (either warp): the MMAs in flight end before tensor memory is freed
@@ -269,26 +282,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         ptx::regs_dec<kRegsUnpack>();
         // ------------------------------------------------------------ unpack
         const int which = (warp - 8) >> 2;         // keys, values
-        const int tt = threadIdx.x & 127;          // the token of the tile
-        const int pg = tt >> p.c.p_shift, place = tt & (p.c.P - 1);
-        const int codes_at = pg * p.c.block_bytes + kv4_codes_at(p.c, which, place);
-        const int pairs_at = pg * p.c.block_bytes + kv4_pairs_at(p.c, which, place);
-        const int vpairs_at = pg * p.c.block_bytes + kv4_pairs_at(p.c, 1, place);
-        int s = 0, slot = which;
-        uint32_t ph = 0, slot_ph = 0;
+        const int tt = (threadIdx.x & 127) >> 1;   // the token of the tile
+        const int side = threadIdx.x & 1;          // which half of its d
+        const int vp = min(p.c.P, TN), place = tt & (vp - 1);
+        const int block_at = tt / vp * (vp * (D + 2 * pair_row));
+        const int codes_at = block_at + (which * vp + place) * (D / 2) + side * (D / 4);
+        const int vpairs_at = block_at + vp * D + (vp + place) * pair_row;
+        const int pairs_at = vpairs_at - (1 - which) * vp * pair_row;
+        const uint32_t off_kv = which ? C::OFF_V : C::OFF_K;
+        int s = 0;
+        uint32_t ph = 0, n = 0;                    // n: tiles so far, slot n % 4
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows(), te = tile_end();
             const int pos0 = w.s.L - w.s.n + (int)((int64_t)w.rt * R / p.group);
             const int pos1 = w.s.L - w.s.n + (int)(((int64_t)w.rt * R + rows - 1) / p.group);
             const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
             const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
-            for (int t = tile_begin(); t < te; ++t) {
+            for (int t = tile_begin(); t < te; ++t, ++n) {
                 const int tok = t * TN;
+                const uint32_t slot = n & (NS - 1);
                 ok = __all_sync(0xffffffffu, wait(raw_full(s), ph, DEVICE_TIMEOUT_TRANSFORM));
-                ok = __all_sync(0xffffffffu, wait(kv_empty(slot), slot_ph ^ 1u, DEVICE_TIMEOUT_TRANSFORM));
+                ok = __all_sync(0xffffffffu, wait(kv_empty(which, slot), (n / NS & 1u) ^ 1u, DEVICE_TIMEOUT_TRANSFORM));
                 if (ok) {
                     const uint8_t* st = smem + C::OFF_RAW + s * stage_bytes;
-                    uint8_t* dst = smem + C::OFF_KV + slot * C::TILE + tt * 128;
+                    uint8_t* dst = smem + off_kv + slot * C::KV_TILE + tt * 128;
                     bool clear = false, spoil = false;
                     if (tok < all_lo || tok + TN > all_hi) {
                         // 0 * NaN must not reach rows that do not see a token: values
@@ -302,11 +319,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         spoil = which == 0 && spoil;
                     }
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        // 32 codes; the rotation spreads a quarter warp over the banks
-                        const int ch = (i + (lane >> (D == 128 ? 1 : 2))) & (D / 32 - 1);
-                        const uint4 cw = *reinterpret_cast<const uint4*>(st + codes_at + ch * 16);
-                        uint32_t pair = *reinterpret_cast<const uint32_t*>(st + pairs_at + ((ch * 32) >> p.c.g_shift) * 4);
+                    for (int c = 0; c < D / 64; ++c) {
+                        // 32 codes; the order spreads a quarter warp's reads and writes over the banks
+                        const int part = D == 128 ? c ^ (tt >> 1 & 1) ^ side : 0;
+                        const uint4 cw = *reinterpret_cast<const uint4*>(st + codes_at + part * 16);
+                        const int d0 = side * (D / 2) + part * 32;
+                        uint32_t pair = *reinterpret_cast<const uint32_t*>(st + pairs_at + (d0 >> p.c.g_shift) * 4);
                         if (clear) pair = 0u;
                         if (spoil) pair = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
                         const uint32_t s2 = __byte_perm(pair, 0, 0x1010), l2 = __byte_perm(pair, 0, 0x3232);
@@ -314,8 +332,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t x = words[j], y = x >> 8;
-                            const int chunk = ch * 4 + j;
-                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * C::HALF + (((chunk & 7) ^ (tt & 7)) << 4)) =
+                            const int chunk = (d0 >> 3) + j;
+                            *reinterpret_cast<uint4*>(dst + (chunk >> 3) * C::KV_HALF + (((chunk & 7) ^ (tt & 7)) << 4)) =
                                 make_uint4(fma2<BF16>(Codes<BF16>::low(x), s2, l2), fma2<BF16>(Codes<BF16>::high(x), s2, l2),
                                            fma2<BF16>(Codes<BF16>::low(y), s2, l2), fma2<BF16>(Codes<BF16>::high(y), s2, l2));
                         }
@@ -324,11 +342,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 }
                 __syncwarp();
                 if (ok && lane == 0) {
-                    ptx::mbar_arrive(kv_full(slot));
+                    ptx::mbar_arrive(kv_full(which, slot));
                     ptx::mbar_arrive(raw_empty(s));
                 }
-                slot += 2;                          // the other warpgroup fills every other slot
-                if (slot >= NS) slot -= NS, slot_ph ^= 1u;
                 if (++s == RS) s = 0, ph ^= 1u;
             }
         }
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const uint64_t sl = f2(sl2, sl2);
-        uint32_t s_ph = 0, od_ph = 1;                // od_ph: parity of the last PV that this tile's P has started
+        uint32_t n = 0;                              // tiles of this row tile so far: S buffer n % 2
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows();
             const bool idle = 128 * i >= rows;       // no rows in this tile
@@ -358,13 +374,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int lo = p.window > 0 ? pos + 1 - p.window : 0;
             if (!idle) {
                 const uint16_t* src = static_cast<const uint16_t*>(p.q) + tq * p.q_stride + (int64_t)head * D;
-                uint8_t* dst = smem + C::OFF_Q + i * C::TILE + r1 * 128;
+                uint8_t* dst = smem + C::OFF_Q + i * C::Q_TILE + r1 * 128;
 #pragma unroll 4
                 for (int ch = 0; ch < D / 8; ++ch) {
                     uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
                     if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
                     v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::HALF + (((ch & 7) ^ (r1 & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::Q_HALF + (((ch & 7) ^ (r1 & 7)) << 4)) =
                         make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 }
@@ -375,20 +391,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int tb = tile_begin(), te = tile_end();
             float m = -INFINITY, l = 0.f;
             if (!idle) {
-                const int first = tb * TN, end = te * TN;
 #pragma unroll 1
-                for (int tok = first; tok < end; tok += 64) {
-                    const int hf = tok >> 6 & 1;
-                    const uint32_t s_half = s_tm + 64 * hf;
-                    if (ok) ok = __all_sync(0xffffffffu, wait(s_full(i, hf), s_ph, DEVICE_TIMEOUT_EPILOGUE));
+                for (int t = tb; t < te; ++t, ++n) {
+                    const uint32_t s_now = s_tm + TN * (n & 1u);
+                    if (ok) ok = __all_sync(0xffffffffu, wait(s_full(i, n & 1u), n >> 1 & 1u, DEVICE_TIMEOUT_EPILOGUE));
                     if (!ok) break;
-                    s_ph ^= (uint32_t)hf;            // after the second half
                     ptx::tc_fence_after();
-                    uint32_t v[2][32];
-                    ptx::tmem_ld32(s_half, v[0]);
-                    ptx::tmem_ld32(s_half + 32, v[1]);
-                    const int h = hi - tok, b = lo - tok;      // this row sees columns [b, h)
-                    const bool masked = __any_sync(0xffffffffu, b > 0 || h < 64);
+                    uint32_t v[64];
+                    ptx::tmem_ld64(s_now, v);
+                    const int h = hi - t * TN, b = lo - t * TN;      // this row sees columns [b, h)
+                    const bool masked = __any_sync(0xffffffffu, b > 0 || h < TN);
                     ptx::tmem_wait_ld();
                     if (masked) {
                         // the few tiles on a mask's edge: bit k of `see` is column k
@@ -396,50 +408,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         const uint64_t from = b <= 0 ? ~0ull : b >= 64 ? 0ull : ~((1ull << b) - 1);
                         const uint32_t see[2] = {(uint32_t)(below & from), (uint32_t)((below & from) >> 32)};
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(see[c] >> k & 1u)) v[c][k] = 0xFF800000u;
+                        for (int k = 0; k < 64; ++k)
+                            if (!(see[k >> 5] >> (k & 31) & 1u)) v[k] = 0xFF800000u;
                     }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            mx[c] = max3(mx[c], __uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1]));
-                            mx[2 + c] = max3(mx[2 + c], __uint_as_float(v[c][k + 2]), __uint_as_float(v[c][k + 3]));
-                        }
-                    const float top = sl2 * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                    const bool grow = top > m + 8.f;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float m1 = grow ? top : m, f = grow ? part_weight(m, m1) : 1.f;
-                        m = m1;
-                        l *= f;
-                        if (tok > first) {
-                            // O is scaled between products: the last one has to have ended
-                            ok = __all_sync(0xffffffffu, wait(o_done(i), od_ph, DEVICE_TIMEOUT_EPILOGUE));
-                            if (!ok) break;
-                            ptx::tc_fence_after();
+                    // Under the maximum so far a sum below 2^14 shows that no probability
+                    // passed 2^14, which both types hold; else the tile is done again under
+                    // the new maximum.  Rows that have seen nothing have none yet.
+                    uint32_t o[32];
+                    float sum;
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t x[16];
-                                ptx::tmem_ld16(o_tm + c, x);
-                                ptx::tmem_wait_ld();
+                    for (bool again = __any_sync(0xffffffffu, m == -INFINITY);;) {
+                        if (again) {
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-                                ptx::tmem_st16(o_tm + c, x);
+                            for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    mx[c] = max3(mx[c], __uint_as_float(v[k + 2 * c]), __uint_as_float(v[k + 2 * c + 1]));
+                            const float top = sl2 * max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                            const bool grow = top > m + 8.f;
+                            const float m1 = grow ? top : m, f = grow ? part_weight(m, m1) : 1.f;
+                            m = m1;
+                            l *= f;
+                            if (t > tb && __any_sync(0xffffffffu, grow)) {
+                                // O is scaled between products: the last one has to have ended
+                                ok = __all_sync(0xffffffffu, wait(o_done(i), (n - 1) & 1u, DEVICE_TIMEOUT_EPILOGUE));
+                                if (!ok) break;
+                                ptx::tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t x[16];
+                                    ptx::tmem_ld16(o_tm + c, x);
+                                    ptx::tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                                    ptx::tmem_st16(o_tm + c, x);
+                                }
                             }
                         }
-                    }
-                    const float mm = m == -INFINITY ? 0.f : m;
-                    const uint64_t nm = f2(-mm, -mm);
-                    uint64_t la = 0, lb = 0;
+                        const float mm = m == -INFINITY ? 0.f : m;
+                        const uint64_t nm = f2(-mm, -mm);
+                        uint64_t la = 0, lb = 0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t o[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            float2 e = un2(fma_f2(f2(__uint_as_float(v[c][2 * k]), __uint_as_float(v[c][2 * k + 1])), sl, nm));
+                        for (int k = 0; k < 32; ++k) {
+                            float2 e = un2(fma_f2(f2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl, nm));
                             e.x = ex2(e.x), e.y = ex2(e.y);
                             if (k & 1)
                                 lb = add_f2(lb, f2(e.x, e.y));
@@ -447,17 +459,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                                 la = add_f2(la, f2(e.x, e.y));
                             o[k] = pack2<BF16>(e.x, e.y);
                         }
-                        ptx::tmem_st16(s_half + 16 * c, o);
+                        const float2 ls = un2(add_f2(la, lb));
+                        sum = ls.x + ls.y;
+                        if (again || !__any_sync(0xffffffffu, !(sum < 16384.f))) break;
+                        again = true;
                     }
-                    const float2 ls = un2(add_f2(la, lb));
-                    l += ls.x + ls.y;
+                    if (!ok) break;
+                    l += sum;
+                    ptx::tmem_st32(s_now, o);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(p_full(i, hf));
-                    od_ph ^= 1u;
+                    if (lane == 0) ptx::mbar_arrive(p_full(i, n & 1u));
                 }
-                if (ok) ok = __all_sync(0xffffffffu, wait(o_done(i), od_ph, DEVICE_TIMEOUT_EPILOGUE));
+                if (ok) ok = __all_sync(0xffffffffu, wait(o_done(i), (n - 1) & 1u, DEVICE_TIMEOUT_EPILOGUE));
                 ptx::tc_fence_after();
             }
             // ---- the item's result, or this block's part of it
