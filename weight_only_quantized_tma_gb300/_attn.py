@@ -5,14 +5,11 @@ and attention over it.  Argument checks and marshalling only; the work is in lib
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
 from . import _lib
-from ._lib import _check, _i32, _i64, _ptr, _stream, _sz, lib
-
-
+from ._lib import WQError, _i32, _i64, _sz, lib
 
 
 class Kv4Layout(ctypes.Structure):
@@ -21,6 +18,22 @@ class Kv4Layout(ctypes.Structure):
 
 
 _DTYPES = {torch.float16: _lib.WQ_F16, torch.bfloat16: _lib.WQ_BF16}
+_fns: dict = {}
+_layouts: dict = {}
+
+
+def _call(name: str, *args) -> None:
+    """The library function `name`; a decode step's calls are short, so it is looked up once."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    status = fn(*args)
+    if status != 0:
+        raise WQError(status, name)
+
+
+def _stream(device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dtype(dtype: torch.dtype) -> int:
@@ -31,49 +44,55 @@ def _dtype(dtype: torch.dtype) -> int:
 
 
 def _rows(t, name, dtype=None, shape=None, device=None):
-    """A [T, heads, D] tensor whose heads of a token are contiguous (any stride from token to token)."""
+    """A [T, heads, D] tensor whose heads of a token are contiguous (any stride from token to token);
+    returns the elements from token to token (a single token's stride says nothing)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    got = t.shape
+    if len(got) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(got)}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape is not None and got != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    _, h, d = t.shape
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+    n, h, d = got
+    step, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-
-
-def _step(t):
-    """Elements from token to token (a single token's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return step if n > 1 else h * d
 
 
 def _flat(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _layout(pages, head_dim: int, group: int, page_size: int, dtype: torch.dtype) -> Kv4Layout:
-    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype != torch.uint8 or pages.dim() != 3:
+def _layout(pages, head_dim: int, group: int, page_size: int, dtype: torch.dtype):
+    """(the layout, a reference to pass); pages [num_pages, kv_heads, block_bytes] gives the rest."""
+    if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype is not torch.uint8 or pages.dim() != 3:
         raise ValueError("pages must be a uint8 CUDA tensor [num_pages, kv_heads, block_bytes]")
     if not pages.is_contiguous():
         raise ValueError("pages must be contiguous")
-    n, heads, block = pages.shape
-    if group <= 0 or block != page_size * (head_dim + 8 * (head_dim // group)):
-        raise ValueError(f"pages: a block of {page_size} tokens with head_dim {head_dim} in groups of {group} has "
-                         f"{page_size * (head_dim + 8 * (head_dim // max(1, group)))} bytes, got {block}")
-    return Kv4Layout(n, heads, head_dim, group, page_size, _dtype(dtype))
+    key = (pages.shape, head_dim, group, page_size, dtype)
+    got = _layouts.get(key)
+    if got is None:
+        n, heads, block = pages.shape
+        if group <= 0 or block != page_size * (head_dim + 8 * (head_dim // group)):
+            raise ValueError(f"pages: a block of {page_size} tokens with head_dim {head_dim} in groups of {group} has "
+                             f"{page_size * (head_dim + 8 * (head_dim // max(1, group)))} bytes, got {block}")
+        lay = Kv4Layout(n, heads, head_dim, group, page_size, _dtype(dtype))
+        if len(_layouts) > 256:
+            _layouts.clear()
+        got = _layouts[key] = (lay, ctypes.byref(lay))
+    return got
 
 
 # ------------------------------------------------------------------ queries and keys
@@ -85,32 +104,35 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, c
 
     positions int64 [T]; cos_sin fp32 [max_pos, rot]: a row's rot / 2 cosines, then its sines.  q and k may be
     slices of one packed projection; q_out / k_out may be q / k themselves."""
-    _rows(q, "q")
+    q_step = _rows(q, "q")
     T, Hq, D = q.shape
-    dt, dev = _dtype(q.dtype), q.device
-    _rows(k, "k", q.dtype, device=dev)
+    dtype, dev = q.dtype, q.device
+    dt = _dtype(dtype)
+    k_step = _rows(k, "k", dtype, None, dev)
+    Hkv = k.shape[1]
     if k.shape[0] != T or k.shape[2] != D:
         raise ValueError(f"k must be [{T}, heads, {D}], got {tuple(k.shape)}")
-    Hkv = k.shape[1]
     _flat(positions, "positions", torch.int64, (T,), dev)
     if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_pos, rot]")
-    _flat(cos_sin, "cos_sin", torch.float32, cos_sin.shape, dev)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _flat(w, name, q.dtype, (D,), dev)
+    most, rot = cos_sin.shape
+    _flat(cos_sin, "cos_sin", torch.float32, (most, rot), dev)
+    if q_weight is not None:
+        _flat(q_weight, "q_weight", dtype, (D,), dev)
+    if k_weight is not None:
+        _flat(k_weight, "k_weight", dtype, (D,), dev)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        q_out, qo_step = torch.empty((T, Hq, D), dtype=dtype, device=dev), Hq * D
     else:
-        _rows(q_out, "q_out", q.dtype, q.shape, dev)
+        qo_step = _rows(q_out, "q_out", dtype, q.shape, dev)
     if k_out is None:
-        k_out = torch.empty((T, Hkv, D), dtype=q.dtype, device=dev)
+        k_out, ko_step = torch.empty((T, Hkv, D), dtype=dtype, device=dev), Hkv * D
     else:
-        _rows(k_out, "k_out", q.dtype, k.shape, dev)
-    _check(lib().wq_qk_norm_rope(_ptr(q), _step(q), _ptr(k), _step(k), dt, T, Hq, Hkv, D, _ptr(q_weight),
-                                 _ptr(k_weight), eps, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
-                                 cos_sin.shape[1], int(interleaved), _ptr(q_out), _step(q_out), _ptr(k_out),
-                                 _step(k_out), _stream(q)), "wq_qk_norm_rope")
+        ko_step = _rows(k_out, "k_out", dtype, k.shape, dev)
+    _call("wq_qk_norm_rope", q.data_ptr(), q_step, k.data_ptr(), k_step, dt, T, Hq, Hkv, D,
+          None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+          positions.data_ptr(), cos_sin.data_ptr(), most, rot, int(interleaved), q_out.data_ptr(), qo_step,
+          k_out.data_ptr(), ko_step, _stream(dev))
     return q_out, k_out
 
 
@@ -119,8 +141,7 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, c
 def wq_kv4_page_bytes(kv_heads: int, head_dim: int, group: int, page_size: int) -> int:
     """Bytes of one page of the cache, all heads."""
     b = _sz(0)
-    _check(lib().wq_kv4_page_bytes(ctypes.byref(Kv4Layout(0, kv_heads, head_dim, group, page_size, 0)),
-                                   ctypes.byref(b)), "wq_kv4_page_bytes")
+    _call("wq_kv4_page_bytes", ctypes.byref(Kv4Layout(0, kv_heads, head_dim, group, page_size, 0)), ctypes.byref(b))
     return b.value
 
 
@@ -133,59 +154,68 @@ def wq_kv4_pages(num_pages: int, kv_heads: int, head_dim: int, group: int, page_
 def wq_kv4_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor, group: int,
                  page_size: int) -> None:
     """Quantises k, v [T, kv_heads, D] into slots (int64 [T]: page * page_size + place; negative: skip)."""
-    _rows(k, "k")
-    T, H, D = k.shape
-    _rows(v, "v", k.dtype, k.shape, k.device)
-    _flat(slots, "slots", torch.int64, (T,), k.device)
-    lay = _layout(pages, D, group, page_size, k.dtype)
-    if lay.kv_heads != H or pages.device != k.device:
-        raise ValueError(f"pages must hold {H} heads on {k.device}")
-    _check(lib().wq_kv4_write(_ptr(k), _step(k), _ptr(v), _step(v), _ptr(slots), T, ctypes.byref(lay), _ptr(pages),
-                              _stream(k)), "wq_kv4_write")
+    k_step = _rows(k, "k")
+    T, H, D = shape = k.shape
+    dev = k.device
+    v_step = _rows(v, "v", k.dtype, shape, dev)
+    _flat(slots, "slots", torch.int64, (T,), dev)
+    lay, ref = _layout(pages, D, group, page_size, k.dtype)
+    if lay.kv_heads != H or pages.device != dev:
+        raise ValueError(f"pages must hold {H} heads on {dev}")
+    _call("wq_kv4_write", k.data_ptr(), k_step, v.data_ptr(), v_step, slots.data_ptr(), T, ref, pages.data_ptr(),
+          _stream(dev))
 
 
 def wq_kv4_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, group: int, page_size: int,
                 dtype: torch.dtype, k: torch.Tensor = None, v: torch.Tensor = None):
     """The cache's values in slots (int64 [T]; negative: zeros) -> (k, v) [T, kv_heads, head_dim]."""
-    lay = _layout(pages, head_dim, group, page_size, dtype)
+    lay, ref = _layout(pages, head_dim, group, page_size, dtype)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be int64 [T]")
     dev = pages.device
-    _flat(slots, "slots", torch.int64, slots.shape, dev)
-    shape = (slots.shape[0], lay.kv_heads, head_dim)
+    T = slots.shape[0]
+    _flat(slots, "slots", torch.int64, (T,), dev)
+    shape = (T, lay.kv_heads, head_dim)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
+        k, k_step = torch.empty(shape, dtype=dtype, device=dev), shape[1] * head_dim
     else:
-        _rows(k, "k", dtype, shape, dev)
+        k_step = _rows(k, "k", dtype, shape, dev)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=dev)
+        v, v_step = torch.empty(shape, dtype=dtype, device=dev), shape[1] * head_dim
     else:
-        _rows(v, "v", dtype, shape, dev)
-    _check(lib().wq_kv4_read(_ptr(pages), ctypes.byref(lay), _ptr(slots), shape[0], _ptr(k), _step(k), _ptr(v),
-                             _step(v), _stream(pages)), "wq_kv4_read")
+        v_step = _rows(v, "v", dtype, shape, dev)
+    _call("wq_kv4_read", pages.data_ptr(), ref, slots.data_ptr(), T, k.data_ptr(), k_step, v.data_ptr(), v_step,
+          _stream(dev))
     return k, v
 
 
 # ------------------------------------------------------------------ attention
 
+_ws_need: dict = {}
 _ws_cache: dict = {}
 
 
-def attn_kv4_workspace(lay: Kv4Layout, q_heads: int, max_q: int, device):
+def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
     """(tensor or None, bytes): a zero-filled workspace shared by calls on one stream.
 
     A call that is being captured into a graph gets its own, which the graph keeps and clears."""
-    need = _sz(0)
-    _check(lib().wq_attn_kv4_workspace_bytes(ctypes.byref(lay), q_heads, max_q, ctypes.byref(need)),
-           "wq_attn_kv4_workspace_bytes")
-    if need.value == 0:
+    lay, ref = layout
+    key = (device.index, lay.kv_heads, lay.head_dim, lay.group, lay.dtype, q_heads, max_q)
+    need = _ws_need.get(key)
+    if need is None:
+        b = _sz(0)
+        _call("wq_attn_kv4_workspace_bytes", ref, q_heads, max_q, ctypes.byref(b))
+        if len(_ws_need) > 4096:
+            _ws_need.clear()
+        need = _ws_need[key] = b.value
+    if need == 0:
         return None, 0
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(need.value, dtype=torch.uint8, device=device), need.value
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+        return torch.zeros(need, dtype=torch.uint8, device=device), need
+    key = (device.index, stream)
     buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < need.value:
-        buf = torch.zeros(need.value, dtype=torch.uint8, device=device)
+    if buf is None or buf.numel() < need:
+        buf = torch.zeros(need, dtype=torch.uint8, device=device)
         _ws_cache[key] = buf
     return buf, buf.numel()
 
@@ -199,33 +229,34 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
     block_table int32 [B, pages of a sequence], kv_lens int32 [B] (the new tokens included); cu_q int32 [B + 1]
     gives each sequence's queries (None: one each), max_q their largest number.  scale defaults to
     1 / sqrt(D); window > 0 keeps the last `window` tokens of each query; lse: fp32 [T, q_heads] to fill."""
-    _rows(q, "q")
-    T, Hq, D = q.shape
-    dev = q.device
-    lay = _layout(pages, D, group, page_size, q.dtype)
+    q_step = _rows(q, "q")
+    T, Hq, D = shape = q.shape
+    dtype, dev = q.dtype, q.device
+    layout = _layout(pages, D, group, page_size, dtype)
     if pages.device != dev:
         raise ValueError(f"pages must be on {dev}")
     if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1:
         raise ValueError("kv_lens must be int32 [B]")
     B = kv_lens.shape[0]
     _flat(kv_lens, "kv_lens", torch.int32, (B,), dev)
-    if (not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, pages]")
     _flat(block_table, "block_table", torch.int32, block_table.shape, dev)
     if cu_q is not None:
         _flat(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        out, out_step = torch.empty(shape, dtype=dtype, device=dev), Hq * D
     else:
-        _rows(out, "out", q.dtype, q.shape, dev)
+        out_step = _rows(out, "out", dtype, shape, dev)
     if lse is not None:
         _flat(lse, "lse", torch.float32, (T, Hq), dev)
+    stream = _stream(dev)
     if ws is None:
-        ws, ws_bytes = attn_kv4_workspace(lay, Hq, max_q, dev)
+        ws, ws_bytes = attn_kv4_workspace(layout, Hq, max_q, dev, stream)
     else:
         ws_bytes = ws.numel() * ws.element_size()
-    _check(lib().wq_attn_kv4(_ptr(q), _step(q), Hq, _ptr(cu_q), B, T, max_q, _ptr(pages), ctypes.byref(lay),
-                             _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
-                             1.0 / math.sqrt(D) if scale is None else scale, int(causal), window, _ptr(out),
-                             _step(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(q)), "wq_attn_kv4")
+    _call("wq_attn_kv4", q.data_ptr(), q_step, Hq, None if cu_q is None else cu_q.data_ptr(), B, T, max_q,
+          pages.data_ptr(), layout[1], block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(),
+          D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), out_step,
+          None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, stream)
     return out

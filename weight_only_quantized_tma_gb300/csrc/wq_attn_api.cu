@@ -64,8 +64,7 @@ wq_status rows_call(const void* k, int64_t k_stride, const void* v, int64_t v_st
     if (T == 0) return WQ_OK;
     if (!k || !v || !slots || (!pages && p.c.num_pages > 0)) return WQ_ERR_NULL;
     const int64_t row = (int64_t)p.c.heads * p.c.D;
-    // a token's rows times T must fit the grid of 256-thread blocks
-    if (!stride_ok(k_stride, row, 8) || !stride_ok(v_stride, row, 8) || T * row / 8 * 2 / 256 >= kMaxTokens)
+    if (!stride_ok(k_stride, row, 8) || !stride_ok(v_stride, row, 8) || T * p.c.heads * 2 >= kMaxTokens - 4096)
         return WQ_ERR_SHAPE;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pages, 16) || !aligned(slots, 8)) return WQ_ERR_MISALIGNED;
     DeviceState d{};
@@ -77,6 +76,7 @@ wq_status rows_call(const void* k, int64_t k_stride, const void* v, int64_t v_st
     p.slots = slots;
     p.T = T;
     p.status = d.status;
+    p.div_heads = make_fastdiv((uint32_t)p.c.heads, (uint32_t)(T * p.c.heads + 4096));
     const bool bf16 = layout->dtype == WQ_BF16;
     return finish_launch(write ? launch_kv4_write(p, bf16, d.sms, (cudaStream_t)stream)
                                : launch_kv4_read(p, bf16, d.sms, (cudaStream_t)stream));
@@ -99,7 +99,7 @@ wq_status wq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
     if (!q || !k || !positions || !cos_sin || !q_out || !k_out) return WQ_ERR_NULL;
     const int64_t rq = (int64_t)Hq * D, rk = (int64_t)Hkv * D;
     if (!stride_ok(q_stride, rq, 4) || !stride_ok(k_stride, rk, 4) || !stride_ok(q_out_stride, rq, 4) ||
-        !stride_ok(k_out_stride, rk, 4) || T * (Hq + Hkv) >= kMaxTokens * 8)
+        !stride_ok(k_out_stride, rk, 4) || T * (Hq + Hkv) >= kMaxTokens - 4096)
         return WQ_ERR_SHAPE;
     if (!aligned(q, 8) || !aligned(k, 8) || !aligned(q_out, 8) || !aligned(k_out, 8) || !aligned(q_weight, 8) ||
         !aligned(k_weight, 8) || !aligned(positions, 8) || !aligned(cos_sin, 16))

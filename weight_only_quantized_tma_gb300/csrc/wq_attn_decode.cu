@@ -33,17 +33,7 @@ struct Launcher {
     static cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
         const int per = blocks_per_sm(p.c);
         if (per == 0) return cudaErrorInvalidConfiguration;
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(sms * per));
-        cfg.blockDim = dim3(160);
-        cfg.dynamicSmemBytes = smem(p.c);
-        cfg.stream = st;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, attn_decode_kernel<BF16, D, NT>, p, stage_bytes(p.c));
+        return launch_pdl(attn_decode_kernel<BF16, D, NT>, (unsigned)(sms * per), 160, smem(p.c), st, p, stage_bytes(p.c));
     }
     static size_t ws_bytes(const Kv4View& c, int sms) {
         return kAttnCounterBytes + (size_t)sms * blocks_per_sm(c) * 2 * attn_slot_floats(C::R, D) * 4;

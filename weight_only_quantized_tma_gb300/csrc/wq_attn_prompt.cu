@@ -12,17 +12,8 @@ cudaError_t launch(const AttnParams& p, int sms, cudaStream_t st) {
     static_assert(most <= 227 * 1024, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<BF16, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)sms);
-    cfg.blockDim = dim3(kPromptThreads);
-    cfg.dynamicSmemBytes = 1024 + C::OFF_RAW + C::RAW_STAGES * stage;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<BF16, D>, p, stage);
+    return launch_pdl(attn_prompt_kernel<BF16, D>, (unsigned)sms, kPromptThreads, 1024 + C::OFF_RAW + C::RAW_STAGES * stage, st,
+                      p, stage);
 }
 
 }  // namespace

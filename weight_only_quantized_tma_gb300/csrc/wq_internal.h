@@ -256,6 +256,8 @@ struct RopeParams {
     int Hq, Hkv, D, rot, interleaved;
     float eps;
     uint32_t* status;
+    int per;                 // heads of one group of lanes
+    FastDiv div_groups;      // groups of one token
 };
 cudaError_t launch_qk_norm_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st);   // wq_rope.cu
 
@@ -267,6 +269,7 @@ struct Kv4RowsParams {   // write and read
     const int64_t* slots;
     int64_t T;
     uint32_t* status;
+    FastDiv div_heads;
 };
 cudaError_t launch_kv4_write(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);   // wq_kv4.cu
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);
@@ -299,6 +302,24 @@ size_t attn_kv4_decode_ws(const Kv4View& c, bool bf16, int64_t rows, int sms);
 // Many rows (wq_attn_prompt.cu).
 cudaError_t launch_attn_kv4_prompt(const AttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t attn_kv4_prompt_ws(const Kv4View& c, int sms);
+
+// A launch whose prologue may overlap the end of the kernel before it on the stream; the
+// kernel waits (griddepcontrol.wait) before it touches memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                       const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 

@@ -19,13 +19,19 @@ __device__ __forceinline__ void load4(const uint16_t* p, float (&x)[4]) {
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
-template <bool BF16, int LPR>
+// One group of LPR lanes takes one token and `per` of its heads, U at a time: the U rows'
+// loads are all issued before the first is used, and the token's angles are read once for
+// all of them (with one row for each group, 8192 tokens of 64 heads took 73.7 us).
+template <bool BF16, int LPR, int U>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
     const int lane = threadIdx.x % LPR;
-    const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const uint32_t group = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+    const uint32_t tok = fastdiv(group, p.div_groups);
+    const int h_begin = (int)(group - tok * p.div_groups.d) * p.per;
     const int heads = p.Hq + p.Hkv;
-    const int64_t t = row / heads;
-    const int h = (int)(row - t * heads);
+    const int64_t t = tok;
     bool active = t < p.T && lane * 8 < p.D;
     int64_t pos = 0;
     if (t < p.T) {
@@ -35,85 +41,126 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
             active = false;
         }
     }
-    const bool is_q = h < p.Hq;
-    const int64_t in_at = is_q ? t * p.q_stride + (int64_t)h * p.D : t * p.k_stride + (int64_t)(h - p.Hq) * p.D;
-    const int64_t out_at =
-        is_q ? t * p.q_out_stride + (int64_t)h * p.D : t * p.k_out_stride + (int64_t)(h - p.Hq) * p.D;
-    const uint16_t* src = static_cast<const uint16_t*>(is_q ? p.q : p.k) + in_at;
-    uint16_t* dst = static_cast<uint16_t*>(is_q ? p.q_out : p.k_out) + out_at;
-    const uint16_t* w = static_cast<const uint16_t*>(is_q ? p.q_weight : p.k_weight);
     // the two chunks (in values)
     const int pairs = p.rot >> 3;               // lanes with rotated chunks
-    const bool turns = lane < pairs;
-    const int ca = turns ? 4 * lane : p.rot + 8 * (lane - pairs);
-    const int cb = turns ? ca + (p.rot >> 1) : ca + 4;
-    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (active) {
-        load4<BF16>(src + ca, a);
-        load4<BF16>(src + cb, b);
-    }
-    // every lane takes part in the exchange: rows with and without a weight share warps
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (w != nullptr && active) {
-        const float r = rsqrtf(sum / (float)p.D + p.eps);
-        float wa[4], wb[4];
-        load4<BF16>(w + ca, wa);
-        load4<BF16>(w + cb, wb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = a[i] * r * wa[i];
-            b[i] = b[i] * r * wb[i];
-        }
-    }
-    if (!active) return;
+    const bool turns = active && lane < pairs;
+    const int ca = lane < pairs ? 4 * lane : p.rot + 8 * (lane - pairs);
+    const int cb = lane < pairs ? ca + (p.rot >> 1) : ca + 4;
+    // cosines and sines of the chunks' pairs: (a[i], b[i]), or neighbours in a and in b
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
     if (turns) {
         const float* cs = p.cos_sin + pos * p.rot;
         const float* sn = cs + (p.rot >> 1);
         if (p.interleaved) {
             const float2 c0 = *reinterpret_cast<const float2*>(cs + ca / 2), c1 = *reinterpret_cast<const float2*>(cs + cb / 2);
             const float2 s0 = *reinterpret_cast<const float2*>(sn + ca / 2), s1 = *reinterpret_cast<const float2*>(sn + cb / 2);
-            const float x0 = a[0], x1 = a[2], y0 = b[0], y1 = b[2];
-            a[0] = x0 * c0.x - a[1] * s0.x, a[1] = a[1] * c0.x + x0 * s0.x;
-            a[2] = x1 * c0.y - a[3] * s0.y, a[3] = a[3] * c0.y + x1 * s0.y;
-            b[0] = y0 * c1.x - b[1] * s1.x, b[1] = b[1] * c1.x + y0 * s1.x;
-            b[2] = y1 * c1.y - b[3] * s1.y, b[3] = b[3] * c1.y + y1 * s1.y;
+            c[0] = c0.x, c[1] = c0.y, c[2] = c1.x, c[3] = c1.y;
+            s[0] = s0.x, s[1] = s0.y, s[2] = s1.x, s[3] = s1.y;
         } else {
-            const float4 c = *reinterpret_cast<const float4*>(cs + ca), s = *reinterpret_cast<const float4*>(sn + ca);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = a[i];
-                a[i] = x * cc[i] - b[i] * ss[i];
-                b[i] = b[i] * cc[i] + x * ss[i];
-            }
+            const float4 cv = *reinterpret_cast<const float4*>(cs + ca), sv = *reinterpret_cast<const float4*>(sn + ca);
+            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+            s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
         }
     }
-    *reinterpret_cast<uint2*>(dst + ca) = make_uint2(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]));
-    *reinterpret_cast<uint2*>(dst + cb) = make_uint2(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]));
+    const float inv_d = 1.0f / (float)p.D;
+    for (int h0 = h_begin; h0 < h_begin + p.per; h0 += U) {   // the same count for every lane
+        uint2 ra[U], rb[U];
+        bool live[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u;
+            live[u] = active && h < heads;
+            ra[u] = rb[u] = make_uint2(0u, 0u);
+            if (live[u]) {
+                const bool is_q = h < p.Hq;
+                const uint16_t* src = is_q ? static_cast<const uint16_t*>(p.q) + t * p.q_stride + (int64_t)h * p.D
+                                           : static_cast<const uint16_t*>(p.k) + t * p.k_stride + (int64_t)(h - p.Hq) * p.D;
+                ra[u] = *reinterpret_cast<const uint2*>(src + ca);
+                rb[u] = *reinterpret_cast<const uint2*>(src + cb);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u;
+            const bool is_q = h < p.Hq;
+            float a[4], b[4];
+            const float2 a0 = unpack2<BF16>(ra[u].x), a1 = unpack2<BF16>(ra[u].y);
+            const float2 b0 = unpack2<BF16>(rb[u].x), b1 = unpack2<BF16>(rb[u].y);
+            a[0] = a0.x, a[1] = a0.y, a[2] = a1.x, a[3] = a1.y;
+            b[0] = b0.x, b[1] = b0.y, b[2] = b1.x, b[3] = b1.y;
+            // every lane takes part in the exchange: rows with and without a weight share warps
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+            for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (!live[u]) continue;
+            const uint16_t* w = static_cast<const uint16_t*>(is_q ? p.q_weight : p.k_weight);
+            if (w != nullptr) {
+                const float r = rsqrtf(sum * inv_d + p.eps);
+                float wa[4], wb[4];
+                load4<BF16>(w + ca, wa);
+                load4<BF16>(w + cb, wb);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = a[i] * r * wa[i];
+                    b[i] = b[i] * r * wb[i];
+                }
+            }
+            if (turns) {
+                if (p.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = a[2 * i], y = b[2 * i];
+                        a[2 * i] = x * c[i] - a[2 * i + 1] * s[i];
+                        a[2 * i + 1] = a[2 * i + 1] * c[i] + x * s[i];
+                        b[2 * i] = y * c[2 + i] - b[2 * i + 1] * s[2 + i];
+                        b[2 * i + 1] = b[2 * i + 1] * c[2 + i] + y * s[2 + i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = a[i];
+                        a[i] = x * c[i] - b[i] * s[i];
+                        b[i] = b[i] * c[i] + x * s[i];
+                    }
+                }
+            }
+            uint16_t* dst = is_q ? static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride + (int64_t)h * p.D
+                                 : static_cast<uint16_t*>(p.k_out) + t * p.k_out_stride + (int64_t)(h - p.Hq) * p.D;
+            *reinterpret_cast<uint2*>(dst + ca) = make_uint2(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]));
+            *reinterpret_cast<uint2*>(dst + cb) = make_uint2(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]));
+        }
+    }
 }
 
-template <bool BF16>
-cudaError_t launch(const RopeParams& p, cudaStream_t st) {
-    const int64_t rows = p.T * (p.Hq + p.Hkv);
-    auto grid = [&](int lpr) { return (unsigned)((rows * lpr + 255) / 256); };
-    if (p.D <= 64)
-        qk_norm_rope_kernel<BF16, 8><<<grid(8), 256, 0, st>>>(p);
-    else if (p.D <= 128)
-        qk_norm_rope_kernel<BF16, 16><<<grid(16), 256, 0, st>>>(p);
-    else
-        qk_norm_rope_kernel<BF16, 32><<<grid(32), 256, 0, st>>>(p);
-    return cudaPeekAtLastError();
+template <bool BF16, int LPR, int U>
+cudaError_t launch_u(RopeParams p, int per, cudaStream_t st) {
+    const int heads = p.Hq + p.Hkv;
+    p.per = per;
+    const uint32_t groups = (uint32_t)((heads + per - 1) / per);
+    const int64_t all = p.T * groups;
+    p.div_groups = make_fastdiv(groups, (uint32_t)(all + 256));
+    return launch_pdl(qk_norm_rope_kernel<BF16, LPR, U>, (unsigned)((all * LPR + 255) / 256), 256, 0, st, p);
+}
+
+template <bool BF16, int LPR>
+cudaError_t launch(const RopeParams& p, int sms, cudaStream_t st) {
+    // As many heads for each group as leave two full blocks for each SM: 8 read the angles
+    // least often, 1 spreads a decode step's few rows widest.
+    const int64_t want = (int64_t)sms * 2 * (256 / LPR);
+    const int heads = p.Hq + p.Hkv;
+    if (p.T * ((heads + 7) / 8) >= want) return launch_u<BF16, LPR, 4>(p, 8, st);
+    if (p.T * ((heads + 3) / 4) >= want) return launch_u<BF16, LPR, 4>(p, 4, st);
+    return launch_u<BF16, LPR, 1>(p, 1, st);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st) {
-    (void)sms;
-    return bf16 ? launch<true>(p, st) : launch<false>(p, st);
+    if (p.D <= 64) return bf16 ? launch<true, 8>(p, sms, st) : launch<false, 8>(p, sms, st);
+    if (p.D <= 128) return bf16 ? launch<true, 16>(p, sms, st) : launch<false, 16>(p, sms, st);
+    return bf16 ? launch<true, 32>(p, sms, st) : launch<false, 32>(p, sms, st);
 }
 
 }  // namespace wq
