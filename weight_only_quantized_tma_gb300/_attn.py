@@ -32,7 +32,13 @@ def _call(name: str, *args) -> None:
         raise WQError(status, name)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    """The current stream's handle (torch's short way to it where there is one: 0.1 against 2 us)."""
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -12,8 +12,9 @@
 //     serves it; Q is loaded in the same order.  V^T: lane g takes codes g D / 8 .. of four
 //     tokens; two tokens' words are merged with byte permutes, since a pair of the V^T
 //     operand is two tokens of one d;
-//   * code -> number is one LOP3 (magic number), one exact subtraction and one fma,
-//     RN(lo + q s): the value that the cache stands for, in every kernel;
+//   * code -> number is a mask and one fma in bf16 (Operand, wq_kv4.cuh), a magic number, an
+//     exact subtraction and one fma in fp16: RN(lo + q s), the value that the cache stands
+//     for, in every kernel;
 //   * the running maximum moves only when a score passes it by more than 2^8, so most
 //     tiles pay one vote in place of a reduction.
 // Warps 0-3 each take 16 of the 64 tokens of a tile with their own maximum, sum and O and
@@ -164,7 +165,8 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
 
     // ---------------------------------------------------------------- compute warps
     const int g = lane >> 2, c = lane & 3;
-    const float sl2 = p.scale * 1.4426950408889634f;
+    constexpr float up = Operand<BF16>::kUp;
+    const float sl2 = p.scale * 1.4426950408889634f * up;
     float* ex = reinterpret_cast<float*>(smem + C::OFF_EX);
     uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
     // this warp's 16 tokens inside a tile (fixed: pages hold a multiple of 16)
@@ -301,17 +303,13 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                 float sc[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-                const uint32_t ks0 = __byte_perm(kp[0], 0, 0x1010), kl0 = __byte_perm(kp[0], 0, 0x3232);
-                const uint32_t ks1 = __byte_perm(kp[1], 0, 0x1010), kl1 = __byte_perm(kp[1], 0, 0x3232);
+                const Operand<BF16> k0 = Operand<BF16>::both(kp[0]), k1 = Operand<BF16>::both(kp[1]);
 #pragma unroll
                 for (int j = 0; j < WK; ++j) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x0 = h ? kw[0][j] >> 8 : kw[0][j], x1 = h ? kw[1][j] >> 8 : kw[1][j];
-                        const uint32_t a[4] = {fma2<BF16>(Codes<BF16>::low(x0), ks0, kl0),
-                                               fma2<BF16>(Codes<BF16>::low(x1), ks1, kl1),
-                                               fma2<BF16>(Codes<BF16>::high(x0), ks0, kl0),
-                                               fma2<BF16>(Codes<BF16>::high(x1), ks1, kl1)};
+                        const uint32_t a[4] = {k0.low(x0), k1.low(x1), k0.high(x0), k1.high(x1)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if constexpr (C::Q_SMEM) {
@@ -370,18 +368,15 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                     pb[nt][1] = transpose8x8(pack2<BF16>(p2, p3));
                 }
                 // ---- O^T += V^T P^T
-                const uint32_t sab = __byte_perm(vpair[0], vpair[1], 0x5410), lab = __byte_perm(vpair[0], vpair[1], 0x7632);
-                const uint32_t scd = __byte_perm(vpair[2], vpair[3], 0x5410), lcd = __byte_perm(vpair[2], vpair[3], 0x7632);
+                const Operand<BF16> vab(__byte_perm(vpair[0], vpair[1], 0x5410), __byte_perm(vpair[0], vpair[1], 0x7632));
+                const Operand<BF16> vcd(__byte_perm(vpair[2], vpair[3], 0x5410), __byte_perm(vpair[2], vpair[3], 0x7632));
 #pragma unroll
                 for (int j = 0; j < WV; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t sel = 0x4400u + 0x1111u * i;
                         const uint32_t xab = __byte_perm(vw[0][j], vw[1][j], sel), xcd = __byte_perm(vw[2][j], vw[3][j], sel);
-                        const uint32_t a[4] = {fma2<BF16>(Codes<BF16>::low(xab), sab, lab),
-                                               fma2<BF16>(Codes<BF16>::high(xab), sab, lab),
-                                               fma2<BF16>(Codes<BF16>::low(xcd), scd, lcd),
-                                               fma2<BF16>(Codes<BF16>::high(xcd), scd, lcd)};
+                        const uint32_t a[4] = {vab.low(xab), vab.high(xab), vcd.low(xcd), vcd.high(xcd)};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[4 * j + i][nt], a, pb[nt][0], pb[nt][1]);
                     }
@@ -456,7 +451,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                         const int64_t row = (int64_t)w.rt * R + r;
                         const int64_t t = w.s.q0 + row / p.group;
                         const int head = w.head * p.group + (int)(row % p.group);
-                        const float inv = l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i];
+                        const float inv = l[nt][i] == 0.f ? 0.f : up / l[nt][i];
                         uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride + (int64_t)head * D + g * (D / 8);
 #pragma unroll
                         for (int k = 0; k < KS; k += 4)
@@ -480,7 +475,8 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
 #pragma unroll
                         for (int k = 0; k < KS; k += 2)
                             __stcg(reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 2 * k),
-                                   make_float4(o[k][nt][i], o[k][nt][2 + i], o[k + 1][nt][i], o[k + 1][nt][2 + i]));
+                                   make_float4(o[k][nt][i] * up, o[k][nt][2 + i] * up, o[k + 1][nt][i] * up,
+                                               o[k + 1][nt][2 + i] * up));
                         if (g == 0)
                             __stcg(reinterpret_cast<float2*>(slot + R * D) + r, make_float2(m[nt][i], l[nt][i]));
                     }

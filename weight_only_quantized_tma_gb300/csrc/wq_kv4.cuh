@@ -94,6 +94,52 @@ __device__ __forceinline__ uint4 word_values(uint32_t w, uint32_t s2, uint32_t l
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (BF16)
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Codes to operands of the attention kernels: values times 1 / kUp.
+//   fp16: as above (kUp = 1).
+//   bf16: a number with exponent field 0 or 1 is its 8 low bits times 2^-133, so a code
+// that is merely masked out is q 2^-133 (bits 0-3) or q 2^-129 (bits 4-7), and one fma
+// with s 2^53 or s 2^49 and lo 2^-80 gives RN(lo + q s) 2^-80: no magic number, no
+// subtraction, no shift for the upper code (9 operations in place of 15 for 8 codes).
+// The scores and the result are multiplied by kUp = 2^80 in fp32.  Exact for |value| >=
+// 2^-46, below that to 2^-53; steps s stay below 2^75.
+template <bool BF16>
+struct Operand {
+    static constexpr float kUp = BF16 ? 1.2089258196146292e24f : 1.0f;
+    uint32_t s_low, s_high, lo;
+    // s and lo of the low and of the high half, in the cache's type
+    __device__ __forceinline__ Operand(uint32_t s2, uint32_t lo2) {
+        if (BF16) {
+            s_low = mul2<true>(s2, 0x5A005A00u);
+            s_high = mul2<true>(s2, 0x58005800u);
+            lo = mul2<true>(lo2, 0x17801780u);
+        } else {
+            s_low = s_high = s2;
+            lo = lo2;
+        }
+    }
+    // one pair (s, lo) for both halves
+    static __device__ __forceinline__ Operand both(uint32_t pair) {
+        return Operand(__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232));
+    }
+    // codes in bits 0-3 and 16-19 of x; in bits 4-7 and 20-23
+    __device__ __forceinline__ uint32_t low(uint32_t x) const {
+        return fma2<BF16>(BF16 ? x & 0x000F000Fu : Codes<BF16>::low(x), s_low, lo);
+    }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const {
+        return fma2<BF16>(BF16 ? x & 0x00F000F0u : Codes<BF16>::high(x), s_high, lo);
+    }
+};
+
 // Offsets inside a page block.
 __device__ __forceinline__ int kv4_codes_at(const Kv4View& c, int which, int place) {
     return (which * c.P + place) * (c.D >> 1);
