@@ -17,8 +17,9 @@
 //     for, in every kernel;
 //   * the running maximum moves only when a score passes it by more than 2^8, so most
 //     tiles pay one vote in place of a reduction.
-// Warps 0-3 each take 16 of the 64 tokens of a tile with their own maximum, sum and O and
-// meet once for each item; warp 4 copies page blocks into a ring with bulk copies.
+// Warps 0-3 each take 32 of the 128 tokens of a tile, as two products side by side, with their
+// own maximum, sum and O, and meet once for each item; warp 4 copies page blocks into a ring
+// with bulk copies.
 #pragma once
 
 #include "wq_attn_sched.cuh"
@@ -26,8 +27,9 @@
 
 namespace wq {
 
-constexpr int kDecodeTN = 64;      // tokens of a tile
-constexpr int kDecodeStages = 4;
+constexpr int kDecodeTN = 128;     // tokens of a tile
+constexpr int kDecodeStages = 3;
+constexpr int kDecodeBlocks = 2;   // 16-token blocks of a warp in a tile
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -74,7 +76,7 @@ template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_decode_kernel(const AttnParams p,
                                                                                           const int stage_bytes) {
     using C = DecodeCfg<D, NT>;
-    constexpr int R = C::R, KS = C::KS, TN = kDecodeTN, ST = kDecodeStages;
+    constexpr int R = C::R, KS = C::KS, TN = kDecodeTN, ST = kDecodeStages, NB = kDecodeBlocks;
     constexpr int WK = D / 32;        // words of codes of a lane and token: K
     constexpr int WV = D / 64;        // V
     extern __shared__ __align__(128) uint8_t smem[];
@@ -101,9 +103,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
     Walk w;
     int used;
     const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
-    const int vp = min(p.c.P, TN);                              // tokens of a page inside a tile
     const int pair_row = 4 * (D >> p.c.g_shift);                // bytes of a token's pairs
-    const int vblock = vp * (D + 2 * pair_row);                 // a (part of a) page block in the ring
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
@@ -119,37 +119,24 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
             for (int t = tb; t < te && ok; ++t) {
                 const int tok = t * TN;
                 // the tile's pages that hold a token to be seen: [skip, pages)
-                const int pages = min((w.v.hi - tok + vp - 1) / vp, TN / vp);
-                const int skip = max(w.v.lo - tok, 0) / vp;
-                int64_t page = 0;
-                const bool parted = p.c.P > TN;
-                if (parted ? (lane < 4 && pages > 0) : (lane >= skip && lane < pages))
-                    page = safe_page(p, w.b, (tok >> p.c.p_shift) + (parted ? 0 : lane));
+                const int pages = min((w.v.hi - tok + p.c.P - 1) >> p.c.p_shift, TN >> p.c.p_shift);
+                const int skip = max(w.v.lo - tok, 0) >> p.c.p_shift;
+                const bool mine = lane >= skip && lane < pages;
+                const int64_t page = mine ? safe_page(p, w.b, (tok >> p.c.p_shift) + lane) : 0;
                 ok = bounded_wait(empty_bar(s), ph ^ 1u, abort_flag, p.status, DEVICE_TIMEOUT_PRODUCER, p.timeout_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) {
-                    if (pages > 0)
-                        ptx::mbar_arrive_expect_tx(full_bar(s), (uint32_t)((pages - skip) * vblock));
+                    if (pages > skip)
+                        ptx::mbar_arrive_expect_tx(full_bar(s), (uint32_t)((pages - skip) * p.c.block_bytes));
                     else
                         ptx::mbar_arrive(full_bar(s));
                 }
                 __syncwarp();
-                const uint32_t dst = sbase + C::OFF_RING + s * stage_bytes;
-                const uint8_t* block = p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes;
-                if (!parted) {
-                    if (lane >= skip && lane < pages) ptx::bulk_load(dst + lane * vblock, block, vblock, full_bar(s), pol);
-                } else if (lane < 4 && pages > 0) {
-                    // half of a page of 128: four pieces (codes and pairs of keys and of values)
-                    const int place = tok & (p.c.P - 1);
-                    const int which = lane & 1;
-                    if (lane < 2)
-                        ptx::bulk_load(dst + which * vp * (D / 2), block + kv4_codes_at(p.c, which, place), vp * (D / 2),
-                                       full_bar(s), pol);
-                    else
-                        ptx::bulk_load(dst + vp * D + which * vp * pair_row, block + kv4_pairs_at(p.c, which, place),
-                                       vp * pair_row, full_bar(s), pol);
-                }
+                if (mine)
+                    ptx::bulk_load(sbase + C::OFF_RING + s * stage_bytes + lane * p.c.block_bytes,
+                                   p.c.pages + page * p.c.page_bytes + (int64_t)w.head * p.c.block_bytes,
+                                   p.c.block_bytes, full_bar(s), pol);
                 issued |= 1u << s;
                 if (++s == ST) s = 0, ph ^= 1u;
             }
@@ -169,14 +156,20 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
     const float sl2 = p.scale * 1.4426950408889634f * up;
     float* ex = reinterpret_cast<float*>(smem + C::OFF_EX);
     uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
-    // this warp's 16 tokens inside a tile (fixed: pages hold a multiple of 16)
-    const int in_page = (16 * warp) & (vp - 1);
-    const uint32_t page_at = (uint32_t)((16 * warp) / vp * vblock);
+    // this warp's blocks of 16 tokens inside a tile (a page holds a multiple of 16): codes
+    // and pairs of keys; those of values follow at fixed distances
+    uint32_t k_codes[NB], k_pairs[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int at = 16 * (NB * warp + n), in_page = at & (p.c.P - 1);
+        const uint32_t page_at = (uint32_t)((at >> p.c.p_shift) * p.c.block_bytes);
+        k_codes[n] = page_at + in_page * (D / 2);
+        k_pairs[n] = page_at + p.c.P * D + in_page * pair_row;
+    }
+    const uint32_t v_codes_off = p.c.P * (D / 2), v_pairs_off = p.c.P * pair_row;
     const int row_k[2] = {token_of_row(g), token_of_row(g) + 8};
     const int row_v[4] = {token_of_row(2 * c), token_of_row(2 * c + 1), token_of_row(2 * c) + 8,
                           token_of_row(2 * c + 1) + 8};
-    const uint32_t k_codes = page_at + in_page * (D / 2), v_codes = page_at + (vp + in_page) * (D / 2);
-    const uint32_t k_pairs = page_at + vp * D + in_page * pair_row, v_pairs = k_pairs + vp * pair_row;
     const int k_group = ((c * (D / 4)) >> p.c.g_shift) * 4, v_group = ((g * (D / 8)) >> p.c.g_shift) * 4;
 
     int s = 0;
@@ -254,69 +247,66 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         for (int t = tb; t < te; ++t) {
             if (ok) ok = __all_sync(0xffffffffu, bounded_wait(full_bar(s), ph, abort_flag, p.status,
                                                               DEVICE_TIMEOUT_TRANSFORM, p.timeout_ns));
-            const int tok = t * TN + 16 * warp;
-            if (ok && tok < w.v.hi && tok + 16 > w.v.lo) {
+            const int tok = t * TN + 16 * NB * warp;
+            if (ok && tok < w.v.hi && tok + 16 * NB > w.v.lo) {
                 const uint8_t* st = smem + C::OFF_RING + s * stage_bytes;
-                const bool masked = tok < all_lo || tok + 16 > all_hi;
-                // ---- S^T: 16 tokens x R rows
-                uint32_t kw[2][WK], kp[2], vw[4][WV], vpair[4];
+                const bool masked = tok < all_lo || tok + 16 * NB > all_hi;
+                // ---- S^T: 16 tokens x R rows for each block
+                uint32_t kw[NB][2][WK], kp[NB][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t* src = st + k_codes + row_k[i] * (D / 2) + c * (D / 8);
-                    if constexpr (WK == 4) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(src);
-                        kw[i][0] = v.x, kw[i][1] = v.y, kw[i][2] = v.z, kw[i][3] = v.w;
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2*>(src);
-                        kw[i][0] = v.x, kw[i][1] = v.y;
-                    }
-                    kp[i] = *reinterpret_cast<const uint32_t*>(st + k_pairs + row_k[i] * pair_row + k_group);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* src = st + v_codes + row_v[i] * (D / 2) + g * (D / 16);
-                    if constexpr (WV == 2) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(src);
-                        vw[i][0] = v.x, vw[i][1] = v.y;
-                    } else {
-                        vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
-                    }
-                    vpair[i] = *reinterpret_cast<const uint32_t*>(st + v_pairs + row_v[i] * pair_row + v_group);
-                }
-                if (masked) {
-                    // What a row does not see must not reach it as 0 * NaN: values that
-                    // nobody sees are cleared, and a NaN among a seen token's values moves
-                    // to its key, where the mask of each row applies.
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t z = 0;
-                        for (int j = 0; j < pair_row; j += 4)
-                            z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(st + v_pairs + row_k[i] * pair_row + j), 0u, z);
-                        if (z & 0x7FFF7FFFu) kp[i] = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                        const uint8_t* src = st + k_codes[n] + row_k[i] * (D / 2) + c * (D / 8);
+                        if constexpr (WK == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(src);
+                            kw[n][i][0] = v.x, kw[n][i][1] = v.y, kw[n][i][2] = v.z, kw[n][i][3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(src);
+                            kw[n][i][0] = v.x, kw[n][i][1] = v.y;
+                        }
+                        kp[n][i] = *reinterpret_cast<const uint32_t*>(st + k_pairs[n] + row_k[i] * pair_row + k_group);
                     }
+                if (masked) {
+                    // What a row does not see must not reach it as 0 * NaN: values that
+                    // nobody sees are cleared below, and a NaN among a seen token's values
+                    // moves to its key, where the mask of each row applies.
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tt = tok + row_v[i];
-                        if (tt < w.v.lo || tt >= w.v.hi || (fma2<BF16>(vpair[i], 0u, 0u) & 0x7FFF7FFFu)) vpair[i] = 0u;
-                    }
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t z = 0;
+                            for (int j = 0; j < pair_row; j += 4)
+                                z = fma2<BF16>(*reinterpret_cast<const uint32_t*>(st + k_pairs[n] + v_pairs_off +
+                                                                                  row_k[i] * pair_row + j), 0u, z);
+                            if (z & 0x7FFF7FFFu) kp[n][i] = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                        }
                 }
-                float sc[NT][4];
+                float sc[NB][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-                const Operand<BF16> k0 = Operand<BF16>::both(kp[0]), k1 = Operand<BF16>::both(kp[1]);
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int j = 0; j < WK; ++j) {
+                    for (int nt = 0; nt < NT; ++nt) sc[n][nt][0] = sc[n][nt][1] = sc[n][nt][2] = sc[n][nt][3] = 0.f;
+                {
+                    const Operand<BF16> k0[NB] = {Operand<BF16>::both(kp[0][0]), Operand<BF16>::both(kp[1][0])};
+                    const Operand<BF16> k1[NB] = {Operand<BF16>::both(kp[0][1]), Operand<BF16>::both(kp[1][1])};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x0 = h ? kw[0][j] >> 8 : kw[0][j], x1 = h ? kw[1][j] >> 8 : kw[1][j];
-                        const uint32_t a[4] = {k0.low(x0), k1.low(x1), k0.high(x0), k1.high(x1)};
+                    for (int j = 0; j < WK; ++j) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (C::Q_SMEM) {
-                                const uint2 q = qs[((2 * j + h) * NT + nt) * 32 + lane];
-                                mma16816<BF16>(sc[nt], a, q.x, q.y);
-                            } else {
-                                mma16816<BF16>(sc[nt], a, qr[2 * j + h][0], qr[2 * j + h][1]);
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) {
+                                const uint32_t x0 = h ? kw[n][0][j] >> 8 : kw[n][0][j], x1 = h ? kw[n][1][j] >> 8 : kw[n][1][j];
+                                const uint32_t a[4] = {k0[n].low(x0), k1[n].low(x1), k0[n].high(x0), k1[n].high(x1)};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    if constexpr (C::Q_SMEM) {
+                                        const uint2 q = qs[((2 * j + h) * NT + nt) * 32 + lane];
+                                        mma16816<BF16>(sc[n][nt], a, q.x, q.y);
+                                    } else {
+                                        mma16816<BF16>(sc[n][nt], a, qr[2 * j + h][0], qr[2 * j + h][1]);
+                                    }
+                                }
                             }
                         }
                     }
@@ -327,14 +317,19 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x0 = sc[nt][i] * sl2, x1 = sc[nt][2 + i] * sl2;
-                        if (masked) {
-                            const int t0 = tok + row_k[0], t1 = tok + row_k[1];
-                            if (t0 < lo[nt][i] || t0 >= hi[nt][i]) x0 = -INFINITY;
-                            if (t1 < lo[nt][i] || t1 >= hi[nt][i]) x1 = -INFINITY;
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            float x0 = sc[n][nt][i] * sl2, x1 = sc[n][nt][2 + i] * sl2;
+                            if (masked) {
+                                const int t0 = tok + 16 * n + row_k[0], t1 = tok + 16 * n + row_k[1];
+                                if (t0 < lo[nt][i] || t0 >= hi[nt][i]) x0 = -INFINITY;
+                                if (t1 < lo[nt][i] || t1 >= hi[nt][i]) x1 = -INFINITY;
+                            }
+                            sc[n][nt][i] = x0, sc[n][nt][2 + i] = x1;
+                            top = fmaxf(top, fmaxf(x0, x1));
                         }
-                        sc[nt][i] = x0, sc[nt][2 + i] = x1;
-                        grow |= fmaxf(x0, x1) > m[nt][i] + 8.f;
+                        grow |= top > m[nt][i] + 8.f;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -342,7 +337,9 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                         float f[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float x = fmaxf(sc[nt][i], sc[nt][2 + i]);
+                            float x = fmaxf(sc[0][nt][i], sc[0][nt][2 + i]);
+#pragma unroll
+                            for (int n = 1; n < NB; ++n) x = fmaxf(x, fmaxf(sc[n][nt][i], sc[n][nt][2 + i]));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -356,30 +353,55 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                             o[k][nt][0] *= f[0], o[k][nt][2] *= f[0], o[k][nt][1] *= f[1], o[k][nt][3] *= f[1];
                     }
                 }
-                uint32_t pb[NT][2];
+                uint32_t pb[NB][NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-                    const float p0 = ex2(sc[nt][0] - m0), p1 = ex2(sc[nt][1] - m1), p2 = ex2(sc[nt][2] - m0),
-                                p3 = ex2(sc[nt][3] - m1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    pb[nt][0] = transpose8x8(pack2<BF16>(p0, p1));
-                    pb[nt][1] = transpose8x8(pack2<BF16>(p2, p3));
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        const float p0 = ex2(sc[n][nt][0] - m0), p1 = ex2(sc[n][nt][1] - m1), p2 = ex2(sc[n][nt][2] - m0),
+                                    p3 = ex2(sc[n][nt][3] - m1);
+                        l[nt][0] += p0 + p2;
+                        l[nt][1] += p1 + p3;
+                        pb[n][nt][0] = transpose8x8(pack2<BF16>(p0, p1));
+                        pb[n][nt][1] = transpose8x8(pack2<BF16>(p2, p3));
+                    }
                 }
                 // ---- O^T += V^T P^T
-                const Operand<BF16> vab(__byte_perm(vpair[0], vpair[1], 0x5410), __byte_perm(vpair[0], vpair[1], 0x7632));
-                const Operand<BF16> vcd(__byte_perm(vpair[2], vpair[3], 0x5410), __byte_perm(vpair[2], vpair[3], 0x7632));
 #pragma unroll
-                for (int j = 0; j < WV; ++j)
+                for (int n = 0; n < NB; ++n) {
+                    uint32_t vw[4][WV], vpair[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t sel = 0x4400u + 0x1111u * i;
-                        const uint32_t xab = __byte_perm(vw[0][j], vw[1][j], sel), xcd = __byte_perm(vw[2][j], vw[3][j], sel);
-                        const uint32_t a[4] = {vab.low(xab), vab.high(xab), vcd.low(xcd), vcd.high(xcd)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[4 * j + i][nt], a, pb[nt][0], pb[nt][1]);
+                        const uint8_t* src = st + k_codes[n] + v_codes_off + row_v[i] * (D / 2) + g * (D / 16);
+                        if constexpr (WV == 2) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(src);
+                            vw[i][0] = v.x, vw[i][1] = v.y;
+                        } else {
+                            vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                        }
+                        vpair[i] = *reinterpret_cast<const uint32_t*>(st + k_pairs[n] + v_pairs_off + row_v[i] * pair_row + v_group);
                     }
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tt = tok + 16 * n + row_v[i];
+                            if (tt < w.v.lo || tt >= w.v.hi || (fma2<BF16>(vpair[i], 0u, 0u) & 0x7FFF7FFFu)) vpair[i] = 0u;
+                        }
+                    }
+                    const Operand<BF16> vab(__byte_perm(vpair[0], vpair[1], 0x5410), __byte_perm(vpair[0], vpair[1], 0x7632));
+                    const Operand<BF16> vcd(__byte_perm(vpair[2], vpair[3], 0x5410), __byte_perm(vpair[2], vpair[3], 0x7632));
+#pragma unroll
+                    for (int j = 0; j < WV; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t sel = 0x4400u + 0x1111u * i;
+                            const uint32_t xab = __byte_perm(vw[0][j], vw[1][j], sel), xcd = __byte_perm(vw[2][j], vw[3][j], sel);
+                            const uint32_t a[4] = {vab.low(xab), vab.high(xab), vcd.low(xcd), vcd.high(xcd)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<BF16>(o[4 * j + i][nt], a, pb[n][nt][0], pb[n][nt][1]);
+                        }
+                }
             }
             __syncwarp();
             if (ok && lane == 0) ptx::mbar_arrive(empty_bar(s));
