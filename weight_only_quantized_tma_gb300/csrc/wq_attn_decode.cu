@@ -45,9 +45,12 @@ auto pick(const Kv4View& c, bool bf16, int64_t rows, F f) {
     auto nt = [&](auto b, auto d) {
         constexpr bool B = decltype(b)::value;
         constexpr int DD = decltype(d)::value;
-        if (rows <= 8) return f(Launcher<B, DD, 1>{});
-        if (rows <= 16) return f(Launcher<B, DD, 2>{});
-        return f(Launcher<B, DD, 4>{});
+        // as few row tiles as can be (each unpacks the codes anew), of equal height
+        const int64_t eights = (rows + 7) / 8, tiles = (eights + kDecodeMaxNT - 1) / kDecodeMaxNT;
+        const int64_t n = (eights + tiles - 1) / tiles;
+        if (n <= 1) return f(Launcher<B, DD, 1>{});
+        if (n == 2) return f(Launcher<B, DD, 2>{});
+        return f(Launcher<B, DD, 3>{});
     };
     using I64 = std::integral_constant<int, 64>;
     using I128 = std::integral_constant<int, 128>;

@@ -17,9 +17,9 @@
 //     for, in every kernel;
 //   * the running maximum moves only when a score passes it by more than 2^8, so most
 //     tiles pay one vote in place of a reduction.
-// Warps 0-3 each take 32 of the 128 tokens of a tile, as two products side by side, with their
-// own maximum, sum and O, and meet once for each item; warp 4 copies page blocks into a ring
-// with bulk copies.
+// Warps 0-3 each take 32 of the 128 tokens of a tile (with 8 rows as two products side by
+// side) with their own maximum, sum and O, and meet once for each item; warp 4 copies page
+// blocks into a ring with bulk copies.
 #pragma once
 
 #include "wq_attn_sched.cuh"
@@ -30,6 +30,7 @@ namespace wq {
 constexpr int kDecodeTN = 128;     // tokens of a tile
 constexpr int kDecodeStages = 3;
 constexpr int kDecodeBlocks = 2;   // 16-token blocks of a warp in a tile
+constexpr int kDecodeMaxNT = 3;    // most groups of 8 rows in a row tile
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -65,6 +66,7 @@ struct DecodeCfg {
     static constexpr int OFF_BAR = (OFF_W + W_BYTES + 15) / 16 * 16;
     static constexpr int OFF_MISC = OFF_BAR + 2 * kDecodeStages * 8;
     static constexpr int OFF_RING = (OFF_MISC + 16 + 127) / 128 * 128;
+    static constexpr int SIDE = NT == 1 ? 2 : 1;     // blocks side by side: more hide latencies, but need registers
     static constexpr int MIN_BLOCKS = NT == 1 ? 3 : 2;
 };
 
@@ -76,7 +78,7 @@ template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_decode_kernel(const AttnParams p,
                                                                                           const int stage_bytes) {
     using C = DecodeCfg<D, NT>;
-    constexpr int R = C::R, KS = C::KS, TN = kDecodeTN, ST = kDecodeStages, NB = kDecodeBlocks;
+    constexpr int R = C::R, KS = C::KS, TN = kDecodeTN, ST = kDecodeStages, NB = C::SIDE;
     constexpr int WK = D / 32;        // words of codes of a lane and token: K
     constexpr int WV = D / 64;        // V
     extern __shared__ __align__(128) uint8_t smem[];
@@ -101,8 +103,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
     ptx::grid_launch_dependents();
 
     Walk w;
-    int used;
-    const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
+    const Runs runs = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w);
     const int pair_row = 4 * (D >> p.c.g_shift);                // bytes of a token's pairs
 
     if (warp == 4) {
@@ -158,13 +159,13 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
     uint2* qs = reinterpret_cast<uint2*>(smem + C::OFF_Q);
     // this warp's blocks of 16 tokens inside a tile (a page holds a multiple of 16): codes
     // and pairs of keys; those of values follow at fixed distances
-    uint32_t k_codes[NB], k_pairs[NB];
+    uint32_t all_codes[kDecodeBlocks], all_pairs[kDecodeBlocks];
 #pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        const int at = 16 * (NB * warp + n), in_page = at & (p.c.P - 1);
+    for (int n = 0; n < kDecodeBlocks; ++n) {
+        const int at = 16 * (kDecodeBlocks * warp + n), in_page = at & (p.c.P - 1);
         const uint32_t page_at = (uint32_t)((at >> p.c.p_shift) * p.c.block_bytes);
-        k_codes[n] = page_at + in_page * (D / 2);
-        k_pairs[n] = page_at + p.c.P * D + in_page * pair_row;
+        all_codes[n] = page_at + in_page * (D / 2);
+        all_pairs[n] = page_at + p.c.P * D + in_page * pair_row;
     }
     const uint32_t v_codes_off = p.c.P * (D / 2), v_pairs_off = p.c.P * pair_row;
     const int row_k[2] = {token_of_row(g), token_of_row(g) + 8};
@@ -247,8 +248,16 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         for (int t = tb; t < te; ++t) {
             if (ok) ok = __all_sync(0xffffffffu, bounded_wait(full_bar(s), ph, abort_flag, p.status,
                                                               DEVICE_TIMEOUT_TRANSFORM, p.timeout_ns));
-            const int tok = t * TN + 16 * NB * warp;
+#pragma unroll 1
+            for (int part = 0; part < kDecodeBlocks / NB; ++part) {
+            const int tok = t * TN + 16 * (kDecodeBlocks * warp + part * NB);
             if (ok && tok < w.v.hi && tok + 16 * NB > w.v.lo) {
+                uint32_t k_codes[NB], k_pairs[NB];
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    k_codes[n] = NB == 1 && part ? all_codes[kDecodeBlocks - 1] : all_codes[n];
+                    k_pairs[n] = NB == 1 && part ? all_pairs[kDecodeBlocks - 1] : all_pairs[n];
+                }
                 const uint8_t* st = smem + C::OFF_RING + s * stage_bytes;
                 const bool masked = tok < all_lo || tok + 16 * NB > all_hi;
                 // ---- S^T: 16 tokens x R rows for each block
@@ -288,8 +297,12 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) sc[n][nt][0] = sc[n][nt][1] = sc[n][nt][2] = sc[n][nt][3] = 0.f;
                 {
-                    const Operand<BF16> k0[NB] = {Operand<BF16>::both(kp[0][0]), Operand<BF16>::both(kp[1][0])};
-                    const Operand<BF16> k1[NB] = {Operand<BF16>::both(kp[0][1]), Operand<BF16>::both(kp[1][1])};
+                    Operand<BF16> k0[NB], k1[NB];
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        k0[n] = Operand<BF16>::both(kp[n][0]);
+                        k1[n] = Operand<BF16>::both(kp[n][1]);
+                    }
 #pragma unroll
                     for (int j = 0; j < WK; ++j) {
 #pragma unroll
@@ -403,6 +416,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                         }
                 }
             }
+            }
             __syncwarp();
             if (ok && lane == 0) ptx::mbar_arrive(empty_bar(s));
             if (++s == ST) s = 0, ph ^= 1u;
@@ -459,8 +473,8 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         if (warp == 1) put(1);
         ptx::named_barrier_sync(1, 128);
         const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
-        const int b_first = whole ? 0 : block_of(w.item0, total, used);
-        const int parts = whole ? 1 : block_of(w.item0 + w.units - 1, total, used) - b_first + 1;
+        const int b_first = whole ? 0 : run_of(runs, w.item0);
+        const int parts = whole ? 1 : run_of(runs, w.item0 + w.units - 1) - b_first + 1;
         if (warp == 0) {
             add(1);
             if (whole && ok) {

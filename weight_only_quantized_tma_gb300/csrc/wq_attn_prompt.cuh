@@ -59,33 +59,6 @@ struct PromptCfg {
     static constexpr int S_COL = 0, O_COL = 256;           // S_i at 128 i + 64 buffer, O_i at 256 + 128 i; P over S
 };
 
-// Two fp32 values in a 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t f2(float x, float y) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
-    return d;
-}
-__device__ __forceinline__ float2 un2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const AttnParams p, const int stage_bytes) {
     using C = PromptCfg<D>;
@@ -139,8 +112,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     ptx::grid_launch_dependents();
 
     Walk w{};
-    int used;
-    const int64_t total = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w, used);
+    const Runs runs = walk_begin<R, TN>(p, blockIdx.x, gridDim.x, w);
     const int pair_row = 4 * (D >> p.c.g_shift);
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
@@ -477,8 +449,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             }
             // ---- the item's result, or this block's part of it
             const bool whole = w.u == w.item0 && w.item0 + w.units <= w.u1;
-            const int b_first = whole ? 0 : block_of(w.item0, total, used);
-            const int parts = whole ? 1 : block_of(w.item0 + w.units - 1, total, used) - b_first + 1;
+            const int b_first = whole ? 0 : run_of(runs, w.item0);
+            const int parts = whole ? 1 : run_of(runs, w.item0 + w.units - 1) - b_first + 1;
             float* part = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
             if (!idle && ok) {
                 const float inv = l == 0.f ? 0.f : up / l;

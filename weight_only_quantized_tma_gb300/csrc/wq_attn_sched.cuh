@@ -80,9 +80,31 @@ struct Walk {
     int units;             // of the item
 };
 
-// Executed by a full warp.  Total number of tiles, and the walk's start for this block.
+// 64-bit tile numbers almost always fit 32 bits, where a division is several times shorter.
+__device__ __forceinline__ int64_t div_short(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Run i of `used` runs of `total` tiles begins at tile run_begin: the first total % used
+// runs are one tile longer.
+struct Runs {
+    int64_t len, longer;   // tiles of a short run, number of long runs
+};
+__device__ __forceinline__ Runs make_runs(int64_t total, int used) {
+    const int64_t len = div_short(total, used);
+    return Runs{len, total - len * used};
+}
+__device__ __forceinline__ int64_t run_begin(const Runs& r, int i) { return r.len * i + min((int64_t)i, r.longer); }
+// The run that holds tile u.
+__device__ __forceinline__ int run_of(const Runs& r, int64_t u) {
+    const int64_t edge = (r.len + 1) * r.longer;
+    return (int)(u < edge ? div_short(u, r.len + 1) : r.longer + div_short(u - edge, r.len));
+}
+
+// Executed by a full warp.  How the tiles are cut into runs, and this block's walk.
 template <int R, int TN>
-__device__ __forceinline__ int64_t walk_begin(const AttnParams& p, int block, int blocks, Walk& w, int& used) {
+__device__ __forceinline__ Runs walk_begin(const AttnParams& p, int block, int blocks, Walk& w) {
     const int lane = threadIdx.x & 31;
     int64_t total = 0, mine = 0;
     for (int64_t b0 = 0; b0 < p.B; b0 += 32) {
@@ -92,11 +114,12 @@ __device__ __forceinline__ int64_t walk_begin(const AttnParams& p, int block, in
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         total += sum;
     }
-    used = (int)min((int64_t)blocks, total);
+    const int used = (int)min((int64_t)blocks, total);
     w.u = w.u1 = 0;
-    if (block >= used) return total;
-    w.u = total * block / used;
-    w.u1 = total * (block + 1) / used;
+    if (block >= used) return Runs{0, 0};
+    const Runs runs = make_runs(total, used);
+    w.u = run_begin(runs, block);
+    w.u1 = run_begin(runs, block + 1);
     int64_t base = 0;
     for (int64_t b0 = 0; b0 < p.B; b0 += 32) {
         if (p.B > 32) mine = seq_units<R, TN>(p, (int)(b0 + lane));
@@ -124,9 +147,9 @@ __device__ __forceinline__ int64_t walk_begin(const AttnParams& p, int block, in
         if (w.item0 + all > w.u) break;
         w.item0 += all;
     }
-    w.head = (int)((w.u - w.item0) / w.units);
+    w.head = (int)div_short(w.u - w.item0, w.units);
     w.item0 += (int64_t)w.head * w.units;
-    return total;
+    return runs;
 }
 
 // Past the current item's part; the next item if any of the run is left.
@@ -145,11 +168,6 @@ __device__ __forceinline__ void walk_next(const AttnParams& p, Walk& w) {
     }
     w.v = row_tile_span<R, TN>(p, w.s, w.rt);
     w.units = w.v.t1 - w.v.t0;
-}
-
-// The block whose run holds tile u, when `total` tiles are cut into `used` runs.
-__device__ __forceinline__ int block_of(int64_t u, int64_t total, int used) {
-    return (int)(((u + 1) * used - 1) / total);
 }
 
 __device__ __forceinline__ int64_t safe_page(const AttnParams& p, int b, int entry) {

@@ -269,7 +269,7 @@ struct Kv4RowsParams {   // write and read
     const int64_t* slots;
     int64_t T;
     uint32_t* status;
-    FastDiv div_heads;
+    FastDiv div_groups;  // groups of heads of one token
 };
 cudaError_t launch_kv4_write(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);   // wq_kv4.cu
 cudaError_t launch_kv4_read(const Kv4RowsParams& p, bool bf16, int sms, cudaStream_t st);

@@ -116,6 +116,7 @@ template <bool BF16>
 struct Operand {
     static constexpr float kUp = BF16 ? 1.2089258196146292e24f : 1.0f;
     uint32_t s_low, s_high, lo;
+    Operand() = default;
     // s and lo of the low and of the high half, in the cache's type
     __device__ __forceinline__ Operand(uint32_t s2, uint32_t lo2) {
         if (BF16) {
@@ -139,6 +140,33 @@ struct Operand {
         return fma2<BF16>(BF16 ? x & 0x00F000F0u : Codes<BF16>::high(x), s_high, lo);
     }
 };
+
+// Two fp32 values in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 un2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // Offsets inside a page block.
 __device__ __forceinline__ int kv4_codes_at(const Kv4View& c, int which, int place) {
