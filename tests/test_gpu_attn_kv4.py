@@ -202,6 +202,29 @@ def test_same_results_every_time_and_on_other_streams(news):
         assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("case", [  # new tokens, length, query heads, key heads, D, G, P, type, sequences
+    (9, 40000, 8, 2, 128, 128, 64, torch.bfloat16, 1), (200, 5000, 8, 2, 64, 32, 16, torch.float16, 2),
+    (192, 5000, 8, 2, 64, 64, 64, torch.bfloat16, 2), (256, 5000, 8, 2, 64, 64, 64, torch.float16, 1),
+    (1, 9000, 8, 2, 128, 64, 32, torch.bfloat16, 7), (25, 20000, 8, 2, 64, 64, 64, torch.float16, 1)])
+def test_many_runs_agree(case):
+    """Waits that end a phase early show as rare differences: many runs of calls that split items over
+    blocks, mix full and part-filled row tiles and move their maxima."""
+    n, L, Hq, H, D, G, P, dt, B = case
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    each = -(-L // P)
+    pages = wq.wq_kv4_pages(each * B, H, D, G, P, "cuda")
+    table = torch.randperm(each * B, device="cuda", generator=gen).to(torch.int32).view(B, each).contiguous()
+    t = torch.arange(L, device="cuda")
+    for b in range(B):
+        kv = torch.randn(2, L, H, D, device="cuda", generator=gen).to(dt)
+        wq.wq_kv4_write(kv[0], kv[1], table[b].long()[t // P] * P + t % P, pages, G, P)
+    q = torch.randn(n * B, Hq, D, device="cuda", generator=gen).to(dt)
+    cu = torch.arange(B + 1, device="cuda", dtype=torch.int32) * n
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    runs = [wq.wq_attn_kv4(q, pages, table, lens, G, P, cu_q=cu, max_q=n) for _ in range(120)]
+    assert torch.stack([(r != runs[0]).any() for r in runs]).sum() == 0
+
+
 @pytest.mark.parametrize("n", [1, 5, 80])
 def test_graph_replays_with_new_lengths(n):
     p = Problem([300, 150, 220], [n, n, n], 4, 2, 64, 32, 16, "f16", seed=13, poison=False)

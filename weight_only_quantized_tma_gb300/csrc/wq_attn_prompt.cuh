@@ -51,7 +51,7 @@ struct PromptCfg {
     static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
     static constexpr int OFF_V = OFF_K + SLOTS * KV_TILE;
     static constexpr int OFF_BAR = OFF_V + SLOTS * KV_TILE;
-    static constexpr int NBARS = 2 * RAW_STAGES + 4 * SLOTS + 15;
+    static constexpr int NBARS = 2 * RAW_STAGES + 4 * SLOTS + 17;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
     static constexpr int OFF_RAW = (OFF_MISC + 16 + 127) / 128 * 128;
     static constexpr int MERGE_ROWS = 32;                  // merge weights live in the Q tiles
@@ -75,11 +75,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
     const uint32_t bar1 = bar0 + 8u * (2 * RS + 4 * NS);
     auto q_full = [&](int i) { return bar1 + 8u * i; };
     auto o_empty = [&](int i) { return bar1 + 8u * (2 + i); };
-    auto o_done = [&](int i) { return bar1 + 8u * (4 + i); };                 // a PV of row tile i has ended
     // of row tile i and S buffer h
-    auto s_full = [&](int i, int h) { return bar1 + 8u * (6 + 2 * i + h); };
-    auto p_full = [&](int i, int h) { return bar1 + 8u * (10 + 2 * i + h); };
-    const uint32_t final_bar = bar1 + 8u * 14;
+    auto s_full = [&](int i, int h) { return bar1 + 8u * (4 + 2 * i + h); };
+    auto p_full = [&](int i, int h) { return bar1 + 8u * (8 + 2 * i + h); };
+    // The PV of a tile in buffer h has ended.  One barrier for each buffer: the softmax runs
+    // a PV ahead, and on one barrier for all it would take the phase before for the one it
+    // waits for (a wait tells phases apart by parity alone).
+    auto o_done = [&](int i, int h) { return bar1 + 8u * (12 + 2 * i + h); };
+    const uint32_t final_bar = bar1 + 8u * 16;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -92,8 +95,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(q_full(i), 4);
             ptx::mbar_init(o_empty(i), 4);
-            ptx::mbar_init(o_done(i), 1);
-            for (int h = 0; h < 2; ++h) ptx::mbar_init(s_full(i, h), 1), ptx::mbar_init(p_full(i, h), 4);
+            for (int h = 0; h < 2; ++h) {
+                ptx::mbar_init(s_full(i, h), 1);
+                ptx::mbar_init(p_full(i, h), 4);
+                ptx::mbar_init(o_done(i, h), 1);
+            }
         }
         ptx::mbar_init(final_bar, 2);
         *abort_flag = 0u;
@@ -174,9 +180,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
     } else if (warp < 18) {
         // ------------------------------------------------------------ MMA issuers
-        // One lane for each row tile, and as few instructions between products as can be:
-        // a product of 128 x 128 x 16 takes 64 cycles, so address arithmetic and waits here
-        // leave the tensor core idle.  The products of a tile are unrolled with constant
+        // One lane for each row tile, and as few instructions between products as can be: a
+        // product of 128 x 128 x 16 takes 64 cycles, a branch in one lane about 30 and a commit
+        // about 50, so the steady loop tests its three barriers together, with one branch.  The products of a tile are unrolled with constant
         // offsets, and the whole of tensor memory is ours, so its addresses are constants.
         const int i = warp - 16;
         if (lane == 0) {
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const uint32_t q_lo = ptx::sdesc_lo(sbase + C::OFF_Q + i * C::Q_TILE);
             const uint32_t k_lo = ptx::sdesc_lo(sbase + C::OFF_K), v_lo = ptx::sdesc_lo_mn(sbase + C::OFF_V, C::KV_HALF);
             const uint32_t s_tm = C::S_COL + 128 * i, o_tm = C::O_COL + 128 * i;
-            const uint32_t b_q = q_full(i), b_s = s_full(i, 0), b_p = p_full(i, 0), b_od = o_done(i), b_oe = o_empty(i);
+            const uint32_t b_q = q_full(i), b_s = s_full(i, 0), b_p = p_full(i, 0), b_od = o_done(i, 0), b_oe = o_empty(i);
             const uint32_t b_kf = kv_full(0, 0), b_ke = kv_empty(0, 0), b_vf = kv_full(1, 0), b_ve = kv_empty(1, 0);
             uint32_t nk = 0, nv = 0;        // tiles of keys and of values so far: slot n % 4, lap n / 4
             uint32_t ns = 0, np = 0;        // S and P of this row tile so far: buffer n % 2
@@ -226,20 +232,47 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 if (ok && tiles > 1) qk();
                 ready(b_oe, o_ph);
                 o_ph ^= 1u;
-                for (int t = 0; t < tiles && ok; ++t) {
+                int t = 0;
+                for (; t + 2 < tiles; ++t) {
+                    // steady: PV of this tile, then S of the tile after next into the same buffer
+                    const uint32_t vs = nv & (NS - 1), ks = nk & (NS - 1), h = np & 1u;
+                    const uint32_t bar_v = b_vf + 8 * vs, bar_k = b_kf + 8 * ks, bar_p = b_p + 8 * h;
+                    const uint32_t par_v = nv / NS & 1u, par_k = nk / NS & 1u, par_p = np >> 1 & 1u;
+                    const bool all = ptx::mbar_test_wait(bar_v, par_v) & ptx::mbar_test_wait(bar_k, par_k) &
+                                     ptx::mbar_test_wait(bar_p, par_p);
+                    if (!all) {
+                        wait(bar_v, par_v, DEVICE_TIMEOUT_MMA);
+                        wait(bar_p, par_p, DEVICE_TIMEOUT_MMA);
+                        if (!wait(bar_k, par_k, DEVICE_TIMEOUT_MMA)) break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t d = s_tm + TN * h, bv = v_lo + vs * (C::KV_TILE >> 4), bk = k_lo + ks * (C::KV_TILE >> 4);
+#pragma unroll
+                    for (int k = 0; k < TN / 16; ++k)
+                        ptx::mma_f16_ts(o_tm, d + 8 * k, bv + k * (2048 >> 4), ptx::kSdescHi, id_o, k > 0 || t > 0);
+                    ptx::mma_commit(b_od + 8 * h);
+                    ptx::mma_commit(b_ve + 8 * vs);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+                        ptx::mma_f16_ss(d, q_lo + (k >> 2) * (C::Q_HALF >> 4) + (k & 3) * 2, ptx::kSdescHi,
+                                        bk + (k >> 2) * (C::KV_HALF >> 4) + (k & 3) * 2, ptx::kSdescHi, id_s, k > 0);
+                    ptx::mma_commit(b_s + 8 * h);
+                    ptx::mma_commit(b_ke + 8 * ks);
+                    ++nv, ++np, ++nk, ++ns;
+                }
+                for (; t < tiles && ok; ++t) {   // the last two
                     const uint32_t slot = nv & (NS - 1), h = np & 1u;
                     ready(b_vf + 8 * slot, nv / NS & 1u);
                     ready(b_p + 8 * h, np >> 1 & 1u);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t b = v_lo + slot * (C::KV_TILE >> 4), a = s_tm + TN * h;   // O (+)= P V
+                    const uint32_t b = v_lo + slot * (C::KV_TILE >> 4), a = s_tm + TN * h;
 #pragma unroll
                     for (int k = 0; k < TN / 16; ++k)
                         ptx::mma_f16_ts(o_tm, a + 8 * k, b + k * (2048 >> 4), ptx::kSdescHi, id_o, k > 0 || t > 0);
-                    ptx::mma_commit(b_od);
+                    ptx::mma_commit(b_od + 8 * h);
                     ptx::mma_commit(b_ve + 8 * slot);
                     ++nv, ++np;
-                    if (t + 2 < tiles) qk();
                 }
             }
             // given up (either warp): the MMAs in flight end before tensor memory is freed
@@ -386,7 +419,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                     // Under the maximum so far a sum below 2^14 shows that no probability
                     // passed 2^14, which both types hold; else the tile is done again under
                     // the new maximum.  Rows that have seen nothing have none yet.
-                    uint32_t o[32];
                     float sum;
 #pragma unroll 1
                     for (bool again = __any_sync(0xffffffffu, m == -INFINITY);;) {
@@ -404,7 +436,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                             l *= f;
                             if (t > tb && __any_sync(0xffffffffu, grow)) {
                                 // O is scaled between products: the last one has to have ended
-                                ok = __all_sync(0xffffffffu, wait(o_done(i), (n - 1) & 1u, DEVICE_TIMEOUT_EPILOGUE));
+                                ok = __all_sync(0xffffffffu, wait(o_done(i, (n - 1) & 1u), (n - 1) >> 1 & 1u, DEVICE_TIMEOUT_EPILOGUE));
                                 if (!ok) break;
                                 ptx::tc_fence_after();
 #pragma unroll 1
@@ -422,29 +454,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         const uint64_t nm = f2(-mm, -mm);
                         uint64_t la = 0, lb = 0;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            float2 e = un2(fma_f2(f2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sl, nm));
-                            e.x = ex2(e.x), e.y = ex2(e.y);
-                            if (k & 1)
-                                lb = add_f2(lb, f2(e.x, e.y));
-                            else
-                                la = add_f2(la, f2(e.x, e.y));
-                            o[k] = pack2<BF16>(e.x, e.y);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t o[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int at = 32 * c + 2 * k;
+                                float2 e = un2(fma_f2(f2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), sl, nm));
+                                e.x = ex2(e.x), e.y = ex2(e.y);
+                                if (k & 1)
+                                    lb = add_f2(lb, f2(e.x, e.y));
+                                else
+                                    la = add_f2(la, f2(e.x, e.y));
+                                o[k] = pack2<BF16>(e.x, e.y);
+                            }
+                            ptx::tmem_st16(s_now + 16 * c, o);   // S is in registers: P may cover it before the check
                         }
                         const float2 ls = un2(add_f2(la, lb));
                         sum = ls.x + ls.y;
                         if (again || !__any_sync(0xffffffffu, !(sum < 16384.f))) break;
                         again = true;
+                        ptx::tmem_wait_st();   // the second P is stored over the first
                     }
                     if (!ok) break;
                     l += sum;
-                    ptx::tmem_st32(s_now, o);
                     ptx::tmem_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(p_full(i, n & 1u));
                 }
-                if (ok) ok = __all_sync(0xffffffffu, wait(o_done(i), (n - 1) & 1u, DEVICE_TIMEOUT_EPILOGUE));
+                if (ok) ok = __all_sync(0xffffffffu, wait(o_done(i, (n - 1) & 1u), (n - 1) >> 1 & 1u, DEVICE_TIMEOUT_EPILOGUE));
                 ptx::tc_fence_after();
             }
             // ---- the item's result, or this block's part of it
