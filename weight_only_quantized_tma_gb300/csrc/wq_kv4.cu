@@ -70,9 +70,9 @@ __device__ __forceinline__ GroupPlace group_place(const Kv4RowsParams& p, int la
 // cost four packed operations: the difference, a multiply-add whose rounding gives the
 // integer, that integer and its exact residual; only where the largest residual reaches
 // half a step (ties, and the products that rounded the wrong way) is the exact search above
-// run.  Bound by instructions until the rows of a token shared their addresses and the
-// arithmetic was packed (118 us for 16384 tokens of 32 heads of 128 before).
-template <bool BF16, int D, int HP>
+// run.  Bound by instructions (16384 tokens of 32 heads of 128, 344 MB: 118 us with an address
+// and unpacked arithmetic for each row, now 92 us, the issue slots 80% full).
+template <bool BF16, int D, int G, int HP>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
             }
         }
     }
-    const int pair_at = ((lane * 8) >> p.c.g_shift) * 4;
-    const bool first = ((lane * 8) & (p.c.G - 1)) == 0;
+    const int pair_at = lane * 8 / G * 4;
+    const bool first = lane * 8 % G == 0;
 #pragma unroll
     for (int u = 0; u < HP; ++u)
 #pragma unroll
@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
             const uint32_t words[4] = {raw[u][which].x, raw[u][which].y, raw[u][which].z, raw[u][which].w};
             uint32_t mn = min2_nan<BF16>(min2_nan<BF16>(words[0], words[1]), min2_nan<BF16>(words[2], words[3]));
             uint32_t mx = max2_nan<BF16>(max2_nan<BF16>(words[0], words[1]), max2_nan<BF16>(words[2], words[3]));
-            for (int off = p.c.G / 16; off > 0; off >>= 1) {
+#pragma unroll
+            for (int off = G / 16; off > 0; off >>= 1) {
                 mn = min2_nan<BF16>(mn, __shfl_xor_sync(0xffffffffu, mn, off));
                 mx = max2_nan<BF16>(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             }
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
                 const uint64_t lo2 = f2(-lo, -lo), inv2 = f2(inv, inv), s2 = f2(-s, -s);
                 const uint64_t big = f2(12582912.0f, 12582912.0f), small = f2(-12582912.0f, -12582912.0f);   // 1.5 * 2^23
                 float2 q[4];
-                float worst = 0.f;
+                float worst = 0.f, worst1 = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = unpack2<BF16>(words[i]);
@@ -130,11 +131,12 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
                     const uint64_t n = add_f2(fma_f2(d, inv2, big), small);    // rounded to an integer
                     const float2 e = un2(fma_f2(n, s2, d));
                     q[i] = un2(n);
-                    worst = max3(worst, fabsf(e.x), fabsf(e.y));
+                    worst = fmaxf(worst, fabsf(e.x));
+                    worst1 = fmaxf(worst1, fabsf(e.y));
                 }
                 // (steps below 1e-30 and codes past 15, which only subnormal steps have, take
                 // the search too)
-                if (worst < 0.5f * s && s >= 1e-30f && range <= 15.4f * s) {
+                if (fmaxf(worst, worst1) < 0.5f * s && s >= 1e-30f && range <= 15.4f * s) {
                     // four codes as one integer below 2^16, in the low bits of 2^23 + it
                     const float a = fmaf(fmaf(fmaf(q[1].y, 16.f, q[1].x), 16.f, q[0].y), 16.f, q[0].x + 8388608.f);
                     const float b = fmaf(fmaf(fmaf(q[3].y, 16.f, q[3].x), 16.f, q[2].y), 16.f, q[2].x + 8388608.f);
@@ -156,7 +158,8 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
         }
 }
 
-// The inverse: one lane turns a word of codes into 8 values (16 bytes out).
+// The inverse: one lane turns a word of codes into 8 values (16 bytes out).  Bound by memory:
+// 50001 tokens of 8 heads of 128, 269 MB, in 42 us (6.5 TB/s).
 template <bool BF16, int D, int HP>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p) {
     ptx::grid_dependency_wait();
@@ -195,8 +198,10 @@ cudaError_t rows_launch(Kv4RowsParams p, bool write, cudaStream_t st) {
     const int64_t all = p.T * groups, per = 256 / (D / 8);
     p.div_groups = make_fastdiv(groups, (uint32_t)(all + 256));
     const unsigned grid = (unsigned)((all + per - 1) / per);
-    return write ? launch_pdl(kv4_write_kernel<BF16, D, HP>, grid, 256, 0, st, p)
-                 : launch_pdl(kv4_read_kernel<BF16, D, HP>, grid, 256, 0, st, p);
+    if (!write) return launch_pdl(kv4_read_kernel<BF16, D, HP>, grid, 256, 0, st, p);
+    if (p.c.G == 32) return launch_pdl(kv4_write_kernel<BF16, D, 32, HP>, grid, 256, 0, st, p);
+    if (p.c.G == 64) return launch_pdl(kv4_write_kernel<BF16, D, 64, HP>, grid, 256, 0, st, p);
+    return launch_pdl(kv4_write_kernel<BF16, D, D == 128 ? 128 : 64, HP>, grid, 256, 0, st, p);
 }
 
 template <int HP>

@@ -19,9 +19,10 @@ __device__ __forceinline__ void load4(const uint16_t* p, float (&x)[4]) {
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
-// One group of LPR lanes takes one token and `per` of its heads, U at a time: the U rows'
-// loads are all issued before the first is used, and the token's angles are read once for
-// all of them (with one row for each group, 8192 tokens of 64 heads took 73.7 us).
+// One group of LPR lanes takes `per` query heads or `per` key heads of one token, U at a time:
+// the U rows' loads are all issued before the first is used, and the token's angles, the
+// weight and the addresses are worked out once for all of them (one row for each group: 73.7
+// us for 8192 tokens of 64 heads; now 53 us, 273 MB at 5.1 TB/s).
 template <bool BF16, int LPR, int U>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     ptx::grid_dependency_wait();
@@ -29,9 +30,11 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     const int lane = threadIdx.x % LPR;
     const uint32_t group = blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
     const uint32_t tok = fastdiv(group, p.div_groups);
-    const int h_begin = (int)(group - tok * p.div_groups.d) * p.per;
-    const int heads = p.Hq + p.Hkv;
+    const int gi = (int)(group - tok * p.div_groups.d);
     const int64_t t = tok;
+    const bool is_q = gi < p.q_groups;
+    const int h_begin = (is_q ? gi : gi - p.q_groups) * p.per;
+    const int heads = min(p.per, (is_q ? p.Hq : p.Hkv) - h_begin);
     bool active = t < p.T && lane * 8 < p.D;
     int64_t pos = 0;
     if (t < p.T) {
@@ -41,6 +44,11 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
             active = false;
         }
     }
+    const uint16_t* src = (is_q ? static_cast<const uint16_t*>(p.q) + t * p.q_stride
+                                : static_cast<const uint16_t*>(p.k) + t * p.k_stride) + h_begin * p.D;
+    uint16_t* dst = (is_q ? static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride
+                          : static_cast<uint16_t*>(p.k_out) + t * p.k_out_stride) + h_begin * p.D;
+    const uint16_t* w = static_cast<const uint16_t*>(is_q ? p.q_weight : p.k_weight);
     // the two chunks (in values)
     const int pairs = p.rot >> 3;               // lanes with rotated chunks
     const bool turns = active && lane < pairs;
@@ -63,26 +71,23 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
         }
     }
     const float inv_d = 1.0f / (float)p.D;
-    for (int h0 = h_begin; h0 < h_begin + p.per; h0 += U) {   // the same count for every lane
+    float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
+    if (w != nullptr && active) {
+        load4<BF16>(w + ca, wa);
+        load4<BF16>(w + cb, wb);
+    }
+    for (int h0 = 0; h0 < p.per; h0 += U) {   // the same count for every lane
         uint2 ra[U], rb[U];
-        bool live[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u;
-            live[u] = active && h < heads;
             ra[u] = rb[u] = make_uint2(0u, 0u);
-            if (live[u]) {
-                const bool is_q = h < p.Hq;
-                const uint16_t* src = is_q ? static_cast<const uint16_t*>(p.q) + t * p.q_stride + (int64_t)h * p.D
-                                           : static_cast<const uint16_t*>(p.k) + t * p.k_stride + (int64_t)(h - p.Hq) * p.D;
-                ra[u] = *reinterpret_cast<const uint2*>(src + ca);
-                rb[u] = *reinterpret_cast<const uint2*>(src + cb);
+            if (active && h0 + u < heads) {
+                ra[u] = *reinterpret_cast<const uint2*>(src + (h0 + u) * p.D + ca);
+                rb[u] = *reinterpret_cast<const uint2*>(src + (h0 + u) * p.D + cb);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u;
-            const bool is_q = h < p.Hq;
             float a[4], b[4];
             const float2 a0 = unpack2<BF16>(ra[u].x), a1 = unpack2<BF16>(ra[u].y);
             const float2 b0 = unpack2<BF16>(rb[u].x), b1 = unpack2<BF16>(rb[u].y);
@@ -94,13 +99,9 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
             for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
 #pragma unroll
             for (int off = LPR / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (!live[u]) continue;
-            const uint16_t* w = static_cast<const uint16_t*>(is_q ? p.q_weight : p.k_weight);
+            if (!active || h0 + u >= heads) continue;
             if (w != nullptr) {
                 const float r = rsqrtf(sum * inv_d + p.eps);
-                float wa[4], wb[4];
-                load4<BF16>(w + ca, wa);
-                load4<BF16>(w + cb, wb);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     a[i] = a[i] * r * wa[i];
@@ -126,19 +127,18 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
                     }
                 }
             }
-            uint16_t* dst = is_q ? static_cast<uint16_t*>(p.q_out) + t * p.q_out_stride + (int64_t)h * p.D
-                                 : static_cast<uint16_t*>(p.k_out) + t * p.k_out_stride + (int64_t)(h - p.Hq) * p.D;
-            *reinterpret_cast<uint2*>(dst + ca) = make_uint2(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]));
-            *reinterpret_cast<uint2*>(dst + cb) = make_uint2(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]));
+            uint16_t* out = dst + (h0 + u) * p.D;
+            *reinterpret_cast<uint2*>(out + ca) = make_uint2(pack2<BF16>(a[0], a[1]), pack2<BF16>(a[2], a[3]));
+            *reinterpret_cast<uint2*>(out + cb) = make_uint2(pack2<BF16>(b[0], b[1]), pack2<BF16>(b[2], b[3]));
         }
     }
 }
 
 template <bool BF16, int LPR, int U>
 cudaError_t launch_u(RopeParams p, int per, cudaStream_t st) {
-    const int heads = p.Hq + p.Hkv;
     p.per = per;
-    const uint32_t groups = (uint32_t)((heads + per - 1) / per);
+    p.q_groups = (p.Hq + per - 1) / per;
+    const uint32_t groups = (uint32_t)(p.q_groups + (p.Hkv + per - 1) / per);
     const int64_t all = p.T * groups;
     p.div_groups = make_fastdiv(groups, (uint32_t)(all + 256));
     return launch_pdl(qk_norm_rope_kernel<BF16, LPR, U>, (unsigned)((all * LPR + 255) / 256), 256, 0, st, p);
@@ -146,12 +146,13 @@ cudaError_t launch_u(RopeParams p, int per, cudaStream_t st) {
 
 template <bool BF16, int LPR>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t st) {
-    // As many heads for each group as leave two full blocks for each SM: 8 read the angles
-    // least often, 1 spreads a decode step's few rows widest.
+    // As many heads for each group as leave two full blocks for each SM: 16 read the angles and
+    // the weight least often, 1 spreads a decode step's few rows widest.  (8192 tokens of 32
+    // query and 32 key heads of 128, rows in flight x heads: 2 x 16 53 us, 2 x 8 55, 2 x 32 57,
+    // 4 x 8 63, 4 x 16 63, 1 x 16 66, 2 x 2 70.)
     const int64_t want = (int64_t)sms * 2 * (256 / LPR);
-    const int heads = p.Hq + p.Hkv;
-    if (p.T * ((heads + 7) / 8) >= want) return launch_u<BF16, LPR, 4>(p, 8, st);
-    if (p.T * ((heads + 3) / 4) >= want) return launch_u<BF16, LPR, 4>(p, 4, st);
+    for (int per = 16; per >= 4; per /= 2)
+        if (p.T * ((p.Hq + per - 1) / per + (p.Hkv + per - 1) / per) >= want) return launch_u<BF16, LPR, 2>(p, per, st);
     return launch_u<BF16, LPR, 1>(p, 1, st);
 }
 
