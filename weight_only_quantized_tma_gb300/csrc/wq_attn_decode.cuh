@@ -520,13 +520,10 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                         if (g == 0)
                             __stcg(reinterpret_cast<float2*>(slot + R * D) + r, make_float2(m[nt][i], l[nt][i]));
                     }
-                __threadfence();
                 __syncwarp();
                 if (lane == 0) {
-                    const uint32_t before = atomicAdd(p.ws_count + b_first, 1u);
-                    const int last = before + 1 == (uint32_t)parts;
+                    const int last = arrive_ticket(p.ws_count + b_first) + 1 == (uint32_t)parts;
                     if (last) p.ws_count[b_first] = 0u;
-                    __threadfence();
                     *last_flag = last;
                 }
             } else if (lane == 0) {
@@ -536,7 +533,6 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         if (!whole) {
             ptx::named_barrier_sync(1, 128);
             if (*last_flag) {
-                __threadfence();
                 merge_parts<BF16, D, R, R, 128>(p, w, b_first, parts, reinterpret_cast<float*>(smem + C::OFF_W),
                                              threadIdx.x, 1);
             }

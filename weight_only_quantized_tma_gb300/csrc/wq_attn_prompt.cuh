@@ -535,21 +535,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 if (lane == 0) ptx::mbar_arrive(o_empty(i));
             }
             if (!whole) {
-                __threadfence();
                 ptx::named_barrier_sync(1, 256);
                 if (threadIdx.x == 0) {
                     int last = 0;
                     if (ok) {
-                        const uint32_t before = atomicAdd(p.ws_count + b_first, 1u);
-                        last = before + 1 == (uint32_t)parts;
+                        last = arrive_ticket(p.ws_count + b_first) + 1 == (uint32_t)parts;
                         if (last) p.ws_count[b_first] = 0u;
-                        __threadfence();
                     }
                     *last_flag = last;
                 }
                 ptx::named_barrier_sync(1, 256);
                 if (*last_flag) {
-                    __threadfence();
                     merge_parts<BF16, D, R, C::MERGE_ROWS, 256>(p, w, b_first, parts,
                                                                 reinterpret_cast<float*>(smem + C::OFF_Q), threadIdx.x, 1);
                 }

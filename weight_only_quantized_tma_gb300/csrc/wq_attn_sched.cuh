@@ -14,6 +14,12 @@
 
 namespace wq {
 
+// 64-bit tile numbers almost always fit 32 bits, where a division is several times shorter.
+__device__ __forceinline__ int64_t div_short(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 struct SeqInfo {
     int q0;      // first query row of q
     int n;       // new tokens
@@ -47,8 +53,11 @@ struct Span {
 template <int R, int TN>
 __device__ __forceinline__ Span row_tile_span(const AttnParams& p, const SeqInfo& s, int rt) {
     const int64_t rows = (int64_t)s.n * p.group;
-    const int first = (int)((int64_t)rt * R / p.group);
-    const int last = (int)((min((int64_t)(rt + 1) * R, rows) - 1) / p.group);
+    int first = 0, last = s.n - 1;
+    if (s.tiles > 1) {
+        first = (int)div_short((int64_t)rt * R, p.group);
+        last = (int)div_short(min((int64_t)(rt + 1) * R, rows) - 1, p.group);
+    }
     Span v;
     v.hi = p.causal ? max(0, min(s.L, s.L - s.n + last + 1)) : s.L;
     v.lo = p.window > 0 ? max(0, s.L - s.n + first + 1 - p.window) : 0;
@@ -80,12 +89,6 @@ struct Walk {
     int units;             // of the item
 };
 
-// 64-bit tile numbers almost always fit 32 bits, where a division is several times shorter.
-__device__ __forceinline__ int64_t div_short(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 // Run i of `used` runs of `total` tiles begins at tile run_begin: the first total % used
 // runs are one tile longer.
 struct Runs {
@@ -102,6 +105,32 @@ __device__ __forceinline__ int run_of(const Runs& r, int64_t u) {
     return (int)(u < edge ? div_short(u, r.len + 1) : r.longer + div_short(u - edge, r.len));
 }
 
+// Sum and inclusive prefix over a warp; 32-bit shuffles where no lane holds much.
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+    if (__all_sync(0xffffffffu, x < (1 << 26))) return (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+__device__ __forceinline__ int64_t warp_prefix(int64_t x) {
+    const int lane = threadIdx.x & 31;
+    if (__all_sync(0xffffffffu, x < (1 << 26))) {
+        int y = (int)x;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, y, off);
+            if (lane >= off) y += v;
+        }
+        return y;
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, x, off);
+        if (lane >= off) x += v;
+    }
+    return x;
+}
+
 // Executed by a full warp.  How the tiles are cut into runs, and this block's walk.
 template <int R, int TN>
 __device__ __forceinline__ Runs walk_begin(const AttnParams& p, int block, int blocks, Walk& w) {
@@ -109,10 +138,7 @@ __device__ __forceinline__ Runs walk_begin(const AttnParams& p, int block, int b
     int64_t total = 0, mine = 0;
     for (int64_t b0 = 0; b0 < p.B; b0 += 32) {
         mine = seq_units<R, TN>(p, (int)(b0 + lane));
-        int64_t sum = mine;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        total += sum;
+        total += warp_sum(mine);
     }
     const int used = (int)min((int64_t)blocks, total);
     w.u = w.u1 = 0;
@@ -123,12 +149,7 @@ __device__ __forceinline__ Runs walk_begin(const AttnParams& p, int block, int b
     int64_t base = 0;
     for (int64_t b0 = 0; b0 < p.B; b0 += 32) {
         if (p.B > 32) mine = seq_units<R, TN>(p, (int)(b0 + lane));
-        int64_t upto = mine;   // inclusive prefix
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += v;
-        }
+        const int64_t upto = warp_prefix(mine);
         const uint32_t m = __ballot_sync(0xffffffffu, base + upto > w.u);
         if (m) {
             const int l = __ffs(m) - 1;
@@ -186,6 +207,13 @@ __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// Arrival on an item's counter: what this thread has written, or seen written through a
+// barrier, is visible to whoever arrives later.
+__device__ __forceinline__ uint32_t arrive_ticket(uint32_t* count) {
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+    return before;
 }
 // weight of a part with maximum m under the common maximum M (log2 domain)
 __device__ __forceinline__ float part_weight(float m, float M) { return m == -INFINITY ? 0.0f : ex2(m - M); }
