@@ -177,6 +177,7 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
         table_stride > kMaxTokens || window < 0 || (window > 0 && !causal) || !std::isfinite(scale))
         return WQ_ERR_SHAPE;
     if (!cu_q && T != B) return WQ_ERR_SHAPE;
+    if (T * (q_heads / p.c.heads) >= kMaxTokens - 4096) return WQ_ERR_SHAPE;
     if (T == 0 || B == 0) return WQ_OK;
     if (!q || !out || !kv_lens || (!block_table && table_stride > 0) || (!pages && p.c.num_pages > 0)) return WQ_ERR_NULL;
     const int64_t row = (int64_t)q_heads * p.c.D;
@@ -200,6 +201,7 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
     p.T = T;
     p.Hq = q_heads;
     p.group = q_heads / p.c.heads;
+    p.div_group = make_fastdiv((uint32_t)p.group, (uint32_t)kMaxTokens);
     p.causal = causal != 0;
     p.window = window;
     p.scale = scale;

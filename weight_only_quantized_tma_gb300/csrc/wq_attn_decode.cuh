@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
     uint32_t qr[C::Q_SMEM ? 1 : KS][2];
 
     for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
-        const int rows = (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R);
+        const int rows = min(R, w.s.n * p.group - w.rt * R);
         // ---- Q operands of the item, in the order of the codes
         auto load_q = [&](int nt, uint32_t (&q)[KS][2]) {
             const int r = nt * 8 + g;
@@ -191,10 +191,9 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
             if (r < rows) {
-                const int64_t row = (int64_t)w.rt * R + r;
-                const int64_t t = w.s.q0 + row / p.group;
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + t * p.q_stride +
-                                      (int64_t)(w.head * p.group + (int)(row % p.group)) * D + c * (D / 4);
+                const int row = w.rt * R + r, qt = row_token(p, row);
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(w.s.q0 + qt) * p.q_stride +
+                                      (w.head * p.group + row - qt * p.group) * D + c * (D / 4);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * i);
@@ -227,14 +226,13 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t row = (int64_t)w.rt * R + nt * 8 + 2 * c + i;
-                const int pos = w.s.L - w.s.n + (int)(row / p.group);
+                const int pos = w.s.L - w.s.n + row_token(p, w.rt * R + nt * 8 + 2 * c + i);
                 hi[nt][i] = p.causal ? min(w.s.L, pos + 1) : w.s.L;
                 lo[nt][i] = p.window > 0 ? pos + 1 - p.window : 0;
             }
         // tokens that every row sees
-        const int pos0 = w.s.L - w.s.n + (int)((int64_t)w.rt * R / p.group);
-        const int pos1 = w.s.L - w.s.n + (int)(((int64_t)w.rt * R + rows - 1) / p.group);
+        const int pos0 = w.s.L - w.s.n + row_token(p, w.rt * R);
+        const int pos1 = w.s.L - w.s.n + row_token(p, w.rt * R + rows - 1);
         const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
         const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
 
@@ -488,9 +486,9 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                     for (int i = 0; i < 2; ++i) {
                         const int r = nt * 8 + 2 * c + i;
                         if (r >= rows) continue;
-                        const int64_t row = (int64_t)w.rt * R + r;
-                        const int64_t t = w.s.q0 + row / p.group;
-                        const int head = w.head * p.group + (int)(row % p.group);
+                        const int row = w.rt * R + r, qt = row_token(p, row);
+                        const int64_t t = w.s.q0 + qt;
+                        const int head = w.head * p.group + row - qt * p.group;
                         const float inv = l[nt][i] == 0.f ? 0.f : up / l[nt][i];
                         uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride + (int64_t)head * D + g * (D / 8);
 #pragma unroll

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         if (ok) ok = bounded_wait(bar, parity, abort_flag, p.status, code, p.timeout_ns);
         return ok;
     };
-    auto item_rows = [&]() { return (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R); };
+    auto item_rows = [&]() { return min(R, w.s.n * p.group - w.rt * R); };
     auto tile_begin = [&]() { return w.v.t0 + (int)(w.u - w.item0); };
     auto tile_end = [&]() { return w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0); };
 
@@ -303,8 +303,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         uint32_t ph = 0, n = 0;                    // n: tiles so far, slot n % 4
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows(), te = tile_end();
-            const int pos0 = w.s.L - w.s.n + (int)((int64_t)w.rt * R / p.group);
-            const int pos1 = w.s.L - w.s.n + (int)(((int64_t)w.rt * R + rows - 1) / p.group);
+            const int pos0 = w.s.L - w.s.n + row_token(p, w.rt * R);
+            const int pos1 = w.s.L - w.s.n + row_token(p, w.rt * R + rows - 1);
             const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
             const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
             for (int t = tile_begin(); t < te; ++t, ++n) {
@@ -374,10 +374,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         for (; w.u < w.u1; walk_next<R, TN>(p, w)) {
             const int rows = item_rows();
             const bool idle = 128 * i >= rows;       // no rows in this tile
-            const int64_t row = (int64_t)w.rt * R + min(r, rows - 1);
-            const int qt = (int)(row / p.group);
+            const int row = w.rt * R + min(r, rows - 1);
+            const int qt = row_token(p, row);
             const int64_t tq = w.s.q0 + qt;
-            const int head = w.head * p.group + (int)(row % p.group);
+            const int head = w.head * p.group + row - qt * p.group;
             const int pos = w.s.L - w.s.n + qt;
             const int hi = p.causal ? min(w.s.L, pos + 1) : w.s.L;
             const int lo = p.window > 0 ? pos + 1 - p.window : 0;

@@ -41,8 +41,13 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     const int64_t most = p.table_stride << p.c.p_shift;
     const int L = p.lens[b];
     s.L = (int)min((int64_t)max(L, 0), most);
-    s.tiles = (int)(((int64_t)s.n * p.group + R - 1) / R);
+    s.tiles = (int)(((uint32_t)(s.n * p.group) + R - 1) / R);
     return s;
+}
+
+// The query token of a row; its head follows from the rest.
+__device__ __forceinline__ int row_token(const AttnParams& p, int row) {
+    return (int)fastdiv((uint32_t)row, p.div_group);
 }
 
 struct Span {
@@ -52,12 +57,8 @@ struct Span {
 
 template <int R, int TN>
 __device__ __forceinline__ Span row_tile_span(const AttnParams& p, const SeqInfo& s, int rt) {
-    const int64_t rows = (int64_t)s.n * p.group;
-    int first = 0, last = s.n - 1;
-    if (s.tiles > 1) {
-        first = (int)div_short((int64_t)rt * R, p.group);
-        last = (int)div_short(min((int64_t)(rt + 1) * R, rows) - 1, p.group);
-    }
+    const int rows = s.n * p.group;
+    const int first = row_token(p, rt * R), last = row_token(p, min((rt + 1) * R, rows) - 1);
     Span v;
     v.hi = p.causal ? max(0, min(s.L, s.L - s.n + last + 1)) : s.L;
     v.lo = p.window > 0 ? max(0, s.L - s.n + first + 1 - p.window) : 0;
@@ -227,7 +228,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Walk& w, 
     constexpr int CH = D / 4;                       // float4 chunks of a row
     constexpr int PER = (RB * CH + NTHR - 1) / NTHR;
     constexpr int NW = NTHR / 32, RW = (RB + NW - 1) / NW;
-    const int all = (int)min((int64_t)R, (int64_t)w.s.n * p.group - (int64_t)w.rt * R);
+    const int all = min(R, w.s.n * p.group - w.rt * R);
     const int warp = tid >> 5, lane = tid & 31;
     // the first part is what its block left unfinished, the others what theirs continued
     auto slot = [&](int j) {
@@ -287,9 +288,8 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Walk& w, 
             if (lane == 0 && r < rows) {
                 weights[r * 33] = lsum[k];
                 if (p.lse != nullptr) {
-                    const int64_t row = (int64_t)w.rt * R + r0 + r;
-                    const int64_t t = w.s.q0 + row / p.group;
-                    p.lse[t * p.Hq + w.head * p.group + (int)(row % p.group)] =
+                    const int row = w.rt * R + r0 + r, qt = row_token(p, row);
+                    p.lse[(int64_t)(w.s.q0 + qt) * p.Hq + w.head * p.group + row - qt * p.group] =
                         lsum[k] == 0.f ? -INFINITY : (mrun[k] + log2f(lsum[k])) * 0.6931471805599453f;
                 }
             }
@@ -300,10 +300,9 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Walk& w, 
             const int idx = tid + i * NTHR, r = idx / CH, ch = idx % CH;
             if (r >= rows) continue;
             const float l = weights[r * 33], inv = l == 0.f ? 0.f : 1.f / l;
-            const int64_t row = (int64_t)w.rt * R + r0 + r;
-            const int64_t t = w.s.q0 + row / p.group;
-            uint16_t* out = static_cast<uint16_t*>(p.out) + t * p.out_stride +
-                            (int64_t)(w.head * p.group + (int)(row % p.group)) * D + ch * 4;
+            const int row = w.rt * R + r0 + r, qt = row_token(p, row);
+            uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(w.s.q0 + qt) * p.out_stride +
+                            (w.head * p.group + row - qt * p.group) * D + ch * 4;
             *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(acc[i].x * inv, acc[i].y * inv),
                                                         pack2<BF16>(acc[i].z * inv, acc[i].w * inv));
         }

@@ -290,6 +290,7 @@ struct AttnParams {
     int64_t table_stride;
     int64_t B, T;
     int Hq, group;                  // query heads, query heads for each key head
+    FastDiv div_group;              // rows (query token x head of a group, below 2^31) to tokens
     int causal, window;
     float scale;
     uint32_t* ws_count;
