@@ -319,8 +319,8 @@ wq_status wq_gemm_bf16_fp4(const void* A, const uint8_t* w_e2m1, const uint8_t* 
  * token are contiguous), so q and k may be slices of one packed projection.  An output may
  * be its own input (same pointer and stride); any other overlap is undefined.
  * Requirements: T >= 0, Hq >= 1, Hkv >= 1, D % 8 == 0, 8 <= D <= 256, rot % 8 == 0,
- * 8 <= rot <= D, eps >= 0, strides >= heads * D and multiples of 4; pointers 8-byte
- * aligned, cos_sin 16-byte aligned. */
+ * 8 <= rot <= D, eps >= 0, T * (Hq + Hkv) < 2^31 - 4097, strides >= heads * D and
+ * multiples of 4; pointers 8-byte aligned, cos_sin 16-byte aligned. */
 wq_status wq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, wq_dtype dtype,
                           int64_t T, int32_t Hq, int32_t Hkv, int32_t D, const void* q_weight, const void* k_weight,
                           float eps, const int64_t* positions, const float* cos_sin, int64_t max_pos, int32_t rot,
@@ -360,8 +360,8 @@ wq_status wq_kv4_page_bytes(const wq_kv4_layout* layout, size_t* bytes);
  * overflow the type, s is the next number below.  A group that holds an
  * infinity or a NaN, or whose range overflows fp32, is stored as NaN throughout and
  * touches no other group.
- * Requirements: T >= 0, strides >= kv_heads * D and multiples of 8; k, v and pages
- * 16-byte aligned, slots 8-byte aligned. */
+ * Requirements: 0 <= T * kv_heads < 2^31 - 4097, strides >= kv_heads * D and multiples
+ * of 8; k, v and pages 16-byte aligned, slots 8-byte aligned. */
 wq_status wq_kv4_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots,
                        int64_t T, const wq_kv4_layout* layout, uint8_t* pages, wq_stream_t stream);
 
@@ -389,14 +389,16 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  * call replays with new lengths.  max_q bounds n for the choice of kernel (a larger n is
  * still right).  Lengths are cut to table_stride * P (a longer one sets the index bit of
  * the device status), decreasing cu_q counts as n = 0, rows past T do not exist, and a
- * page outside the cache sets the index bit (page 0 is read in its place).
+ * page outside the cache sets the index bit (page 0 is read in its place).  Rows of out
+ * and lse that belong to no sequence are left as they were.
  * q_stride / out_stride: elements from token to token.  Results do not change from run to
  * run.  ws: at least wq_attn_kv4_workspace_bytes bytes, 16-byte aligned; its first 16 KiB
  * hold arrival counters: zero-fill them once, every call leaves them zero; calls that
  * share a workspace must not overlap on the GPU.
  * Requirements: B >= 0, T >= 0, q_heads a multiple of kv_heads, window >= 0 and 0 unless
- * causal, scale finite, 1 <= max_q, strides >= q_heads * D and multiples of 8; q, out
- * and pages 16-byte aligned, the int32 arrays and lse 4-byte aligned. */
+ * causal, scale finite, 1 <= max_q, T * q_heads / kv_heads < 2^31 - 4097, strides >=
+ * q_heads * D and multiples of 8; q, out and pages 16-byte aligned, the int32 arrays and
+ * lse 4-byte aligned. */
 wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const int32_t* cu_q, int64_t B, int64_t T,
                       int64_t max_q, const uint8_t* pages, const wq_kv4_layout* layout, const int32_t* block_table,
                       int64_t table_stride, const int32_t* kv_lens, float scale, int32_t causal, int32_t window,

@@ -89,3 +89,12 @@ def test_attention_refusals(L):
     for kw, status in BAD_LAYOUTS:
         assert f(l=lay(**kw)) == status
     assert f(T=0, cu=None, B=0, q=None) == OK
+
+
+def test_row_numbers_stay_within_31_bits(L):
+    """Rows (a token's head) are counted in 32 bits on the device: more of them are refused, not wrapped."""
+    T = 1 << 30     # two heads of each token: 2^31 rows
+    assert L.wq_qk_norm_rope(P, 128, P, 128, 0, T, 1, 1, 128, None, None, 1e-6, P, P, 8, 128, 0, P, 128, P, 128, None) == SHAPE
+    assert L.wq_kv4_write(P, 256, P, 256, P, T, lay(), P, None) == SHAPE
+    assert L.wq_kv4_read(P, lay(), P, T, P, 256, P, 256, None) == SHAPE
+    assert L.wq_attn_kv4(P, 512, 4, P, 2, T, T, P, lay(), P, 8, P, 1.0, 1, 0, P, 512, None, None, 0, None) == SHAPE

@@ -7,15 +7,20 @@
 namespace wq {
 namespace {
 
+constexpr int kMaxDevices = 64;
+
 template <bool BF16, int D, int NT>
 struct Launcher {
     using C = DecodeCfg<D, NT>;
     static int stage_bytes(const Kv4View& c) { return (kDecodeTN * (D + 8 * (D / c.G)) + 127) / 128 * 128; }
     static int smem(const Kv4View& c) { return C::OFF_RING + kDecodeStages * stage_bytes(c); }
     static int blocks_per_sm(const Kv4View& c) {
-        // resident blocks for each group size; asked once for each instantiation
-        static std::atomic<int> known[3];
-        std::atomic<int>& k = known[c.g_shift - 5];
+        // resident blocks for each group size; asked (and the kernel's shared memory allowed) once for
+        // each instantiation and device
+        static std::atomic<int> known[kMaxDevices][3];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+        std::atomic<int>& k = known[dev][c.g_shift - 5];
         int n = k.load(std::memory_order_relaxed);
         if (n == 0) {
             const int bytes = smem(c);

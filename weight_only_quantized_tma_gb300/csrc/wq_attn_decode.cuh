@@ -21,9 +21,10 @@
 // side) with their own maximum, sum and O, and meet once for each item; warp 4 copies page
 // blocks into a ring with bulk copies.
 //
-// Measured: 64 sequences of 300 to 16384 tokens, 32 query and 8 key heads of 128, bf16: 148 us
-// for 582 MB (3.9 TB/s); copies alone take 100 us, arithmetic alone 138 us, so what bounds it
-// is the latency between a warp's instructions (issue slots 53% full), not a unit.
+// Measured: 64 sequences of 300 to 16384 tokens, 32 query and 8 key heads of 128, bf16: 142 us
+// for 582 MB (4.1 TB/s); when it took 148 us, copies alone took 100 and arithmetic alone 138,
+// so what bounds it is the latency between a warp's instructions (issue slots 56% full), not a
+// unit.
 #pragma once
 
 #include "wq_attn_sched.cuh"
