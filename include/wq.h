@@ -387,10 +387,10 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  * their out NaN, a value at least the places where it stands.
  * kv_lens, cu_q and block_table are read on the device: a CUDA graph that captured the
  * call replays with new lengths.  max_q bounds n for the choice of kernel (a larger n is
- * still right).  Lengths are cut to table_stride * P (a longer one sets the index bit of
- * the device status), decreasing cu_q counts as n = 0, rows past T do not exist, and a
- * page outside the cache sets the index bit (page 0 is read in its place).  Rows of out
- * and lse that belong to no sequence are left as they were.
+ * still right).  Lengths are cut to table_stride * P and to 2^31 - 4097 (a longer one
+ * sets the index bit of the device status), decreasing cu_q counts as n = 0, rows past
+ * T do not exist, and a page outside the cache sets the index bit (page 0 is read in
+ * its place).  Rows of out and lse that belong to no sequence are left as they were.
  * q_stride / out_stride: elements from token to token.  Results do not change from run to
  * run.  ws: at least wq_attn_kv4_workspace_bytes bytes, 16-byte aligned; its first 16 KiB
  * hold arrival counters: zero-fill them once, every call leaves them zero; calls that

@@ -340,3 +340,21 @@ def test_empty_and_refusals():
               dict(ws=torch.zeros(64, dtype=torch.uint8, device="cuda")[1:17])):
         with pytest.raises(wq.WQError):
             wq.wq_attn_kv4(**{**ok, **b})
+
+
+def test_foreign_workspaces_are_refused():
+    p = Problem([30, 20], [1, 1], 4, 2, 64, 32, 16, "f16", seed=20)
+    call = dict(q=p.dq, pages=p.pages, block_table=p.table, kv_lens=p.kv_lens, group=32, page_size=16)
+    for ws in (torch.zeros(1 << 26, dtype=torch.uint8), torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")[::2], 0):
+        with pytest.raises(ValueError):
+            wq.wq_attn_kv4(**call, ws=ws)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [100, 200], [9, 210], [350, 12]])   # more queries than tokens, too
+def test_windows_beyond_every_length(news):
+    p = Problem([300, 200], news, 4, 2, 64, 32, 16, "bf16", seed=21)
+    call = dict(q=p.dq, pages=p.pages, block_table=p.table, kv_lens=p.kv_lens, group=32, page_size=16, cu_q=p.cu,
+                max_q=max(news))
+    whole = wq.wq_attn_kv4(**call)
+    for window in (300, (1 << 31) - 1, 1 << 31, (1 << 32) + 5):
+        assert torch.equal(wq.wq_attn_kv4(**call, window=window), whole)

@@ -203,6 +203,7 @@ def wq_kv4_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, group: 
 
 # ------------------------------------------------------------------ attention
 
+_LONGEST = (1 << 31) - 1   # no sequence is longer, so a longer window is this one
 _ws_need: dict = {}
 _ws_cache: dict = {}
 
@@ -266,9 +267,11 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
     if ws is None:
         ws, ws_bytes = attn_kv4_workspace(layout, Hq, max_q, dev, stream)
     else:
+        if not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {dev}")
         ws_bytes = ws.numel() * ws.element_size()
     _call("wq_attn_kv4", q.data_ptr(), q_step, Hq, None if cu_q is None else cu_q.data_ptr(), B, T, max_q,
           pages.data_ptr(), layout[1], block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(),
-          D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), out_step,
+          D ** -0.5 if scale is None else scale, int(causal), min(window, _LONGEST), out.data_ptr(), out_step,
           None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, stream)
     return out

@@ -197,6 +197,7 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
     p.lens = kv_lens;
     // without pages no token is cached: every length is cut to 0
     p.table_stride = p.c.num_pages > 0 ? table_stride : 0;
+    p.most = (int)std::min(p.table_stride << p.c.p_shift, kMaxTokens - 4096);
     p.B = B;
     p.T = T;
     p.Hq = q_heads;

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
         bool ok = true;
         uint32_t issued = 0;
         for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
-            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > (p.table_stride << p.c.p_shift))
+            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > p.most)
                 atomicOr(p.status, DEVICE_INDEX);
             const int tb = w.v.t0 + (int)(w.u - w.item0), te = w.v.t0 + (int)(min(w.item0 + w.units, w.u1) - w.item0);
             for (int t = tb; t < te && ok; ++t) {
@@ -229,13 +229,13 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
             for (int i = 0; i < 2; ++i) {
                 const int pos = w.s.L - w.s.n + row_token(p, w.rt * R + nt * 8 + 2 * c + i);
                 hi[nt][i] = p.causal ? min(w.s.L, pos + 1) : w.s.L;
-                lo[nt][i] = p.window > 0 ? pos + 1 - p.window : 0;
+                lo[nt][i] = first_seen(p, pos);
             }
         // tokens that every row sees
         const int pos0 = w.s.L - w.s.n + row_token(p, w.rt * R);
         const int pos1 = w.s.L - w.s.n + row_token(p, w.rt * R + rows - 1);
         const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
-        const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
+        const int all_lo = first_seen(p, pos1);
 
         float o[KS][NT][4], m[NT][2], l[NT][2];
 #pragma unroll

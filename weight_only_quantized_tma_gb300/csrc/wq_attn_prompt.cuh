@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         int s = 0;
         uint32_t ph = 0, issued = 0;
         for (; w.u < w.u1 && ok; walk_next<R, TN>(p, w)) {
-            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > (p.table_stride << p.c.p_shift))
+            if (w.u == w.item0 && lane == 0 && p.lens[w.b] > p.most)
                 atomicOr(p.status, DEVICE_INDEX);
             const int te = tile_end();
             for (int t = tile_begin(); t < te; ++t) {
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int pos0 = w.s.L - w.s.n + row_token(p, w.rt * R);
             const int pos1 = w.s.L - w.s.n + row_token(p, w.rt * R + rows - 1);
             const int all_hi = p.causal ? min(w.s.L, pos0 + 1) : w.s.L;
-            const int all_lo = p.window > 0 ? pos1 + 1 - p.window : 0;
+            const int all_lo = first_seen(p, pos1);
             for (int t = tile_begin(); t < te; ++t, ++n) {
                 const int tok = t * TN;
                 const uint32_t slot = n & (NS - 1);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int head = w.head * p.group + row - qt * p.group;
             const int pos = w.s.L - w.s.n + qt;
             const int hi = p.causal ? min(w.s.L, pos + 1) : w.s.L;
-            const int lo = p.window > 0 ? pos + 1 - p.window : 0;
+            const int lo = first_seen(p, pos);
             if (!idle) {
                 const uint16_t* src = static_cast<const uint16_t*>(p.q) + tq * p.q_stride + (int64_t)head * D;
                 uint8_t* dst = smem + C::OFF_Q + i * C::Q_TILE + r1 * 128;

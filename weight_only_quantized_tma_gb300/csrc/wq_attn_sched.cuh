@@ -38,9 +38,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
         s.q0 = a;
         s.n = max(e - a, 0);
     }
-    const int64_t most = p.table_stride << p.c.p_shift;
-    const int L = p.lens[b];
-    s.L = (int)min((int64_t)max(L, 0), most);
+    s.L = min(max(p.lens[b], 0), p.most);
     s.tiles = (int)(((uint32_t)(s.n * p.group) + R - 1) / R);
     return s;
 }
@@ -48,6 +46,12 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
 // The query token of a row; its head follows from the rest.
 __device__ __forceinline__ int row_token(const AttnParams& p, int row) {
     return (int)fastdiv((uint32_t)row, p.div_group);
+}
+
+// The first token that a query at this position sees.  Queries before the first token see none: all of
+// them count as position -1, so that no window makes the difference wrap.
+__device__ __forceinline__ int first_seen(const AttnParams& p, int pos) {
+    return p.window > 0 ? max(pos, -1) + 1 - p.window : 0;
 }
 
 struct Span {
@@ -61,7 +65,7 @@ __device__ __forceinline__ Span row_tile_span(const AttnParams& p, const SeqInfo
     const int first = row_token(p, rt * R), last = row_token(p, min((rt + 1) * R, rows) - 1);
     Span v;
     v.hi = p.causal ? max(0, min(s.L, s.L - s.n + last + 1)) : s.L;
-    v.lo = p.window > 0 ? max(0, s.L - s.n + first + 1 - p.window) : 0;
+    v.lo = max(0, first_seen(p, s.L - s.n + first));
     if (v.lo >= v.hi) v.lo = v.hi = 0;
     v.t0 = v.lo / TN;
     v.t1 = max((v.hi + TN - 1) / TN, v.t0 + 1);   // an empty tile still writes its rows

@@ -288,6 +288,7 @@ struct AttnParams {
     const int32_t* table;
     const int32_t* lens;
     int64_t table_stride;
+    int most;                       // tokens of the longest sequence: the table's, and token numbers stay int
     int64_t B, T;
     int Hq, group;                  // query heads, query heads for each key head
     FastDiv div_group;              // rows (query token x head of a group, below 2^31) to tokens
