@@ -381,7 +381,9 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  *     out = sum_j softmax_j(scale * q . K_j) V_j
  *     lse = log sum_j exp(scale * q . K_j)          (fp32 [T][q_heads], may be NULL)
  * accumulated in fp32, one rounding of out; the probabilities are rounded to dtype as
- * operands of the tensor cores.  A query that sees nothing gets out = 0, lse = -inf.
+ * operands of the tensor cores.  Keys and values of any size count as what wq_kv4_read
+ * returns (bf16 values below 2^-96 to within 2^-104); a probability below 2^-126 of its
+ * row's largest counts as 0.  A query that sees nothing gets out = 0, lse = -inf.
  * What pages hold past a sequence's length, NaN included, has no effect, and a NaN among
  * a sequence's keys or values only reaches the queries that see it: a key makes all of
  * their out NaN, a value at least the places where it stands.

@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                         uint32_t pair = *reinterpret_cast<const uint32_t*>(st + pairs_at + (d0 >> p.c.g_shift) * 4);
                         if (clear) pair = 0u;
                         if (spoil) pair = BF16 ? 0x7FC07FC0u : 0x7E007E00u;
+                        if (which) pair = summand<BF16>(pair);
                         const Operand<BF16> op = Operand<BF16>::both(pair);
                         const uint32_t words[4] = {cw.x, cw.y, cw.z, cw.w};
 #pragma unroll
@@ -366,8 +367,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i, o_tm = tmem + lanes + C::O_COL + 128 * i;
         // a zero scale becomes a tiny one, so that a masked -inf stays -inf; a negative
         // one moves its sign to Q
-        constexpr float up = Operand<BF16>::kUp;
-        const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f) * up;
+        const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const uint64_t sl = f2(sl2, sl2);
         uint32_t n = 0;                              // tiles of this row tile so far: S buffer n % 2
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
             const int parts = whole ? 1 : run_of(runs, w.item0 + w.units - 1) - b_first + 1;
             float* part = p.ws_part + (size_t)(2 * blockIdx.x + (w.u == w.item0 ? 1 : 0)) * attn_slot_floats(R, D);
             if (!idle && ok) {
-                const float inv = l == 0.f ? 0.f : up / l;
+                const float inv = l == 0.f ? 0.f : kSumUnit<BF16> / l;
                 uint16_t* out = static_cast<uint16_t*>(p.out) + tq * p.out_stride + (int64_t)head * D;
                 float* po = part + (size_t)r * D;
 #pragma unroll 1
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                                                pack2<BF16>(d[4] * inv, d[5] * inv), pack2<BF16>(d[6] * inv, d[7] * inv));
                             } else {
                                 float4* dst = reinterpret_cast<float4*>(po + c + 8 * j);
-                                __stcg(dst, make_float4(d[0] * up, d[1] * up, d[2] * up, d[3] * up));
-                                __stcg(dst + 1, make_float4(d[4] * up, d[5] * up, d[6] * up, d[7] * up));
+                                __stcg(dst, make_float4(d[0], d[1], d[2], d[3]));
+                                __stcg(dst + 1, make_float4(d[4], d[5], d[6], d[7]));
                             }
                         }
                     }

@@ -204,8 +204,8 @@ __device__ __forceinline__ int64_t safe_page(const AttnParams& p, int b, int ent
 }
 
 // Workspace: arrival counters, one for each block, then two partial results for each
-// block (the item it continues, the item it leaves unfinished): R rows of D sums, then R
-// pairs (maximum, sum of probabilities).
+// block (the item it continues, the item it leaves unfinished): R rows of D sums in units of
+// kSumUnit, then R pairs (maximum, sum of probabilities).
 __host__ __device__ constexpr size_t attn_slot_floats(int R, int D) { return (size_t)R * (D + 2); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -303,7 +303,7 @@ __device__ __forceinline__ void merge_parts(const AttnParams& p, const Walk& w, 
         for (int i = 0; i < PER; ++i) {
             const int idx = tid + i * NTHR, r = idx / CH, ch = idx % CH;
             if (r >= rows) continue;
-            const float l = weights[r * 33], inv = l == 0.f ? 0.f : 1.f / l;
+            const float l = weights[r * 33], inv = l == 0.f ? 0.f : kSumUnit<BF16> / l;
             const int row = w.rt * R + r0 + r, qt = row_token(p, row);
             uint16_t* out = static_cast<uint16_t*>(p.out) + (int64_t)(w.s.q0 + qt) * p.out_stride +
                             (w.head * p.group + row - qt * p.group) * D + ch * 4;

@@ -94,50 +94,75 @@ __device__ __forceinline__ uint4 word_values(uint32_t w, uint32_t s2, uint32_t l
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Sums of bf16 values may pass what fp32 holds, so the attention kernels add them up in units of
+// kSumUnit: that leaves 2^30 for the number of tokens and for a running maximum that lags behind,
+// and rounds values below 2^-96 to 2^-104.
 template <bool BF16>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if (BF16)
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+constexpr float kSumUnit = BF16 ? 1073741824.0f : 1.0f;   // 2^30
+// a pair (s, lo) in these units
+template <bool BF16>
+__device__ __forceinline__ uint32_t summand(uint32_t pair) {
+    if (BF16) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(pair) : "r"(0x30803080u));
+    return pair;
 }
 
-// Codes to operands of the attention kernels: values times 1 / kUp.
-//   fp16: as above (kUp = 1).
-//   bf16: a number with exponent field 0 or 1 is its 8 low bits times 2^-133, so a code
-// that is merely masked out is q 2^-133 (bits 0-3) or q 2^-129 (bits 4-7), and one fma
-// with s 2^53 or s 2^49 and lo 2^-80 gives RN(lo + q s) 2^-80: no magic number, no
-// subtraction, no shift for the upper code (9 operations in place of 15 for 8 codes).
-// The scores and the result are multiplied by kUp = 2^80 in fp32.  Exact for |value| >=
-// 2^-46, below that to 2^-53; steps s stay below 2^75.
+// Codes to operands of the attention kernels: RN(lo + q s) for every s and lo, the value that the
+// cache stands for (word_values gives the same).  Eight codes take 13 operations in fp16, 15 in
+// bf16.
 template <bool BF16>
 struct Operand {
-    static constexpr float kUp = BF16 ? 1.2089258196146292e24f : 1.0f;
-    uint32_t s_low, s_high, lo;
+    uint32_t s, lo;
     Operand() = default;
     // s and lo of the low and of the high half, in the cache's type
-    __device__ __forceinline__ Operand(uint32_t s2, uint32_t lo2) {
-        if (BF16) {
-            s_low = mul2<true>(s2, 0x5A005A00u);
-            s_high = mul2<true>(s2, 0x58005800u);
-            lo = mul2<true>(lo2, 0x17801780u);
-        } else {
-            s_low = s_high = s2;
-            lo = lo2;
-        }
-    }
+    __device__ __forceinline__ Operand(uint32_t s2, uint32_t lo2) : s(s2), lo(lo2) {}
     // one pair (s, lo) for both halves
     static __device__ __forceinline__ Operand both(uint32_t pair) {
         return Operand(__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232));
     }
     // codes in bits 0-3 and 16-19 of x; in bits 4-7 and 20-23
-    __device__ __forceinline__ uint32_t low(uint32_t x) const {
-        return fma2<BF16>(BF16 ? x & 0x000F000Fu : Codes<BF16>::low(x), s_low, lo);
+    __device__ __forceinline__ uint32_t low(uint32_t x) const { return fma2<BF16>(Codes<BF16>::low(x), s, lo); }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const { return fma2<BF16>(Codes<BF16>::high(x), s, lo); }
+};
+
+// The same in bf16 with 9 operations for 8 codes, in units of 1 / kUp and for most pairs.  A number
+// with exponent field 0 or 1 is its 8 low bits times 2^-133, so a code that is merely masked out is
+// q 2^-133 (bits 0-3) or q 2^-129 (bits 4-7), and one fma with s 2^53 or s 2^49 and lo 2^-80 gives
+// (lo + q s) 2^-80: no magic number, no subtraction, no shift for the upper code.  Exact for what
+// ShortRange lets pass: s 2^53 does not overflow, and where s and lo are zero or 2^-46 at least
+// lo + q s is a multiple of 2^-53, the last bit of the subnormal numbers in these units.
+struct ShortOperand {
+    static constexpr float kUp = 1.2089258196146292e24f;   // 2^80
+    uint32_t s_low, s_high, lo;
+    ShortOperand() = default;
+    __device__ __forceinline__ ShortOperand(uint32_t s2, uint32_t lo2) {
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(s_low) : "r"(s2), "r"(0x5A005A00u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(s_high) : "r"(s2), "r"(0x58005800u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(lo2), "r"(0x17801780u));
     }
-    __device__ __forceinline__ uint32_t high(uint32_t x) const {
-        return fma2<BF16>(BF16 ? x & 0x00F000F0u : Codes<BF16>::high(x), s_high, lo);
+    static __device__ __forceinline__ ShortOperand both(uint32_t pair) {
+        return ShortOperand(__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232));
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t x) const { return fma2<true>(x & 0x000F000Fu, s_low, lo); }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const { return fma2<true>(x & 0x00F000F0u, s_high, lo); }
+};
+
+// Collects pairs (s, lo) and tells whether one of them is no case for ShortOperand: s and lo have
+// to be zero or in 2^-46 <= |x| < 2^75.
+struct ShortRange {
+    static constexpr uint32_t kLeast = (127 - 46) << 7, kPast = (127 + 75) << 7;
+    uint32_t least = 0x7FFF7FFFu, most = 0u;
+    __device__ __forceinline__ void add(uint32_t pair) {
+        const uint32_t u = pair & 0x7FFF7FFFu;
+        // as signed halves u + 7FFF (no carry) puts zero last and the smallest number first
+        asm("min.s16x2 %0, %0, %1;" : "+r"(least) : "r"(u + 0x7FFF7FFFu));
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(u));
+    }
+    __device__ __forceinline__ bool outside() const {
+        constexpr uint32_t lo2 = (kLeast + 0x7FFFu) * 0x10001u, hi2 = (kPast - 1) * 0x10001u;
+        uint32_t a, b;
+        asm("min.s16x2 %0, %1, %2;" : "=r"(a) : "r"(least), "r"(lo2));
+        asm("max.u16x2 %0, %1, %2;" : "=r"(b) : "r"(most), "r"(hi2));
+        return a != lo2 || b != hi2;
     }
 };
 
