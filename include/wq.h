@@ -398,7 +398,7 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  * hold arrival counters: zero-fill them once, every call leaves them zero; calls that
  * share a workspace must not overlap on the GPU.
  * Requirements: B >= 0, T >= 0, q_heads a multiple of kv_heads, window >= 0 and 0 unless
- * causal, scale finite, 1 <= max_q, T * q_heads / kv_heads < 2^31 - 4097, strides >=
+ * causal, |scale| <= 2^127, 1 <= max_q, T * q_heads / kv_heads < 2^31 - 4097, strides >=
  * q_heads * D and multiples of 8; q, out and pages 16-byte aligned, the int32 arrays and
  * lse 4-byte aligned. */
 wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const int32_t* cu_q, int64_t B, int64_t T,

@@ -98,3 +98,13 @@ def test_row_numbers_stay_within_31_bits(L):
     assert L.wq_kv4_write(P, 256, P, 256, P, T, lay(), P, None) == SHAPE
     assert L.wq_kv4_read(P, lay(), P, T, P, 256, P, 256, None) == SHAPE
     assert L.wq_attn_kv4(P, 512, 4, P, 2, T, T, P, lay(), P, 8, P, 1.0, 1, 0, P, 512, None, None, 0, None) == SHAPE
+
+
+def test_scales_whose_logarithmic_form_overflows_are_refused(L):
+    """The kernels work with scale * log2(e) in fp32."""
+    def f(scale):   # (a misaligned out where the scale passes: nothing reaches the device)
+        return L.wq_attn_kv4(P, 512, 4, P, 2, 4, 2, P, lay(), P, 8, P, scale, 1, 0, P + 8, 512, None, None, 0, None)
+    for scale in (2.0 ** 127 * 1.001, -3e38, float("inf"), float("nan")):
+        assert f(scale) == SHAPE
+    for scale in (2.0 ** 127, -2.0 ** 127, 0.0, 1e-45):
+        assert f(scale) == MISALIGNED

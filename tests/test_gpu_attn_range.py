@@ -95,7 +95,7 @@ def test_one_token_of_another_size(e, causal, n):
 
 
 @pytest.mark.parametrize("n", NEWS)
-@pytest.mark.parametrize("e", [45, 60, 100, 118])
+@pytest.mark.parametrize("e", [-110, 45, 60, 100, 118])
 def test_sizes_of_scales(e, n):
     """A scale of one size, keys and queries of the other."""
     rng = np.random.default_rng(e + 500)
@@ -117,3 +117,19 @@ def test_largest_values(rising, dtype, n):
         k = ref.round16(k + np.linspace(0, 12, 500)[:, None, None], dtype)
     q = ref.round16(np.abs(_numbers(rng, (n, 4, 64), dtype)), dtype)
     Sequence(k, v, 64, 32, dtype).check(q)
+
+
+@pytest.mark.parametrize("n", NEWS)
+@pytest.mark.parametrize("e", [-103, -120])
+def test_small_scales_of_large_scores(e, n):
+    rng = np.random.default_rng(e + 600)
+    k, v = _numbers(rng, (150, 1, 64), "bf16", -e - 20), _numbers(rng, (150, 1, 64), "bf16")
+    Sequence(k, v, 64, 32, "bf16").check(_numbers(rng, (n, 4, 64), "bf16", 17), scale=2.0 ** e)
+
+
+@pytest.mark.parametrize("n", NEWS)
+def test_zero_scale_of_large_scores(n):
+    """Every visible token counts the same, however large its score."""
+    rng = np.random.default_rng(700)
+    k, v = _numbers(rng, (150, 1, 64), "bf16", 100), _numbers(rng, (150, 1, 64), "bf16")
+    Sequence(k, v, 64, 32, "bf16").check(_numbers(rng, (n, 4, 64), "bf16", 10), scale=0.0)

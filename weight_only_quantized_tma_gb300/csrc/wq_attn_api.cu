@@ -174,7 +174,7 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
     if (st != WQ_OK) return st;
     if (q_heads < 1 || q_heads > 65535 || q_heads % p.c.heads != 0) return WQ_ERR_SHAPE;
     if (B < 0 || B > kMaxTokens || T < 0 || T > kMaxTokens || max_q < 1 || table_stride < 0 ||
-        table_stride > kMaxTokens || window < 0 || (window > 0 && !causal) || !std::isfinite(scale))
+        table_stride > kMaxTokens || window < 0 || (window > 0 && !causal) || !(std::fabs(scale) <= 0x1p127f))
         return WQ_ERR_SHAPE;
     if (!cu_q && T != B) return WQ_ERR_SHAPE;
     if (T * (q_heads / p.c.heads) >= kMaxTokens - 4096) return WQ_ERR_SHAPE;

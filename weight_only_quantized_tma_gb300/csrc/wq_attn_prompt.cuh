@@ -365,9 +365,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
         const int r = threadIdx.x;                   // row of the item
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t s_tm = tmem + lanes + C::S_COL + 128 * i, o_tm = tmem + lanes + C::O_COL + 128 * i;
-        // a zero scale becomes a tiny one, so that a masked -inf stays -inf; a negative
-        // one moves its sign to Q
-        const float sl2 = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f);
+        // a negative scale moves its sign to Q, and a zero one goes to Q altogether, so that a masked
+        // -inf stays -inf
+        const float sl2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
         const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
         const uint64_t sl = f2(sl2, sl2);
         uint32_t n = 0;                              // tiles of this row tile so far: S buffer n % 2
@@ -389,6 +389,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                     uint4 v = *reinterpret_cast<const uint4*>(src + ch * 8);
                     if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
                     v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                    if (p.scale == 0.f)
+                        v = make_uint4(fma2<BF16>(v.x, 0u, 0u), fma2<BF16>(v.y, 0u, 0u), fma2<BF16>(v.z, 0u, 0u),
+                                       fma2<BF16>(v.w, 0u, 0u));
                     *reinterpret_cast<uint4*>(dst + (ch >> 3) * C::Q_HALF + (((ch & 7) ^ (r1 & 7)) << 4)) =
                         make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
