@@ -22,12 +22,21 @@ _fns: dict = {}
 _layouts: dict = {}
 
 
-def _call(name: str, *args) -> None:
-    """The library function `name`; a decode step's calls are short, so it is looked up once."""
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(name: str, device, *args) -> None:
+    """The library function `name`; a decode step's calls are short, so it is looked up once.
+
+    The library works on the current device, so the tensors' own is made that (None: host only)."""
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(lib(), name)
-    status = fn(*args)
+    if device is None or device.index == _current():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
     if status != 0:
         raise WQError(status, name)
 
@@ -141,7 +150,7 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, c
         k_out, ko_step = _empty(k), Hkv * D
     else:
         ko_step = _rows(k_out, "k_out", dtype, k.shape, dev)
-    _call("wq_qk_norm_rope", q.data_ptr(), q_step, k.data_ptr(), k_step, dt, T, Hq, Hkv, D,
+    _call("wq_qk_norm_rope", dev, q.data_ptr(), q_step, k.data_ptr(), k_step, dt, T, Hq, Hkv, D,
           None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
           positions.data_ptr(), cos_sin.data_ptr(), most, rot, int(interleaved), q_out.data_ptr(), qo_step,
           k_out.data_ptr(), ko_step, _stream(dev))
@@ -153,7 +162,8 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, c
 def wq_kv4_page_bytes(kv_heads: int, head_dim: int, group: int, page_size: int) -> int:
     """Bytes of one page of the cache, all heads."""
     b = _sz(0)
-    _call("wq_kv4_page_bytes", ctypes.byref(Kv4Layout(0, kv_heads, head_dim, group, page_size, 0)), ctypes.byref(b))
+    _call("wq_kv4_page_bytes", None, ctypes.byref(Kv4Layout(0, kv_heads, head_dim, group, page_size, 0)),
+          ctypes.byref(b))
     return b.value
 
 
@@ -174,7 +184,7 @@ def wq_kv4_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: t
     lay, ref = _layout(pages, D, group, page_size, k.dtype)
     if lay.kv_heads != H or pages.device != dev:
         raise ValueError(f"pages must hold {H} heads on {dev}")
-    _call("wq_kv4_write", k.data_ptr(), k_step, v.data_ptr(), v_step, slots.data_ptr(), T, ref, pages.data_ptr(),
+    _call("wq_kv4_write", dev, k.data_ptr(), k_step, v.data_ptr(), v_step, slots.data_ptr(), T, ref, pages.data_ptr(),
           _stream(dev))
 
 
@@ -196,7 +206,7 @@ def wq_kv4_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, group: 
         v, v_step = _empty(k), shape[1] * head_dim
     else:
         v_step = _rows(v, "v", dtype, shape, dev)
-    _call("wq_kv4_read", pages.data_ptr(), ref, slots.data_ptr(), T, k.data_ptr(), k_step, v.data_ptr(), v_step,
+    _call("wq_kv4_read", dev, pages.data_ptr(), ref, slots.data_ptr(), T, k.data_ptr(), k_step, v.data_ptr(), v_step,
           _stream(dev))
     return k, v
 
@@ -208,6 +218,14 @@ _ws_need: dict = {}
 _ws_cache: dict = {}
 
 
+def _capturing(device) -> bool:
+    """Whether the device's current stream is being captured into a graph."""
+    if device.index == _current():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
     """(tensor or None, bytes): a zero-filled workspace shared by calls on one stream.
 
@@ -217,13 +235,13 @@ def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
     need = _ws_need.get(key)
     if need is None:
         b = _sz(0)
-        _call("wq_attn_kv4_workspace_bytes", ref, q_heads, max_q, ctypes.byref(b))
+        _call("wq_attn_kv4_workspace_bytes", device, ref, q_heads, max_q, ctypes.byref(b))
         if len(_ws_need) > 4096:
             _ws_need.clear()
         need = _ws_need[key] = b.value
     if need == 0:
         return None, 0
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(device):
         return torch.zeros(need, dtype=torch.uint8, device=device), need
     key = (device.index, stream)
     buf = _ws_cache.get(key)
@@ -270,7 +288,7 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
         if not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
             raise ValueError(f"ws must be a contiguous tensor on {dev}")
         ws_bytes = ws.numel() * ws.element_size()
-    _call("wq_attn_kv4", q.data_ptr(), q_step, Hq, None if cu_q is None else cu_q.data_ptr(), B, T, max_q,
+    _call("wq_attn_kv4", dev, q.data_ptr(), q_step, Hq, None if cu_q is None else cu_q.data_ptr(), B, T, max_q,
           pages.data_ptr(), layout[1], block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(),
           D ** -0.5 if scale is None else scale, int(causal), min(window, _LONGEST), out.data_ptr(), out_step,
           None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, stream)
