@@ -125,6 +125,10 @@ def _check(status: int, fn: str):
 
 
 def _stream(t: torch.Tensor):
+    """The current stream of t's device, which has to be the current one: the library works there."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device} but cuda:{torch.cuda.current_device()} is current: "
+                         "call under torch.cuda.device(...)")
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
