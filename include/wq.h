@@ -395,8 +395,10 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  * its place).  Rows of out and lse that belong to no sequence are left as they were.
  * q_stride / out_stride: elements from token to token.  Results do not change from run to
  * run.  ws: at least wq_attn_kv4_workspace_bytes bytes, 16-byte aligned; its first 16 KiB
- * hold arrival counters: zero-fill them once, every call leaves them zero; calls that
- * share a workspace must not overlap on the GPU.
+ * hold arrival counters: zero-fill them once after allocating the workspace; every call
+ * leaves them zero again (a call that ends with a timeout bit in the device status may
+ * not, and leaves rows of out unwritten or wrong).  Calls that share a workspace must not
+ * overlap on the GPU.
  * Requirements: B >= 0, T >= 0, q_heads a multiple of kv_heads, window >= 0 and 0 unless
  * causal, |scale| <= 2^127, 1 <= max_q, T * q_heads / kv_heads < 2^31 - 4097, strides >=
  * q_heads * D and multiples of 8; q, out and pages 16-byte aligned, the int32 arrays and

@@ -113,3 +113,29 @@ def test_capture_is_asked_of_the_tensors_device(machine):
     assert not _attn._ws_cache      # the graph's own workspace
     _arguments("cuda:0")["wq_attn_kv4"]()
     assert list(_attn._ws_cache) == [(0, 40)]
+
+
+@pytest.mark.parametrize("clear", [False, True])
+@pytest.mark.parametrize("bits,timeout", [(0, False), (1 << 6, False), (1 << 1, True), (1 << 6 | 1 << 3, True)])
+def test_a_timeout_clears_the_arrival_counters(machine, monkeypatch, bits, timeout, clear):
+    """A kernel that gave up may leave counters that are not zero: later calls must not count from there.
+    Workspaces of other devices stay as they are, and so do all of them after an index out of range."""
+    zeroed = []
+    monkeypatch.setattr(_lib, "_ws_caches", [_lib._ws_cache, _attn._ws_cache], raising=False)
+    monkeypatch.setattr(_lib, "_zero_counters", lambda buf: zeroed.append(id(buf)), raising=False)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: zeroed.append("wait"))
+    for own in (0, 1):
+        _arguments(f"cuda:{own}")["wq_attn_kv4"]()
+        _lib._ws_cache[(own, 7)] = torch.zeros(1 << 20, dtype=torch.uint8, device=f"cuda:{own}")
+    machine.status_bits = bits
+    if clear:
+        wq.wq_clear_device_status()
+        assert machine.status_bits == 0
+    else:
+        assert wq.wq_device_status() == bits
+    mine = [id(_lib._ws_cache[(0, 7)]), id(_attn._ws_cache[(0, 40)])]
+    assert zeroed == (["wait", *mine, "wait"] if timeout else [])
+
+
+def test_every_cache_of_workspaces_is_known():
+    assert any(c is _attn._ws_cache for c in _lib._ws_caches) and any(c is _lib._ws_cache for c in _lib._ws_caches)

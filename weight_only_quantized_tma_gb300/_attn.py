@@ -216,6 +216,7 @@ def wq_kv4_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, group: 
 _LONGEST = (1 << 31) - 1   # no sequence is longer, so a longer window is this one
 _ws_need: dict = {}
 _ws_cache: dict = {}
+_lib._ws_caches.append(_ws_cache)
 
 
 def _capturing(device) -> bool:

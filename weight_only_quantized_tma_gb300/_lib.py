@@ -160,6 +160,24 @@ def _adtype(A: torch.Tensor) -> int:
 # ------------------------------------------------------------------ workspaces
 
 _ws_cache: dict = {}
+_ws_caches = [_ws_cache]     # of every operator: keys (device index, stream)
+
+
+def _zero_counters(buf: torch.Tensor) -> None:
+    buf[:16384].zero_()
+
+
+def _recover_workspaces() -> None:
+    """A kernel that gave up on a wait may have left arrival counters that are not zero in the workspaces
+    of the current device, and later calls would count from there.  (They are cleared, not replaced: a
+    captured graph may hold one.)"""
+    device = torch.cuda.current_device()
+    torch.cuda.synchronize()
+    for cache in _ws_caches:
+        for key, buf in cache.items():
+            if key[0] == device:
+                _zero_counters(buf)
+    torch.cuda.synchronize()
 
 
 def workspace(op: int, a_dtype: int, M: int, N: int, K: int, G: int, device) -> tuple:
@@ -483,14 +501,19 @@ def wq_gemm_bf16_fp4(A: torch.Tensor, w: torch.Tensor, sf_kernel: torch.Tensor, 
 # ------------------------------------------------------------------ device status
 
 def wq_device_status() -> int:
+    """The current device's status word.  Where it tells of a timeout, the arrival counters of the workspaces
+    that this binding holds are cleared; those of your own are yours to clear before their next use."""
     bits = ctypes.c_uint32(0)
     st = lib().wq_device_status(ctypes.byref(bits))
     if st not in (0, 9, 10):
         raise WQError(st, "wq_device_status")
+    if st == 9:
+        _recover_workspaces()
     return bits.value
 
 
 def wq_clear_device_status():
+    wq_device_status()      # for the workspaces: after this nobody learns of a timeout
     _check(lib().wq_clear_device_status(), "wq_clear_device_status")
 
 
