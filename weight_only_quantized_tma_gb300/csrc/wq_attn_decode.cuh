@@ -488,12 +488,11 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
                 if (++s == ST) s = 0, ph ^= 1u;
             }
         }
-        if (!ok) {
-            // given up: let the copies in flight land before the block may end.  A stage
-            // passed in this lap was filled with parity ph, the others in the lap before.
-            for (int i = 0; i < ST; ++i)
-                if (issued >> i & 1u) drain_wait(full_bar(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
-        }
+        // The copies in flight land before the block may end: whoever waits for them may have given up,
+        // this warp or another.  A stage passed in this lap was filled with parity ph, the others in the
+        // lap before.
+        for (int i = 0; i < ST; ++i)
+            if (issued >> i & 1u) drain_wait(full_bar(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
         return;
     }
 

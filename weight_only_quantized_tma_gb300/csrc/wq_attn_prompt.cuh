@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                 if (++s == RS) s = 0, ph ^= 1u;
             }
         }
-        if (!ok)   // given up: copies in flight land before the block may end
-            for (int i = 0; i < RS; ++i)
-                if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
+        // copies in flight land before the block may end: whoever waits for them may have given up
+        for (int i = 0; i < RS; ++i)
+            if (issued >> i & 1u) drain_wait(raw_full(i), i < s ? ph : ph ^ 1u, p.timeout_ns);
     } else if (warp < 18) {
         // ------------------------------------------------------------ MMA issuers
         // One lane for each row tile, and as few instructions between products as can be: a
@@ -279,11 +279,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(const At
                     ++nv, ++np;
                 }
             }
-            // given up (either warp): the MMAs in flight end before tensor memory is freed
-            if (*abort_flag) {
-                ptx::mma_commit(final_bar);
-                drain_wait(final_bar, 0u, p.timeout_ns);
-            }
+            // the MMAs in flight end before tensor memory is freed: whoever waits for them may have given up
+            ptx::mma_commit(final_bar);
+            drain_wait(final_bar, 0u, p.timeout_ns);
         }
         __syncwarp();
     }
