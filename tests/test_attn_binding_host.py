@@ -139,3 +139,31 @@ def test_a_timeout_clears_the_arrival_counters(machine, monkeypatch, bits, timeo
 
 def test_every_cache_of_workspaces_is_known():
     assert any(c is _attn._ws_cache for c in _lib._ws_caches) and any(c is _lib._ws_cache for c in _lib._ws_caches)
+
+
+BIG = 1 << 32     # what an int32 drops
+
+
+@pytest.mark.parametrize("name", ["group", "page_size", "head_dim", "kv_heads"])
+def test_sizes_that_would_wrap_are_refused(machine, name):
+    sizes = dict(kv_heads=1, head_dim=64, group=32, page_size=16)
+    sizes[name] += BIG
+    with pytest.raises(ValueError):
+        wq.wq_kv4_page_bytes(**sizes)
+    # pages of the size that Python's own arithmetic asks for: with a group beyond the head, smaller than
+    # the library's pages of group 32
+    block = sizes["page_size"] * (sizes["head_dim"] + 8 * (sizes["head_dim"] // sizes["group"]))
+    pages = Stub((3, sizes["kv_heads"], block), torch.uint8)
+    k = Stub((4, sizes["kv_heads"], sizes["head_dim"]), H)
+    with pytest.raises(ValueError):
+        wq.wq_kv4_read(pages, Stub((4,), torch.int64), sizes["head_dim"], sizes["group"], sizes["page_size"], H, k=k, v=k)
+    assert not machine.calls
+
+
+def test_counts_beyond_every_sequence_do_not_wrap(machine):
+    q, pages = Stub((4, 2, 64), H), Stub((3, 1, 16 * 80), torch.uint8)
+    table, lens, cu = Stub((4, 2), torch.int32), Stub((4,), torch.int32), Stub((5,), torch.int32)
+    for given, max_q, window in ((5, 5, 5), (BIG + 5, (1 << 31) - 1, (1 << 31) - 1), (-BIG, 0, -1), (-(1 << 64) + 5, 0, -1)):
+        wq.wq_attn_kv4(q, pages, table, lens, 32, 16, cu_q=cu, max_q=given, window=given, out=q)
+        name, _, args = machine.calls[-1]
+        assert name == "wq_attn_kv4" and (args[6], args[14]) == (max_q, window)

@@ -90,6 +90,13 @@ def _flat(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _int32(**sizes):
+    """ctypes would drop the high bits of what an int32 does not hold, and a wrong size pass for a right one."""
+    for name, x in sizes.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError(f"{name} is out of range: {x}")
+
+
 def _layout(pages, head_dim: int, group: int, page_size: int, dtype: torch.dtype):
     """(the layout, a reference to pass); pages [num_pages, kv_heads, block_bytes] gives the rest."""
     if not isinstance(pages, torch.Tensor) or not pages.is_cuda or pages.dtype is not torch.uint8 or pages.dim() != 3:
@@ -100,6 +107,7 @@ def _layout(pages, head_dim: int, group: int, page_size: int, dtype: torch.dtype
     got = _layouts.get(key)
     if got is None:
         n, heads, block = pages.shape
+        _int32(kv_heads=heads, head_dim=head_dim, group=group, page_size=page_size)
         if group <= 0 or block != page_size * (head_dim + 8 * (head_dim // group)):
             raise ValueError(f"pages: a block of {page_size} tokens with head_dim {head_dim} in groups of {group} has "
                              f"{page_size * (head_dim + 8 * (head_dim // max(1, group)))} bytes, got {block}")
@@ -161,6 +169,7 @@ def wq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, c
 
 def wq_kv4_page_bytes(kv_heads: int, head_dim: int, group: int, page_size: int) -> int:
     """Bytes of one page of the cache, all heads."""
+    _int32(kv_heads=kv_heads, head_dim=head_dim, group=group, page_size=page_size)
     b = _sz(0)
     _call("wq_kv4_page_bytes", None, ctypes.byref(Kv4Layout(0, kv_heads, head_dim, group, page_size, 0)),
           ctypes.byref(b))
@@ -213,7 +222,7 @@ def wq_kv4_read(pages: torch.Tensor, slots: torch.Tensor, head_dim: int, group: 
 
 # ------------------------------------------------------------------ attention
 
-_LONGEST = (1 << 31) - 1   # no sequence is longer, so a longer window is this one
+_LONGEST = (1 << 31) - 1   # no sequence is longer, so a longer window or max_q is this one
 _ws_need: dict = {}
 _ws_cache: dict = {}
 _lib._ws_caches.append(_ws_cache)
@@ -283,6 +292,7 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
     if lse is not None:
         _flat(lse, "lse", torch.float32, (T, Hq), dev)
     stream = _stream(dev)
+    max_q, window = max(min(max_q, _LONGEST), 0), max(min(window, _LONGEST), -1)
     if ws is None:
         ws, ws_bytes = attn_kv4_workspace(layout, Hq, max_q, dev, stream)
     else:
@@ -291,6 +301,6 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
         ws_bytes = ws.numel() * ws.element_size()
     _call("wq_attn_kv4", dev, q.data_ptr(), q_step, Hq, None if cu_q is None else cu_q.data_ptr(), B, T, max_q,
           pages.data_ptr(), layout[1], block_table.data_ptr(), block_table.shape[1], kv_lens.data_ptr(),
-          D ** -0.5 if scale is None else scale, int(causal), min(window, _LONGEST), out.data_ptr(), out_step,
+          D ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(), out_step,
           None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(), ws_bytes, stream)
     return out
