@@ -353,8 +353,9 @@ wq_status wq_kv4_page_bytes(const wq_kv4_layout* layout, size_t* bytes);
 /* Quantises the keys and values of T tokens into their slots.  k, v: dtype, heads of a
  * token contiguous, k_stride / v_stride elements from token to token.  slots: int64 [T],
  * page * P + place in the page.  A negative slot skips its token; a slot past the cache
- * sets the index bit of the device status and skips it; of tokens that share a slot any
- * may win.  For each group of G values:
+ * sets the index bit of the device status and skips it.  The slots of a call differ: where
+ * tokens share one it may end up with codes of one and pairs of another (padding takes a
+ * negative slot).  For each group of G values:
  *     lo = min,  s = RN((max - lo) / 15),  q = nearest integer to (x - lo) / s in 0..15
  * (half to even; q = 0 where s is 0), decided on fp32 differences; where lo + 15 s would
  * overflow the type, s is the next number below.  A group that holds an
@@ -389,8 +390,8 @@ wq_status wq_kv4_read(const uint8_t* pages, const wq_kv4_layout* layout, const i
  * their out NaN, a value at least the places where it stands.
  * kv_lens, cu_q and block_table are read on the device: a CUDA graph that captured the
  * call replays with new lengths.  max_q bounds n for the choice of kernel (a larger n is
- * still right).  Lengths are cut to table_stride * P and to 2^31 - 4097 (a longer one
- * sets the index bit of the device status), decreasing cu_q counts as n = 0, rows past
+ * still right).  Lengths are cut to table_stride * P and to 2^31 - 4097 (a longer one of
+ * a sequence with queries sets the index bit of the device status), decreasing cu_q counts as n = 0, rows past
  * T do not exist, and a page outside the cache sets the index bit (page 0 is read in
  * its place).  Rows of out and lse that belong to no sequence are left as they were.
  * q_stride / out_stride: elements from token to token.  Results do not change from run to

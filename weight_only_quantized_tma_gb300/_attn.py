@@ -184,7 +184,8 @@ def wq_kv4_pages(num_pages: int, kv_heads: int, head_dim: int, group: int, page_
 
 def wq_kv4_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages: torch.Tensor, group: int,
                  page_size: int) -> None:
-    """Quantises k, v [T, kv_heads, D] into slots (int64 [T]: page * page_size + place; negative: skip)."""
+    """Quantises k, v [T, kv_heads, D] into slots (int64 [T]: page * page_size + place; negative: skip; no two
+    alike: a shared one may hold parts of both tokens)."""
     k_step = _rows(k, "k")
     T, H, D = shape = k.shape
     dev = k.device
