@@ -167,3 +167,14 @@ def test_counts_beyond_every_sequence_do_not_wrap(machine):
         wq.wq_attn_kv4(q, pages, table, lens, 32, 16, cu_q=cu, max_q=given, window=given, out=q)
         name, _, args = machine.calls[-1]
         assert name == "wq_attn_kv4" and (args[6], args[14]) == (max_q, window)
+
+
+def test_workspace_bytes(machine):
+    pages = Stub((3, 1, 16 * 80), torch.uint8)
+    assert wq.wq_attn_kv4_workspace_bytes(pages, 2, 64, 32, 16, H, max_q=BIG) == 1000
+    name, device, args = machine.calls[-1]
+    assert name == "wq_attn_kv4_workspace_bytes" and device == 1 and args[1:3] == (2, (1 << 31) - 1)
+    for bad in (dict(q_heads=2 + BIG), dict(group=64), dict(page_size=32), dict(head_dim=128), dict(dtype=torch.float32)):
+        with pytest.raises(ValueError):
+            wq.wq_attn_kv4_workspace_bytes(**{**dict(pages=pages, q_heads=2, head_dim=64, group=32, page_size=16, dtype=H),
+                                              **bad})

@@ -38,3 +38,17 @@ def test_counters_left_by_a_timeout_reach_no_later_call(n, clear_only):
     assert wq.wq_device_status() == 0
     got = wq.wq_attn_kv4(**call, out=torch.full_like(want, 7.0))
     assert torch.equal(got, want) and (buf[:16384] == 0).all()
+
+
+@pytest.mark.parametrize("n", [1, 5, 50])
+def test_a_workspace_of_the_callers_own(n):
+    call = _problem(n)
+    want = wq.wq_attn_kv4(**call)
+    need = wq.wq_attn_kv4_workspace_bytes(call["pages"], Hq, D, G, P, torch.bfloat16, max_q=n)
+    room = torch.zeros(need + 4096, dtype=torch.uint8, device="cuda")
+    room[need:] = 5
+    for _ in range(3):
+        assert torch.equal(wq.wq_attn_kv4(**call, ws=room[:need]), want)
+    assert (room[:16384] == 0).all() and (room[need:] == 5).all()
+    with pytest.raises(wq.WQError):
+        wq.wq_attn_kv4(**call, ws=room[: need - 16])

@@ -10,6 +10,7 @@ paged key / value cache held in 4 bits, and attention over it.
 """
 from ._attn import (  # noqa: F401
     wq_attn_kv4,
+    wq_attn_kv4_workspace_bytes,
     wq_kv4_page_bytes,
     wq_kv4_pages,
     wq_kv4_read,

@@ -237,10 +237,7 @@ def _capturing(device) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
-def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
-    """(tensor or None, bytes): a zero-filled workspace shared by calls on one stream.
-
-    A call that is being captured into a graph gets its own, which the graph keeps and clears."""
+def _workspace_bytes(layout, q_heads: int, max_q: int, device) -> int:
     lay, ref = layout
     key = (device.index, lay.kv_heads, lay.head_dim, lay.group, lay.dtype, q_heads, max_q)
     need = _ws_need.get(key)
@@ -250,6 +247,22 @@ def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
         if len(_ws_need) > 4096:
             _ws_need.clear()
         need = _ws_need[key] = b.value
+    return need
+
+
+def wq_attn_kv4_workspace_bytes(pages: torch.Tensor, q_heads: int, head_dim: int, group: int, page_size: int,
+                                dtype: torch.dtype, max_q: int = 1) -> int:
+    """Bytes of a workspace for wq_attn_kv4 over these pages, whatever the lengths and the number of sequences."""
+    _int32(q_heads=q_heads)
+    return _workspace_bytes(_layout(pages, head_dim, group, page_size, dtype), q_heads, max(min(max_q, _LONGEST), 0),
+                            pages.device)
+
+
+def attn_kv4_workspace(layout, q_heads: int, max_q: int, device, stream: int):
+    """(tensor or None, bytes): a zero-filled workspace shared by calls on one stream.
+
+    A call that is being captured into a graph gets its own, which the graph keeps and clears."""
+    need = _workspace_bytes(layout, q_heads, max_q, device)
     if need == 0:
         return None, 0
     if _capturing(device):
@@ -270,7 +283,9 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
 
     block_table int32 [B, pages of a sequence], kv_lens int32 [B] (the new tokens included); cu_q int32 [B + 1]
     gives each sequence's queries (None: one each), max_q their largest number.  scale defaults to
-    1 / sqrt(D); window > 0 keeps the last `window` tokens of each query; lse: fp32 [T, q_heads] to fill."""
+    1 / sqrt(D); window > 0 keeps the last `window` tokens of each query; lse: fp32 [T, q_heads] to fill.
+    ws: a workspace of your own, zero-filled once, of wq_attn_kv4_workspace_bytes bytes or more, for calls that do
+    not overlap (None: the binding keeps one for each stream)."""
     q_step = _rows(q, "q")
     T, Hq, D = shape = q.shape
     dtype, dev = q.dtype, q.device
