@@ -44,7 +44,10 @@ class Sequence:
         err = np.abs(out - want)
         assert (err <= tol).all(), (np.isnan(out).sum(), float((err / np.maximum(tol, 1e-300)).max()))
         S = max(1.0, float(np.abs(q).sum(-1).max() * np.abs(self.K).max() * abs(sc)))
-        assert (np.abs(lse.double().cpu().numpy() - wl) <= 2 * self.D * 2.0 ** -24 * S + 2e-6).all()
+        lse = lse.double().cpu().numpy()
+        empty = np.isneginf(wl)     # more queries than tokens: the first ones see nothing
+        assert np.isneginf(lse[empty]).all()
+        assert (np.abs(lse[~empty] - wl[~empty]) <= 2 * self.D * 2.0 ** -24 * S + 2e-6).all()
 
 
 # new tokens with 4 query heads for each key head: 4, 12, 20 rows (few rows), 240 (many)
@@ -110,7 +113,8 @@ def test_sizes_of_scales(e, n):
 def test_largest_values(rising, dtype, n):
     """Values at the type's end, of one sign: no sum of them passes what it is divided by."""
     rng = np.random.default_rng(800)
-    top = 64000.0 if dtype == "f16" else 2.0 ** 127 * 1.953125   # a step of the type short of the end: roundings stay below
+    # a few steps of the type short of its end, so that the roundings of probabilities stay below it
+    top = 64000.0 if dtype == "f16" else 2.0 ** 127 * 1.953125
     k, v = _numbers(rng, (500, 1, 64), dtype), np.full((500, 1, 64), top)
     v[::3, :, ::5] *= 0.5
     if rising:      # the running maximum follows late
@@ -133,3 +137,46 @@ def test_zero_scale_of_large_scores(n):
     rng = np.random.default_rng(700)
     k, v = _numbers(rng, (150, 1, 64), "bf16", 100), _numbers(rng, (150, 1, 64), "bf16")
     Sequence(k, v, 64, 32, "bf16").check(_numbers(rng, (n, 4, 64), "bf16", 10), scale=0.0)
+
+
+@pytest.mark.parametrize("n", NEWS)
+@pytest.mark.parametrize("e", [0, -60, 90])
+@pytest.mark.parametrize("D,G", [(128, 32), (64, 32)])
+def test_columns_of_zeros(D, G, e, n):
+    """Heads padded with zeros: the padding's results are zero, the others as without it."""
+    rng = np.random.default_rng(e + 900)
+    k, v = _numbers(rng, (150, 2, D), "bf16"), _numbers(rng, (150, 2, D), "bf16", e)
+    k[..., D - 32:], v[..., D - 32:] = 0, 0
+    Sequence(k, v, G, 16, "bf16").check(_numbers(rng, (n, 8, D), "bf16"))
+
+
+@pytest.mark.parametrize("n", [1, 2, 3])
+@pytest.mark.parametrize("L", [1, 2, 3, 17])
+@pytest.mark.parametrize("e", [-70, 0, 80])
+def test_a_few_tokens(e, L, n):
+    rng = np.random.default_rng(e + 1000 + L)
+    k, v = _numbers(rng, (L, 2, 64), "bf16"), _numbers(rng, (L, 2, 64), "bf16", e)
+    Sequence(k, v, 64, 16, "bf16").check(_numbers(rng, (n, 8, 64), "bf16"))
+
+
+@pytest.mark.parametrize("n", NEWS)
+@pytest.mark.parametrize("e", [-70, 0, 80])
+@pytest.mark.parametrize("P", [16, 64])
+def test_pages_before_the_window_are_not_touched(P, e, n):
+    """Their table entries may be anything, and what lies in the seen pages outside the window too."""
+    L, window = 400, 100
+    rng = np.random.default_rng(e + 1100)
+    k, v = _numbers(rng, (L, 2, 64), "bf16"), _numbers(rng, (L, 2, 64), "bf16", e)
+    gone = (L - n + 1 - window) // P * P          # tokens of pages that nobody sees
+    s = Sequence(k, v, 32, P, "bf16")
+    q = _numbers(rng, (n, 8, 64), "bf16")
+    call = dict(cu_q=torch.tensor([0, n], dtype=torch.int32, device="cuda"), max_q=n, window=window)
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    wq.wq_clear_device_status()
+    a = wq.wq_attn_kv4(ref.on_gpu(q, "bf16"), s.pages, s.table, lens, 32, P, **call)
+    table = s.table.clone()
+    table[0, : gone // P] = torch.tensor([-5, 10 ** 6] * (gone // P), dtype=torch.int32, device="cuda")[: gone // P]
+    b = wq.wq_attn_kv4(ref.on_gpu(q, "bf16"), s.pages, table, lens, 32, P, **call)
+    assert wq.wq_device_status() == 0 and torch.equal(a, b)
+    want, _, A = ref.attention(q, s.K, s.V, 64 ** -0.5, n, True, window)
+    assert (np.abs(a.double().cpu().numpy() - want) <= 2.5 * ref.unit("bf16") * A).all()
