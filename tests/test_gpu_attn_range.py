@@ -180,3 +180,16 @@ def test_pages_before_the_window_are_not_touched(P, e, n):
     assert wq.wq_device_status() == 0 and torch.equal(a, b)
     want, _, A = ref.attention(q, s.K, s.V, 64 ** -0.5, n, True, window)
     assert (np.abs(a.double().cpu().numpy() - want) <= 2.5 * ref.unit("bf16") * A).all()
+
+
+@pytest.mark.parametrize("n", NEWS)
+@pytest.mark.parametrize("e", [0, -60, 90])
+def test_sums_that_cancel(e, n):
+    """Values of opposite sign under equal scores: results of exactly zero, beside values of another size."""
+    rng = np.random.default_rng(e + 1200)
+    k = np.broadcast_to(_numbers(rng, (1, 2, 64), "bf16"), (128, 2, 64)).copy()
+    v = np.ones((128, 2, 64))
+    v[:, :, ::3] = -1
+    v[1::2] *= -1
+    v[..., 32:] = _numbers(rng, (128, 2, 32), "bf16", e)
+    Sequence(k, v, 32, 16, "bf16").check(_numbers(rng, (n, 8, 64), "bf16"), causal=False)

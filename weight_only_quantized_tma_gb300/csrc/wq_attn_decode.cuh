@@ -16,17 +16,17 @@
 //     an exact subtraction and one fma in fp16: RN(lo + q s), the value that the cache stands
 //     for, in every kernel.  An item whose pairs or queries are too large or too small for
 //     ShortOperand is done again, straight from the cache, with the longer form (64 sequences
-//     with values of some 2^-60 take 442 us where ordinary ones take 150);
+//     with values of some 2^-60 or 2^80 take three to four times as long);
 //   * the running maximum moves only when a score passes it by more than 2^8, so most
 //     tiles pay one vote in place of a reduction.
 // Warps 0-3 each take 32 of the 128 tokens of a tile (with 8 rows as two products side by
 // side) with their own maximum, sum and O, and meet once for each item; warp 4 copies page
 // blocks into a ring with bulk copies.
 //
-// Measured: 64 sequences of 300 to 16384 tokens, 32 query and 8 key heads of 128, bf16: 142 us
-// for 582 MB (4.1 TB/s); when it took 148 us, copies alone took 100 and arithmetic alone 138,
-// so what bounds it is the latency between a warp's instructions (issue slots 56% full), not a
-// unit.
+// Measured: 64 sequences of 300 to 16384 tokens, 32 query and 8 key heads of 128, bf16: 147 us
+// for 582 MB (4.0 TB/s).  What bounds it is the latency between a warp's instructions (issue
+// slots 58% full), not a unit: in an earlier form of 148 us copies alone took 100 and arithmetic
+// alone 138.
 #pragma once
 
 #include <type_traits>
@@ -400,11 +400,47 @@ __device__ __forceinline__ void decode_tiles(const AttnParams& p, const Walk& w,
         }
 }
 
-// The same once more for every s and lo, from the cache itself: its results in `back`, o, m and l.  A
-// call, so that the kernel's registers stay with the quick form (inlined: 162 us in place of 150 for
-// the 64 sequences; Operand for every item: 172).
+// Whether ShortOperand rounds one of the values that a compute warp has worked with: looks at the
+// pairs in the cache again, a lane for each of 32 tokens and 16 tiles' loads at a time.
+template <int D>
+__device__ __forceinline__ bool decode_rounded(const AttnParams& p, const Walk w, int tb, int te) {
+    constexpr int N = 16;
+    const int pair_row = 4 * (D >> p.c.g_shift), first = 32 * (threadIdx.x >> 5) + (threadIdx.x & 31);
+    bool found = false;
+    for (int t = tb; t < te; t += N) {
+        const uint8_t* pairs[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int tt = (t + j) * kDecodeTN + first;
+            pairs[j] = nullptr;
+            if (t + j < te && tt >= w.v.lo && tt < w.v.hi) {
+                const int64_t page = p.table[(int64_t)w.b * p.table_stride + (tt >> p.c.p_shift)];
+                pairs[j] = p.c.pages + (page >= 0 && page < p.c.num_pages ? page : 0) * p.c.page_bytes +
+                           (int64_t)w.head * p.c.block_bytes + p.c.P * D + (tt & (p.c.P - 1)) * pair_row;
+            }
+        }
+        for (int x = 0; x < pair_row; x += 4) {
+            uint32_t k[N], v[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                k[j] = pairs[j] ? *reinterpret_cast<const uint32_t*>(pairs[j] + x) : 0u;
+                v[j] = pairs[j] ? *reinterpret_cast<const uint32_t*>(pairs[j] + p.c.P * pair_row + x) : 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) found |= ShortOperand::refuses(k[j]) || ShortOperand::refuses(v[j]);
+        }
+    }
+    return __any_sync(0xffffffffu, found);
+}
+
+// The same once more for every s and lo, from the cache itself, where it is needed: o, m and l are in
+// `back`, and the new ones go there.  A call with everything in memory, so that the kernel's registers
+// stay with the quick form (147 us for the 64 sequences; inlined some 10 us more, with o, m and l held
+// across the call 15, with Operand for every item 20, without looking for what is not exact 5 less).
 template <int D, int NT>
-__device__ __noinline__ void decode_again(const AttnParams& p, const Walk w, int tb, int te, uint8_t* smem, float* back) {
+__device__ __noinline__ void decode_again(const AttnParams& p, const Walk w, int tb, int te, uint8_t* smem, float* back,
+                                          bool sure) {
+    if (!sure && !decode_rounded<D>(p, w, tb, te)) return;
     constexpr int KS = D / 16;
     float o[KS][NT][4], m[NT][2], l[NT][2];
     uint32_t qr[DecodeCfg<D, NT>::Q_SMEM ? 1 : KS][2];
@@ -530,30 +566,42 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
             p, w, tb, te, smem, stage_bytes, qr, ring, o, m, l, seen);
         const bool ok = ring.ok;
         if constexpr (BF16) {
-            // Where that may not have been exact, once more.  An overflow shows in the keys' largest step
-            // or makes a sum infinite or NaN; values that were rounded, by 2^-53 at most, matter to large
-            // queries and to results below 2^-30 (0 where all of a lane's values are: no doubt).  With
+            // Where that was not exact, once more.  An overflow shows in the keys' largest step or makes a
+            // sum infinite or NaN.  Values that were rounded, by 2^-53 at most, matter to large queries
+            // and to results below 2^-30; what is 0 because all of a lane's values are is none of these,
+            // and for the rest (a sum of many values is exactly 0 now and then) the pairs tell.  With
             // scales above 2^25 scores themselves may leave fp32's range in these units.
-            doubt |= seen.k_step >= 0x7F800000u || fabsf(p.scale) > 33554432.f;
+            bool again = seen.k_step >= 0x7F800000u || fabsf(p.scale) > 33554432.f;
             seen.v_any |= __shfl_xor_sync(0xffffffffu, seen.v_any, 1);
             seen.v_any |= __shfl_xor_sync(0xffffffffu, seen.v_any, 2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float least = INFINITY, sum = 0.f;
+                    float least = INFINITY, sum = l[nt][i];
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         least = fminf(least, fminf(fabsf(o[k][nt][i]), fabsf(o[k][nt][2 + i])));
                         sum += fabsf(o[k][nt][i]) + fabsf(o[k][nt][2 + i]);
                     }
+                    again |= !(sum < INFINITY);
                     if (nt * 8 + 2 * c + i < rows && (seen.v_any & 0x7FFF7FFFu))
-                        doubt |= !(least >= l[nt][i] * 7.703719777548943e-34f && sum < INFINITY);   // 2^-110
-                    doubt |= l[nt][i] != l[nt][i];
+                        doubt |= least < l[nt][i] * 7.703719777548943e-34f;   // 2^-110
                 }
-            if (ok && __any_sync(0xffffffffu, doubt)) {
+            again = __any_sync(0xffffffffu, again);
+            constexpr float unit = ShortOperand::kUp / kSumUnit<true>;
+            if (__builtin_expect(ok && (again || __any_sync(0xffffffffu, doubt)), 0)) {
                 float back[C::REGS];
-                decode_again<D, NT>(p, w, tb, te, smem, back);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) back[(k * NT + nt) * 4 + i] = o[k][nt][i] * unit;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) back[KS * NT * 4 + nt * 4 + i] = m[nt][i], back[KS * NT * 4 + nt * 4 + 2 + i] = l[nt][i];
+                }
+                decode_again<D, NT>(p, w, tb, te, smem, back, again);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -569,7 +617,7 @@ __global__ void __launch_bounds__(160, (DecodeCfg<D, NT>::MIN_BLOCKS)) attn_deco
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[k][nt][i] *= ShortOperand::kUp / kSumUnit<true>;
+                        for (int i = 0; i < 4; ++i) o[k][nt][i] *= unit;
             }
         }
 

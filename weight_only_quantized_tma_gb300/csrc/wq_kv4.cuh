@@ -127,9 +127,9 @@ struct Operand {
 // The same in bf16 with 9 operations for 8 codes, in units of 1 / kUp and for most pairs.  A number
 // with exponent field 0 or 1 is its 8 low bits times 2^-133, so a code that is merely masked out is
 // q 2^-133 (bits 0-3) or q 2^-129 (bits 4-7), and one fma with s 2^53 or s 2^49 and lo 2^-80 gives
-// (lo + q s) 2^-80: no magic number, no subtraction, no shift for the upper code.  Exact for what
-// ShortRange lets pass: s 2^53 does not overflow, and where s and lo are zero or 2^-46 at least
-// lo + q s is a multiple of 2^-53, the last bit of the subnormal numbers in these units.
+// (lo + q s) 2^-80: no magic number, no subtraction, no shift for the upper code.  Steps s from
+// 2^75 on overflow; what is no multiple of 2^-53 is rounded to one, by 2^-53 at most.  Where s and
+// lo are zero or 2^-46 at least there is nothing to round.
 struct ShortOperand {
     static constexpr float kUp = 1.2089258196146292e24f;   // 2^80
     uint32_t s_low, s_high, lo;
@@ -144,25 +144,11 @@ struct ShortOperand {
     }
     __device__ __forceinline__ uint32_t low(uint32_t x) const { return fma2<true>(x & 0x000F000Fu, s_low, lo); }
     __device__ __forceinline__ uint32_t high(uint32_t x) const { return fma2<true>(x & 0x00F000F0u, s_high, lo); }
-};
-
-// Collects pairs (s, lo) and tells whether one of them is no case for ShortOperand: s and lo have
-// to be zero or in 2^-46 <= |x| < 2^75.
-struct ShortRange {
-    static constexpr uint32_t kLeast = (127 - 46) << 7, kPast = (127 + 75) << 7;
-    uint32_t least = 0x7FFF7FFFu, most = 0u;
-    __device__ __forceinline__ void add(uint32_t pair) {
-        const uint32_t u = pair & 0x7FFF7FFFu;
-        // as signed halves u + 7FFF (no carry) puts zero last and the smallest number first
-        asm("min.s16x2 %0, %0, %1;" : "+r"(least) : "r"(u + 0x7FFF7FFFu));
-        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(u));
-    }
-    __device__ __forceinline__ bool outside() const {
-        constexpr uint32_t lo2 = (kLeast + 0x7FFFu) * 0x10001u, hi2 = (kPast - 1) * 0x10001u;
-        uint32_t a, b;
-        asm("min.s16x2 %0, %1, %2;" : "=r"(a) : "r"(least), "r"(lo2));
-        asm("max.u16x2 %0, %1, %2;" : "=r"(b) : "r"(most), "r"(hi2));
-        return a != lo2 || b != hi2;
+    // Whether a pair is none of those that are taken exactly.
+    static __device__ __forceinline__ bool refuses(uint32_t pair) {
+        const uint32_t s = pair & 0x7FFFu, l = pair >> 16 & 0x7FFFu;
+        constexpr uint32_t least = (127 - 46) << 7, past = (127 + 75) << 7;
+        return (s != 0 && (s < least || s >= past)) || (l != 0 && (l < least || l >= past));
     }
 };
 
