@@ -68,6 +68,8 @@ class Machine:
         monkeypatch.setattr(_lib, "_ws_cache", {})
         monkeypatch.setattr(_attn, "_stream", lambda device: 40 + device.index)
         monkeypatch.setattr(_attn, "_current", lambda: self.device, raising=False)
+        monkeypatch.setattr(_attn, "_several", None, raising=False)
+        monkeypatch.setattr(torch.cuda, "device_count", lambda: 4)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: self.device)
         monkeypatch.setattr(torch.cuda, "device", on)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.device == self.capturing)

@@ -23,6 +23,15 @@ _layouts: dict = {}
 
 
 _current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_several = None     # whether there is more than one device (with one, nothing is asked: 0.1 us of a call's 6)
+
+
+def _foreign(device) -> bool:
+    """Whether another device is current."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    return _several and device.index != _current()
 
 
 def _call(name: str, device, *args) -> None:
@@ -32,11 +41,11 @@ def _call(name: str, device, *args) -> None:
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(lib(), name)
-    if device is None or device.index == _current():
-        status = fn(*args)
-    else:
+    if _several is not False and device is not None and _foreign(device):
         with torch.cuda.device(device):
             status = fn(*args)
+    else:
+        status = fn(*args)
     if status != 0:
         raise WQError(status, name)
 
@@ -231,10 +240,10 @@ _lib._ws_caches.append(_ws_cache)
 
 def _capturing(device) -> bool:
     """Whether the device's current stream is being captured into a graph."""
-    if device.index == _current():
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.device(device):
-        return torch.cuda.is_current_stream_capturing()
+    if _several is not False and _foreign(device):
+        with torch.cuda.device(device):
+            return torch.cuda.is_current_stream_capturing()
+    return torch.cuda.is_current_stream_capturing()
 
 
 def _workspace_bytes(layout, q_heads: int, max_q: int, device) -> int:
@@ -308,7 +317,10 @@ def wq_attn_kv4(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
     if lse is not None:
         _flat(lse, "lse", torch.float32, (T, Hq), dev)
     stream = _stream(dev)
-    max_q, window = max(min(max_q, _LONGEST), 0), max(min(window, _LONGEST), -1)
+    if not 0 <= max_q <= _LONGEST:
+        max_q = _LONGEST if max_q > 0 else 0
+    if not -1 <= window <= _LONGEST:
+        window = _LONGEST if window > 0 else -1
     if ws is None:
         ws, ws_bytes = attn_kv4_workspace(layout, Hq, max_q, dev, stream)
     else:
