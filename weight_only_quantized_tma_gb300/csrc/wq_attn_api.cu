@@ -48,10 +48,15 @@ bool stride_ok(int64_t stride, int64_t row, int64_t step) {
     return stride >= row && stride <= kMaxStride && stride % step == 0;
 }
 
-// The few-row kernel's tiles hold 8 to 24 rows, the many-row kernel's 128.  Where the first
-// would unpack the codes twice the second is as fast or faster: 35 rows of 64 over 24
-// sequences of up to 6001 tokens take 84 us in two row tiles of the first, 57 us in the second;
-// 24 rows over 24 sequences of 4096 tokens 42 us against 52 us for 35.
+// The few-row kernel's tiles hold 8 to 24 rows, the many-row kernel's 256.  Where the first
+// would unpack the codes twice the second is as fast or faster once sequences are long.  Few / many
+// rows, us, 8 key heads in bf16 (fp16 within 3 us of it), cold:
+//   rows                             24       32       40       64      128
+//   24 sequences of 4096, D = 64    53/80    88/80    88/82   119/84   223/90
+//   24 sequences of 4096, D = 128   88/131  143/133  145/137  201/141  375/154
+//   8 sequences of 1000, D = 64     20/27    27/31    27/31    31/33    41/41
+//   8 sequences of 1000, D = 128    37/39    41/37    41/41    47/45    68/61
+// (lengths are on the device, so the rule is on rows alone).
 bool many_rows(int64_t rows) { return rows > 24; }
 
 size_t attn_ws(const Kv4View& c, bool bf16, int64_t rows, int sms) {

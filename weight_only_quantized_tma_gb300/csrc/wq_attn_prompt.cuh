@@ -25,7 +25,7 @@
 // MN-major, so V is never transposed.  Eight codes of a word land in the order 0 4 1 5 2 6
 // 3 7 that the unpack gives; Q is stored in the same order and O is read back through it.
 //
-// Measured: 4096 queries over 16384 tokens, 32 query and 8 key heads of 128, bf16: 814 us, 1183
+// Measured: 4096 queries over 16384 tokens, 32 query and 8 key heads of 128, bf16: 822 us, 1170
 // TFLOP/s, the tensor pipe 64% busy.  (Products of 64 columns from shared memory take 48 cycles
 // in place of 32, 128 bytes of operands a cycle: 1261 cycles for 64 tokens and 256 rows.)
 #pragma once

@@ -23,7 +23,8 @@ __device__ __forceinline__ int nearest_code(float d, float s, float inv) {
     return i < 0 ? 0 : (i > 15 ? 15 : i);
 }
 
-// RN(x / 15) in fp32: the product with 1 / 15 and one correction by its exact residual.
+// RN(x / 15) in fp32: the product with 1 / 15 and one correction by its exact residual
+// (Markstein's method).
 // (Results below the normal range, whose residual is not exact, are divided.)
 __device__ __forceinline__ float fifteenth(float x) {
     if (x < 1e-30f) return __fdiv_rn(x, 15.0f);
@@ -71,7 +72,8 @@ __device__ __forceinline__ GroupPlace group_place(const Kv4RowsParams& p, int la
 // integer, that integer and its exact residual; only where the largest residual reaches
 // half a step (ties, and the products that rounded the wrong way) is the exact search above
 // run.  Bound by instructions (16384 tokens of 32 heads of 128, 344 MB: 118 us with an address
-// and unpacked arithmetic for each row, now 92 us, the issue slots 80% full).
+// and unpacked arithmetic for each row, now 87 us, the issue slots 78% full).  The least and the
+// greatest value have shuffles of their own; one packed (least, -greatest) would halve them.
 template <bool BF16, int D, int G, int HP>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
     ptx::grid_dependency_wait();
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const Kv4RowsParams p) {
 }
 
 // The inverse: one lane turns a word of codes into 8 values (16 bytes out).  Bound by memory:
-// 50001 tokens of 8 heads of 128, 269 MB, in 42 us (6.5 TB/s).
+// 50001 tokens of 8 heads of 128, 269 MB, in 42 us (6.4 TB/s).
 template <bool BF16, int D, int HP>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4RowsParams p) {
     ptx::grid_dependency_wait();

@@ -21,8 +21,9 @@ __device__ __forceinline__ void load4(const uint16_t* p, float (&x)[4]) {
 
 // One group of LPR lanes takes `per` query heads or `per` key heads of one token, U at a time:
 // the U rows' loads are all issued before the first is used, and the token's angles, the
-// weight and the addresses are worked out once for all of them (one row for each group: 73.7
-// us for 8192 tokens of 64 heads; now 53 us, 273 MB at 5.1 TB/s).
+// weight and the addresses are worked out once for all of them (8192 tokens of 64 heads of 128:
+// 73.7 us with one row for each group, now 48.1 us, 273 MB at 5.7 TB/s; warps wait for memory
+// half of the time, issue slots 64% full).
 template <bool BF16, int LPR, int U>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeParams p) {
     ptx::grid_dependency_wait();
@@ -148,8 +149,8 @@ template <bool BF16, int LPR>
 cudaError_t launch(const RopeParams& p, int sms, cudaStream_t st) {
     // As many heads for each group as leave two full blocks for each SM: 16 read the angles and
     // the weight least often, 1 spreads a decode step's few rows widest.  (8192 tokens of 32
-    // query and 32 key heads of 128, rows in flight x heads: 2 x 16 53 us, 2 x 8 55, 2 x 32 57,
-    // 4 x 8 63, 4 x 16 63, 1 x 16 66, 2 x 2 70.)
+    // query and 32 key heads of 128, rows in flight x heads: 2 x 16 48.1 us, 2 x 8 49.9, 2 x 32
+    // 53.0, 2 x 4 54.3, 4 x 16 57.1, 4 x 8 57.8, 1 x 16 59.5, 2 x 2 66.1.)
     const int64_t want = (int64_t)sms * 2 * (256 / LPR);
     for (int per = 16; per >= 4; per /= 2)
         if (p.T * ((p.Hq + per - 1) / per + (p.Hkv + per - 1) / per) >= want) return launch_u<BF16, LPR, 2>(p, per, st);
