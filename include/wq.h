@@ -27,6 +27,11 @@
  * keys (wq_qk_norm_rope), a paged key / value cache held in 4 bits (wq_kv4_write,
  * wq_kv4_read) and attention over it (wq_attn_kv4).
  *
+ * Around projections with both operands in 8 bits (e4m3, a scale for each block of 128):
+ * norm with the residual's addition (wq_add_rms_norm, wq_add_rms_norm_fp8), a quantiser
+ * (wq_quantize_fp8), the product (wq_gemm_w8a8_fp8) and the first half of a gated
+ * feed-forward block (wq_gemm_w8a8_fp8_gated).
+ *
  * Conventions for every entry point:
  *   - All arrays are row-major and live in device memory unless stated.  The
  *     caller allocates and owns every buffer; the library never allocates,
@@ -412,6 +417,64 @@ wq_status wq_attn_kv4(const void* q, int64_t q_stride, int32_t q_heads, const in
 /* Workspace bytes of wq_attn_kv4 on the current device for these heads and max_q, whatever
  * the lengths, the number of sequences and the cache's size.  Host only. */
 wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_heads, int64_t max_q, size_t* bytes);
+
+/* ------------------------------------------------------------------ 8-bit activations */
+
+/* What a decoder layer runs around projections whose operands are both e4m3 (no passage of the
+ * source pages: they treat 16-bit activations).  Activations of T tokens: codes uint8 [T][K] and
+ * fp32 scales [ceil(K / 128)][T], one for each token and block of 128 values along K (the last
+ * block may be shorter); a value is e4m3(code) * scale.  The kernels that make them take
+ *     scale = max(max |y| / 448, 2^-96),   code = e4m3(y / scale)
+ * of a block's fp32 values y (round to nearest even).  A block that holds an infinity or a NaN
+ * gets a NaN for its scale: its values are NaN, and no other block is touched. */
+
+/* Norm of rows with the residual's addition, T rows of H values, in fp32 with one rounding:
+ *     s = x + residual,   sum = RN(s),   out = RN(s * rsqrt(mean(s^2) + eps) * weight)
+ * (the norm is of s before it is rounded; a NULL residual: s = x, and sum is not written).  The
+ * mean holds for every s that fp32 holds.  Strides are elements from row to row.  sum may be
+ * residual or x itself, out may be x or residual (same pointer and stride); sum and out differ, and
+ * any other overlap is undefined.
+ * Requirements: T >= 0, 8 <= H <= 32768, H % 8 == 0, eps >= 0, strides >= H and multiples of 8;
+ * pointers 16-byte aligned. */
+wq_status wq_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          wq_dtype dtype, int64_t T, int64_t H, const void* weight, float eps, void* sum,
+                          int64_t sum_stride, void* out, int64_t out_stride, wq_stream_t stream);
+
+/* The same with its output in 8 bits: codes [T][H] and scales [ceil(H / 128)][T] of the fp32
+ * values.  H % 16 == 0; codes 16-byte aligned. */
+wq_status wq_add_rms_norm_fp8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                              wq_dtype dtype, int64_t T, int64_t H, const void* weight, float eps, void* sum,
+                              int64_t sum_stride, uint8_t* codes, float* scales, wq_stream_t stream);
+
+/* 16-bit rows x [T][K] (x_stride elements from row to row) to codes and scales.
+ * Requirements: T >= 0, K >= 16, K % 16 == 0, x_stride >= K and a multiple of 8, T / 16 * K / 128
+ * (each rounded up) < 2^31 - 1; x and codes 16-byte aligned. */
+wq_status wq_quantize_fp8(const void* x, int64_t x_stride, wq_dtype dtype, int64_t T, int64_t K, uint8_t* codes,
+                          float* scales, wq_stream_t stream);
+
+/* Product of 8-bit activations and 8-bit weights:
+ *     out[m][n] = sum_b a_scale[b][m] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]  (+ bias[n])
+ * a, a_scale: activations [M][K] as above.  w: e4m3 codes [N][K]; w_scale: fp32
+ * [ceil(N / 128)][ceil(K / 128)], one for each block of 128 x 128.  Sums of a block and over the
+ * blocks are held in fp32; out is 16-bit (dtype) [M][N], rounded once.  bias: NULL or [N] of dtype.
+ * A NaN among a token's codes or scales makes that token's outputs NaN, one of a weight row that
+ * row's column.  Results do not change from run to run.
+ * Requirements: M >= 0, N >= 8, N % 8 == 0, N <= 2^29, 16 <= K <= 2^30, K % 16 == 0; a, w and out
+ * 16-byte aligned, the scales 4-byte, bias 2-byte. */
+wq_status wq_gemm_w8a8_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                           const void* bias, int64_t M, int64_t N, int64_t K, wq_dtype dtype, void* out,
+                           wq_stream_t stream);
+
+/* First half of a gated feed-forward block:
+ *     gate = a . w[0 .. F)^T,  up = a . w[F .. 2F)^T,  h = gate / (1 + exp(-gate)) * up
+ * (products as wq_gemm_w8a8_fp8's, h in fp32).  w: [2 F][K]; w_scale: fp32 [2][ceil(F / 128)]
+ * [ceil(K / 128)], the blocks of either half counted from its own first row.  Output: codes [M][F]
+ * and scales [ceil(F / 128)][M] of h (out NULL, dtype ignored), or out, 16-bit [M][F], rounded once
+ * (codes and scales NULL).
+ * Requirements: as above with N = F, F % 16 == 0; codes 16-byte aligned. */
+wq_status wq_gemm_w8a8_fp8_gated(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
+                                 int64_t M, int64_t F, int64_t K, wq_dtype dtype, void* out, uint8_t* codes,
+                                 float* scales, wq_stream_t stream);
 
 /* ------------------------------------------------------------------ planning */
 

@@ -7,6 +7,10 @@ libwq.so (C ABI: include/wq.h); this package only binds it.
 
 Between the projections of an attention layer: norm + rotation of queries and keys, a
 paged key / value cache held in 4 bits, and attention over it.
+
+Around projections with both operands in 8 bits: norm with the residual's addition, a
+quantiser of activations, the block-scaled product, and the first half of a gated
+feed-forward block.
 """
 from ._attn import (  # noqa: F401
     wq_attn_kv4,
@@ -16,6 +20,13 @@ from ._attn import (  # noqa: F401
     wq_kv4_read,
     wq_kv4_write,
     wq_qk_norm_rope,
+)
+from ._fp8 import (  # noqa: F401
+    wq_add_rms_norm,
+    wq_add_rms_norm_fp8,
+    wq_gemm_w8a8_fp8,
+    wq_gemm_w8a8_fp8_gated,
+    wq_quantize_fp8,
 )
 from ._lib import (  # noqa: F401
     WQError,

@@ -92,6 +92,13 @@ _SIGNATURES = {
     "wq_attn_kv4": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, ctypes.c_float,
                                    _i32, _i32, _vp, _i64, _vp, _vp, _sz, _vp]),
     "wq_attn_kv4_workspace_bytes": (ctypes.c_int, [_vp, _i32, _i64, ctypes.POINTER(_sz)]),
+    "wq_add_rms_norm": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, ctypes.c_float, _vp, _i64,
+                                       _vp, _i64, _vp]),
+    "wq_add_rms_norm_fp8": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, ctypes.c_float, _vp,
+                                           _i64, _vp, _vp, _vp]),
+    "wq_quantize_fp8": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _i64, _i64, _vp, _vp, _vp]),
+    "wq_gemm_w8a8_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _vp]),
+    "wq_gemm_w8a8_fp8_gated": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp]),
     "wq_debug_fastdiv": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_uint32, _vp, _i64, _vp, ctypes.POINTER(_i32)]),
 }
 

@@ -1,0 +1,41 @@
+// wq_fp8.cuh -- device helpers for 8-bit (e4m3) activations with a scale for each token and
+// block of 128 values (include/wq.h, "8-bit activations").
+#pragma once
+
+#include "wq_kv4.cuh"
+
+namespace wq {
+
+// Larger of both; a NaN in either gives NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Four fp32 to four e4m3 codes (a in the lowest byte), nearest even, at most +-448.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// The scale of a block whose largest magnitude is `most`, and what its values are multiplied with.  An
+// infinity or a NaN in the block gives a NaN for the scale (and codes of 0): the block's values are NaN.
+// The product with the nearest reciprocal puts a value within 2^-23 of its quotient, so that only one
+// that close to the middle between two codes can become the other of them.
+struct BlockScale {
+    float scale, inv;
+    __device__ __forceinline__ explicit BlockScale(float most) {
+        const bool finite = most <= 3.402823466e38f;
+        scale = finite ? fmaxf(__fdiv_rn(most, 448.0f), 0x1p-96f) : __int_as_float(0x7FC00000);
+        inv = finite ? __frcp_rn(scale) : 0.0f;
+    }
+};
+
+}  // namespace wq

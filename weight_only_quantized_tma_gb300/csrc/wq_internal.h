@@ -306,14 +306,50 @@ size_t attn_kv4_decode_ws(const Kv4View& c, bool bf16, int64_t rows, int sms);
 cudaError_t launch_attn_kv4_prompt(const AttnParams& p, bool bf16, int sms, cudaStream_t st);
 size_t attn_kv4_prompt_ws(const Kv4View& c, int sms);
 
+// Norm and quantiser of rows (wq_norm.cu).
+struct NormParams {
+    const void* x;
+    const void* residual;      // null: none
+    void* sum;
+    const void* weight;
+    void* out;                 // 16-bit output, or
+    uint8_t* codes;            // e4m3 [T][H] with
+    float* scales;             // [blocks of 128][T]
+    int64_t x_stride, r_stride, sum_stride, out_stride;   // elements
+    int64_t T;
+    int H;
+    float eps, inv_h;
+    FastDiv div_blocks;        // quantiser: blocks of threads for each 16 tokens
+};
+cudaError_t launch_add_rms_norm(const NormParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_quantize_fp8(const NormParams& p, bool bf16, int sms, cudaStream_t st);
+
+// Products of 8-bit activations and 8-bit weights (wq_gemm_w8a8.cu).
+struct W8A8Params {
+    const uint8_t* a;          // e4m3 [M][K]
+    const float* a_scale;      // [kblocks][M]
+    const uint8_t* w;          // e4m3 [N][K]; gated: the gate's N rows, then the N of up
+    const float* w_scale;      // [blocks of 128 rows][kblocks]; gated: twice that
+    const void* bias;          // null or 16-bit [N]
+    void* out;                 // 16-bit [M][N], or
+    uint8_t* codes;            // gated: e4m3 [M][N] with
+    float* scales;             // [blocks of 128][M]
+    int64_t M, N;
+    int K, kblocks;
+    bool gated, out_bf16;
+    uint32_t* status;
+    long long timeout_ns;
+};
+cudaError_t launch_w8a8(const W8A8Params& p, int sms, cudaStream_t st);
+
 // A launch whose prologue may overlap the end of the kernel before it on the stream; the
 // kernel waits (griddepcontrol.wait) before it touches memory.
 template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+cudaError_t launch_pdl(void (*kernel)(Params...), unsigned grid, dim3 threads, size_t smem, cudaStream_t st,
                        const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
