@@ -467,6 +467,18 @@ const int64_t kMaxDim = (1LL << 31) - 1;
 
 }  // namespace
 
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    const auto fn = encode_fn();
+    if (!fn || rank < 1 || rank > 3) return false;
+    cuuint64_t d[3], s[2];
+    cuuint32_t b[3], es[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
+    for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
+    return fn(m, dt, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int current_device_state(DeviceState* out) {
     DeviceInfo* d = nullptr;
     const wq_status st = device_info(&d);

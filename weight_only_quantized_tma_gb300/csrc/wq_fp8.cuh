@@ -38,4 +38,14 @@ struct BlockScale {
     }
 };
 
+// The largest magnitude of a warp's values in every lane; a NaN among them gives NaN.
+__device__ __forceinline__ float warp_most(float v) {
+    float r;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// g / (1 + exp(-g)): -0 far below (exp overflows to infinity), NaN at minus infinity (0 times it).
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
 }  // namespace wq

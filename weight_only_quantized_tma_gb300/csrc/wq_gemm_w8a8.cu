@@ -1,102 +1,111 @@
 // wq_gemm_w8a8.cu -- products of 8-bit activations and 8-bit weights (include/wq.h: wq_gemm_w8a8_fp8,
-// wq_gemm_w8a8_fp8_gated).
-//
-//   out[m, n] = sum_kb  a_scale[kb, m] w_scale[n / 128, kb]  sum_{k in kb} a[m, k] w[n, k]
-//
-// Plain kernel: 32 tokens x 128 weight rows for each block of 256 threads, products and sums in fp32.
-#include "wq_fp8.cuh"
+// wq_gemm_w8a8_fp8_gated): which kernel, its tensor maps, its launch.
+#include <algorithm>
+#include <mutex>
+
+#include "wq_w8a8_narrow.cuh"
 
 namespace wq {
 namespace {
 
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-    const uint32_t h = ptx::e4m3x2_to_f16x2(v);
-    return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
-}
+constexpr int kMaxDevices = 64;
+constexpr int kMaxSplits = 8;
 
-template <bool GATED>
-__global__ void __launch_bounds__(256) w8a8_plain_kernel(const W8A8Params p) {
-    constexpr int P = GATED ? 2 : 1;
-    __shared__ float as[32][33], ws[P][128][33];
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
-    const int64_t m0 = (int64_t)blockIdx.y * 32;
-    const int nb = blockIdx.x, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;   // rows tx + 32 j, tokens ty * 4 + i
-    const int64_t n0 = (int64_t)nb * 128;
-    const int64_t nblocks = (p.N + 127) / 128;
-    float acc[P][4][4] = {};
-    for (int kb = 0; kb < p.kblocks; ++kb) {
-        float part[P][4][4] = {};
-        for (int k0 = kb * 128; k0 < kb * 128 + 128 && k0 < p.K; k0 += 32) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < 32 * 32; e += 256) {
-                const int64_t m = m0 + e / 32;
-                const int k = k0 + e % 32;
-                as[e / 32][e % 32] = m < p.M && k < p.K ? from_e4m3(p.a[m * p.K + k]) : 0.f;
+// One instantiation: its attributes, and how many clusters of S blocks the device holds at once (asked once for
+// each device).
+template <typename C>
+struct Narrow {
+    static constexpr auto kernel = w8a8_narrow_kernel<C>;
+    struct Device {
+        std::once_flag once;
+        cudaError_t err = cudaSuccess;
+        int clusters[kMaxSplits + 1] = {};
+    };
+    static const Device* device(int sms) {
+        static Device devices[kMaxDevices];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+        Device& d = devices[dev];
+        std::call_once(d.once, [&]() {
+            d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+            int blocks = 0;
+            if (d.err == cudaSuccess)
+                d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, C::NTHREADS, C::SMEM);
+            d.clusters[1] = std::max(1, blocks) * sms;
+            for (int S = 2; S <= C::SMAX && d.err == cudaSuccess; ++S) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr = {};
+                fill(cfg, &attr, (unsigned)S, S, nullptr);
+                int n = 0;
+                if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) (void)cudaGetLastError(), n = 0;
+                d.clusters[S] = n - (n + 15) / 16;   // (fewer are placed at once than the query reports)
             }
-            for (int h = 0; h < P; ++h)
-                for (int e = threadIdx.x; e < 128 * 32; e += 256) {
-                    const int64_t n = n0 + e / 32;
-                    const int k = k0 + e % 32;
-                    ws[h][e / 32][e % 32] = n < p.N && k < p.K ? from_e4m3(p.w[(h * p.N + n) * p.K + k]) : 0.f;
-                }
-            __syncthreads();
-            for (int k = 0; k < 32; ++k)
-#pragma unroll
-                for (int h = 0; h < P; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[h][i][j] += as[ty * 4 + i][k] * ws[h][tx + 32 * j][k];
-        }
-#pragma unroll
-        for (int h = 0; h < P; ++h) {
-            const float sw = p.w_scale[(h * nblocks + nb) * p.kblocks + kb];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t m = m0 + ty * 4 + i;
-                const float s = m < p.M ? sw * p.a_scale[(int64_t)kb * p.M + m] : 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[h][i][j] += s * part[h][i][j];
-            }
-        }
+        });
+        return d.err == cudaSuccess ? &d : nullptr;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + ty * 4 + i;
-        float v[4], top = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tx + 32 * j;
-            v[j] = acc[0][i][j];
-            if (GATED) v[j] = v[j] / (1.f + __expf(-v[j])) * acc[P - 1][i][j];
-            if (!GATED && p.bias != nullptr && n < p.N) v[j] += p.out_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[n]) : __half2float(static_cast<const __half*>(p.bias)[n]);
-            if (n < p.N) top = max_nan(top, fabsf(v[j]));
-            if (p.out != nullptr && m < p.M && n < p.N) {
-                if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[m * p.N + n] = __float2bfloat16_rn(v[j]);
-                else static_cast<__half*>(p.out)[m * p.N + n] = __float2half_rn(v[j]);
-            }
-        }
-        if (GATED && p.codes != nullptr) {
-            for (int off = 16; off > 0; off >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const BlockScale q(top);
-            if (m < p.M) {
-                for (int j = 0; j < 4; ++j)
-                    if (n0 + tx + 32 * j < p.N) p.codes[m * p.N + n0 + tx + 32 * j] = q.inv == 0.f ? 0 : (uint8_t)to_e4m3x4(v[j] * q.inv, 0.f, 0.f, 0.f);
-                if (tx == 0) p.scales[(int64_t)nb * p.M + m] = q.scale;
-            }
-        }
+    static void fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned grid, int S, cudaStream_t st) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(C::NTHREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = st;
+        attr->id = cudaLaunchAttributeClusterDimension;
+        attr->val.clusterDim.x = (unsigned)S;
+        attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
     }
-}
+    static cudaError_t launch(W8A8Params p, int sms, cudaStream_t st) {
+        const Device* d = device(sms);
+        if (!d) return cudaErrorInvalidDevice;
+        const int64_t tiles_m = (p.M + C::BN - 1) / C::BN, tiles_n = (p.N + 127) / 128, tiles = tiles_m * tiles_n;
+        if (tiles * kMaxSplits >= (1LL << 31)) return cudaErrorInvalidValue;
+        // Slices of K: the rounds of clusters times (blocks of a slice, and 4 blocks' time to start and end),
+        // and 2 blocks' time for the exchange.
+        int S = 1;
+        int64_t best = 0;
+        for (int s = 1; s <= C::SMAX && (s == 1 || p.kblocks >= 2 * s); ++s) {
+            if (d->clusters[s] < 1) continue;
+            const int64_t rounds = (tiles + d->clusters[s] - 1) / d->clusters[s];
+            const int64_t cost = rounds * ((p.kblocks + s - 1) / s + 4) + (s > 1 ? 2 : 0);
+            if (s == 1 || cost < best) S = s, best = cost;
+        }
+        p.tiles_m = (int)tiles_m;
+        p.tiles_n = (int)tiles_n;
+        p.splits = S;
+        p.box_m = (int)std::min<int64_t>(C::BN, p.M);
+        const uint64_t a_dims[2] = {(uint64_t)p.K, (uint64_t)p.M}, a_strides[1] = {(uint64_t)p.K};
+        const uint64_t w_dims[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)C::H};
+        const uint64_t w_strides[2] = {(uint64_t)p.K, (uint64_t)p.K * p.N};
+        const uint32_t a_box[2] = {128, (uint32_t)p.box_m}, w_box[3] = {128, 128, 1};
+        if (!encode_tensor_map(&p.tmap_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a, 2, a_dims, a_strides, a_box,
+                               CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tensor_map(&p.tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, 3, w_dims, w_strides, w_box,
+                               CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2] = {};
+        fill(cfg, &attr[1], (unsigned)(tiles * S), S, st);
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = S > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kernel, p);
+    }
+};
 
 }  // namespace
 
 cudaError_t launch_w8a8(const W8A8Params& p, int sms, cudaStream_t st) {
-    (void)sms;
-    const dim3 grid((unsigned)((p.N + 127) / 128), (unsigned)((p.M + 31) / 32));
-    if (p.gated) w8a8_plain_kernel<true><<<grid, 256, 0, st>>>(p);
-    else w8a8_plain_kernel<false><<<grid, 256, 0, st>>>(p);
-    return cudaGetLastError();
+    if (p.gated) {
+        if (p.M <= 16) return Narrow<NarrowCfg<16, true, 2, 4, 2>>::launch(p, sms, st);
+        if (p.M <= 32) return Narrow<NarrowCfg<32, true, 2, 2, 2>>::launch(p, sms, st);
+        return Narrow<NarrowCfg<64, true, 3, 4, 1>>::launch(p, sms, st);
+    }
+    if (p.M <= 16) return Narrow<NarrowCfg<16, false, 4, 8, 2>>::launch(p, sms, st);
+    if (p.M <= 32) return Narrow<NarrowCfg<32, false, 4, 8, 2>>::launch(p, sms, st);
+    if (p.M <= 64) return Narrow<NarrowCfg<64, false, 3, 3, 2>>::launch(p, sms, st);
+    return Narrow<NarrowCfg<128, false, 4, 4, 1>>::launch(p, sms, st);
 }
 
 }  // namespace wq

@@ -324,8 +324,14 @@ struct NormParams {
 cudaError_t launch_add_rms_norm(const NormParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_quantize_fp8(const NormParams& p, bool bf16, int sms, cudaStream_t st);
 
+// A tiled tensor map (wq_api.cu): `rank` dimensions, innermost first, strides in bytes of the outer ones.
+bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
+
 // Products of 8-bit activations and 8-bit weights (wq_gemm_w8a8.cu).
 struct W8A8Params {
+    CUtensorMap tmap_a;        // activations {K, M}, 128-byte swizzle
+    CUtensorMap tmap_w;        // weights {K, N, halves}, 128-byte swizzle
     const uint8_t* a;          // e4m3 [M][K]
     const float* a_scale;      // [kblocks][M]
     const uint8_t* w;          // e4m3 [N][K]; gated: the gate's N rows, then the N of up
@@ -336,6 +342,9 @@ struct W8A8Params {
     float* scales;             // [blocks of 128][M]
     int64_t M, N;
     int K, kblocks;
+    int tiles_m, tiles_n;      // token tiles, weight tiles
+    int splits;                // slices of K, one cluster for each tile
+    int box_m;                 // token rows of a copy
     bool gated, out_bf16;
     uint32_t* status;
     long long timeout_ns;
