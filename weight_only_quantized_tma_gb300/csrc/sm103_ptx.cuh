@@ -6,7 +6,7 @@
 //   * tcgen05: TMEM alloc/dealloc, MMA (kind::f16, A operand in TMEM), commit,
 //     32x32b loads/stores, and the thread-sync fences,
 //   * narrow-float converts (e4m3x2 / e2m1x2 -> f16x2).
-// No multicast form of any copy is defined here.
+// No multicast form of any copy is defined here (one commit arrives on both CTAs of a pair).
 #pragma once
 
 #include <cstdint>
@@ -304,6 +304,14 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                      : "memory");
+}
+
+// The same for the barriers at this offset in both CTAs of a pair.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

@@ -4,6 +4,7 @@
 #include <mutex>
 
 #include "wq_w8a8_narrow.cuh"
+#include "wq_w8a8_wide.cuh"
 
 namespace wq {
 namespace {
@@ -94,9 +95,81 @@ struct Narrow {
     }
 };
 
+// Pairs of blocks over tiles of 256 tokens x 256 weight rows.
+template <bool GATED>
+struct Wide {
+    using C = WideCfg<GATED>;
+    static constexpr auto kernel = w8a8_wide_kernel<C>;
+    struct Device {
+        std::once_flag once;
+        cudaError_t err = cudaSuccess;
+        int pairs = 0;       // held at once
+    };
+    static const Device* device() {
+        static Device devices[kMaxDevices];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+        Device& d = devices[dev];
+        std::call_once(d.once, [&]() {
+            d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr = {};
+            fill(cfg, &attr, 2, nullptr);
+            if (d.err == cudaSuccess) d.err = cudaOccupancyMaxActiveClusters(&d.pairs, kernel, &cfg);
+        });
+        return d.err == cudaSuccess && d.pairs > 0 ? &d : nullptr;
+    }
+    static void fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, unsigned grid, cudaStream_t st) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(C::NTHREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cfg.stream = st;
+        attr->id = cudaLaunchAttributeClusterDimension;
+        attr->val.clusterDim.x = 2;
+        attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    static cudaError_t launch(W8A8Params p, cudaStream_t st) {
+        const Device* d = device();
+        if (!d) return cudaErrorInvalidDevice;
+        const int64_t tiles_m = (p.M + 255) / 256, tiles_n = (p.N + C::TILE_N - 1) / C::TILE_N;
+        if (tiles_m * tiles_n >= (1LL << 30)) return cudaErrorInvalidValue;
+        p.tiles_m = (int)tiles_m;
+        p.tiles_n = (int)tiles_n;
+        // the smaller operand's tiles run fastest, so that it stays in L2
+        p.walk_n_fast = p.N * C::H < p.M;
+        p.div_walk = make_fastdiv((uint32_t)(p.walk_n_fast ? tiles_n : tiles_m), (uint32_t)(tiles_m * tiles_n));
+        const uint64_t a_dims[2] = {(uint64_t)p.K, (uint64_t)p.M}, a_strides[1] = {(uint64_t)p.K};
+        const uint64_t w_dims[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)C::H};
+        const uint64_t w_strides[2] = {(uint64_t)p.K, (uint64_t)p.K * p.N};
+        const uint32_t a_box[2] = {128, 128}, w_box[3] = {128, 128 / C::H, 1};
+        const bool codes = p.out == nullptr;
+        const uint64_t o_dims[2] = {(uint64_t)p.N, (uint64_t)p.M}, o_strides[1] = {(uint64_t)p.N * (codes ? 1 : 2)};
+        const uint32_t o_box[2] = {64, 32};
+        if (!encode_tensor_map(&p.tmap_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a, 2, a_dims, a_strides, a_box,
+                               CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tensor_map(&p.tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, 3, w_dims, w_strides, w_box,
+                               CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tensor_map(&p.tmap_out, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                               codes ? (const void*)p.codes : p.out, 2, o_dims, o_strides, o_box,
+                               codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[2] = {};
+        fill(cfg, &attr[1], 2 * (unsigned)std::min<int64_t>(tiles_m * tiles_n, d->pairs), st);
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kernel, p);
+    }
+};
+
 }  // namespace
 
 cudaError_t launch_w8a8(const W8A8Params& p, int sms, cudaStream_t st) {
+    if (p.M >= 256) return p.gated ? Wide<true>::launch(p, st) : Wide<false>::launch(p, st);
     if (p.gated) {
         if (p.M <= 16) return Narrow<NarrowCfg<16, true, 2, 4, 2>>::launch(p, sms, st);
         if (p.M <= 32) return Narrow<NarrowCfg<32, true, 2, 2, 2>>::launch(p, sms, st);

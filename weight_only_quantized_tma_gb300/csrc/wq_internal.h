@@ -332,6 +332,7 @@ bool encode_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base,
 struct W8A8Params {
     CUtensorMap tmap_a;        // activations {K, M}, 128-byte swizzle
     CUtensorMap tmap_w;        // weights {K, N, halves}, 128-byte swizzle
+    CUtensorMap tmap_out;      // many tokens: the output {N, M}
     const uint8_t* a;          // e4m3 [M][K]
     const float* a_scale;      // [kblocks][M]
     const uint8_t* w;          // e4m3 [N][K]; gated: the gate's N rows, then the N of up
@@ -345,6 +346,8 @@ struct W8A8Params {
     int tiles_m, tiles_n;      // token tiles, weight tiles
     int splits;                // slices of K, one cluster for each tile
     int box_m;                 // token rows of a copy
+    FastDiv div_walk;          // many tokens: tiles in the order of the walk
+    bool walk_n_fast;
     bool gated, out_bf16;
     uint32_t* status;
     long long timeout_ns;

@@ -1,0 +1,299 @@
+// wq_w8a8_wide.cuh -- product of e4m3 activations and e4m3 weights for many tokens: tokens are the tensor
+// cores' M dimension, so a thread's row has one activation scale and its 128 columns one weight scale.
+//
+//   acc[m][n] += (a_scale[kb][m] w_scale[n / 128][kb]) * D_kb[m][n]
+//
+// A pair of blocks (cluster of two, cta_group::2) computes 256 tokens x 256 weight rows: each holds its 128
+// tokens and the copies of half of the weight rows, D_kb of 128 k is one accumulation of four products in one
+// of two buffers of tensor memory (256 columns each, all 512), and while the tensor cores fill one, eight warps
+// read the other, scale it and add it in registers (128 columns for each thread of two warpgroups).  GATED: the
+// 256 rows are 64 of the gate, the same 64 of up, the next 64 of the gate, of up, so a thread holds gate and up
+// of the same 64 numbers, and the pair's tile is one block of 128 of the output.
+#pragma once
+
+#include "wq_common.cuh"
+#include "wq_fp8.cuh"
+
+namespace wq {
+
+template <bool GATED_>
+struct WideCfg {
+    static constexpr bool GATED = GATED_;
+    static constexpr int H = GATED ? 2 : 1;
+    static constexpr int NTHREADS = 384;        // warp 0 copies, 1 products, 2 tensor memory, 4-11 sums
+    static constexpr int STAGES = GATED ? 6 : 5;
+    static constexpr int STAGE = 2 * 128 * 128;             // 128 tokens, 128 weight rows
+    static constexpr int OUT_WARP = GATED ? 4096 : 8192;    // a warp's part of the output: 32 rows of 128 or 256 bytes
+    static constexpr int OFF_OUT = STAGES * STAGE;
+    static constexpr int MOST = 2048;           // codes take half of a warp's part; largest magnitudes [2 tiles][32] behind
+    static constexpr int OFF_BAR = OFF_OUT + 8 * OUT_WARP;
+    static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;         // full, empty, acc full / empty (2), pairs of warps (4), final
+    static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static constexpr int TILE_N = GATED ? 128 : 256;            // columns of the output
+    // registers: 168 x 384 at launch = 72 x 128 + 216 x 256
+    static constexpr int REGS_ISSUE = 72, REGS_SUM = 216;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <typename C>
+__global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_constant__ W8A8Params p) {
+    constexpr int STAGES = C::STAGES, H = C::H;
+    constexpr bool GATED = C::GATED;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t bar0 = sbase + C::OFF_BAR;
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+    auto pair_bar = [&](int q) { return bar0 + 8u * (2 * STAGES + 4 + q); };
+    const uint32_t final_bar = bar0 + 8u * (2 * STAGES + 8);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank();     // 0 issues the products of both
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(full(s), rank == 0 ? 2 : 1);   // its own copies, and the other block's, passed on
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 16);
+        for (int q = 0; q < 4; ++q) ptx::mbar_init(pair_bar(q), 2);
+        ptx::mbar_init(final_bar, 1);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+        ptx::prefetch_tmap(&p.tmap_a);
+        ptx::prefetch_tmap(&p.tmap_w);
+        ptx::prefetch_tmap(&p.tmap_out);
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc<2>(sbase + C::OFF_MISC, 512);
+        ptx::tmem_relinquish<2>();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();      // both blocks' barriers are initialised
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    const int n_tiles = p.tiles_m * p.tiles_n, first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+    auto tile_at = [&](int t, int& mt, int& nt) {
+        const int q = (int)fastdiv((uint32_t)t, p.div_walk), r = t - q * (int)p.div_walk.d;
+        mt = p.walk_n_fast ? q : r;
+        nt = p.walk_n_fast ? r : q;
+    };
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
+        if (ok) ok = bounded_wait<true>(bar, parity, abort_flag, p.status, code, p.timeout_ns);
+        return ok;
+    };
+
+    if (warp < 4) {
+        ptx::regs_dec<C::REGS_ISSUE>();
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------------------- copies
+            const uint64_t pol = ptx::policy_evict_last();
+            int s = 0;
+            uint32_t ph = 0;
+            long long issued = 0;
+            for (int t = first; t < n_tiles && ok; t += step) {
+                int mt, nt;
+                tile_at(t, mt, nt);
+                for (int kb = 0; kb < p.kblocks && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++kb) {
+                    const uint32_t dst = sbase + s * C::STAGE;
+                    ptx::mbar_arrive_expect_tx(full(s), C::STAGE);
+                    ptx::tma_load_2d(dst, &p.tmap_a, kb * 128, mt * 256 + rank * 128, full(s), pol);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        ptx::tma_load_3d(dst + 16384 + h * 8192, &p.tmap_w, kb * 128, nt * C::TILE_N + rank * (128 / H), h,
+                                         full(s), pol);
+                    ++issued;
+                    if (++s == STAGES) s = 0, ph ^= 1u;
+                }
+            }
+            // every stage released: the commits that arrive here have all landed
+            for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
+                if (++s == STAGES) s = 0, ph ^= 1u;
+            if (!ok)
+                for (long long j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+                    if (!drain_wait(full((int)(j % STAGES)), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
+                        atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+        } else if (warp == 1 && lane == 0 && rank == 1) {
+            // -------------------------------------------------------- the landing of this block's copies, passed on
+            const uint32_t to = ptx::mapa_shared(full(0), 0);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int t = first; t < n_tiles && ok; t += step)
+                for (int kb = 0; kb < p.kblocks && wait(full(s), ph, DEVICE_TIMEOUT_MMA); ++kb) {
+                    ptx::mbar_arrive_cluster(to + 8u * s);
+                    if (++s == STAGES) s = 0, ph ^= 1u;
+                }
+        } else if (warp == 1 && lane == 0) {
+            // -------------------------------------------------------- products
+            constexpr uint32_t idesc = ptx::make_idesc_e4m3(256, 256);
+            int s = 0;
+            uint32_t ph = 0, n = 0;      // n: blocks of K so far, buffer n % 2
+            for (int t = first; t < n_tiles && ok; t += step)
+                for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
+                    const int b = n & 1u;
+                    if (!wait(acc_empty(b), (n >> 1 & 1u) ^ 1u, DEVICE_TIMEOUT_MMA) || !wait(full(s), ph, DEVICE_TIMEOUT_MMA))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint32_t a_lo = ptx::sdesc_lo(sbase + s * C::STAGE), b_lo = a_lo + (16384 >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_f8_ss<2>(tmem + b * 256, a_lo + 2 * k, ptx::kSdescHi, b_lo + 2 * k, ptx::kSdescHi, idesc, k > 0);
+                    ptx::mma_commit_pair(empty(s));
+                    ptx::mma_commit_pair(acc_full(b));
+                    if (++s == STAGES) s = 0, ph ^= 1u;
+                }
+            // the last arrivals of the other block land before this one may end
+            if (n > 0) wait(acc_empty((n - 1) & 1u), (n - 1) >> 1 & 1u, DEVICE_TIMEOUT_MMA);
+            if (n > 1) wait(acc_empty(n & 1u), (n - 2) >> 1 & 1u, DEVICE_TIMEOUT_MMA);
+            if (!ok) {
+                ptx::mma_commit<2>(final_bar);
+                if (!drain_wait(final_bar, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+            }
+        }
+        __syncwarp();
+    } else {
+        ptx::regs_inc<C::REGS_SUM>();
+        // ------------------------------------------------------------ sums
+        const int g = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + g * 128;
+        const uint32_t acc_empty0 = ptx::mapa_shared(acc_empty(0), 0);
+        const int64_t wblocks = (p.N + 127) >> 7;
+        uint8_t* out_s = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
+        uint32_t n = 0, turn = 0;
+        for (int t = first; t < n_tiles && ok; t += step, ++turn) {
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int64_t m = (int64_t)mt * 256 + rank * 128 + row;
+            // weight scales of this thread's columns: one block of rows, or one of each half
+            const int64_t wb = GATED ? nt : 2 * nt + g;
+            const float* sa = p.a_scale + (m < p.M ? m : 0);
+            const float* sw = p.w_scale + (wb < wblocks ? wb : 0) * p.kblocks;
+            const int64_t up = wblocks * p.kblocks;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            // scales of this block of K and the next, loaded two blocks ahead
+            float ra[2], rw[2][H];
+            auto fetch = [&](int i, int kb) {
+                if (kb < p.kblocks) {
+                    ra[i] = __ldg(sa + (int64_t)kb * p.M);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) rw[i][h] = __ldg(sw + h * up + kb);
+                }
+            };
+            auto block = [&](int i, int kb) {
+                const int b = n & 1u;
+                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) return false;
+                ++n;
+                ptx::tc_fence_after();
+                uint32_t v[2][32];
+                ptx::tmem_ld32(base + b * 256, v[0]);
+                uint64_t s[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) s[h] = f2(ra[i] * rw[i][h], ra[i] * rw[i][h]);
+                fetch(i, kb + 2);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ptx::tmem_wait_ld_of(v[c & 1]);
+                    if (c < 3) {
+                        ptx::tmem_ld32(base + b * 256 + 32 * (c + 1), v[(c + 1) & 1]);
+                    } else {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster(acc_empty0 + 8u * b);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const int col = 32 * c + j;
+                        const float2 r = un2(fma_f2(f2(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1])),
+                                                    s[GATED ? c >> 1 : 0], f2(acc[col], acc[col + 1])));
+                        acc[col] = r.x, acc[col + 1] = r.y;
+                    }
+                }
+                return true;
+            };
+            fetch(0, 0);
+            fetch(1, 1);
+            for (int kb = 0; kb < p.kblocks; kb += 2) {
+                if (!block(0, kb)) break;
+                if (kb + 1 < p.kblocks && !block(1, kb + 1)) break;
+            }
+            if (!ok) break;
+            // ---- output: through this warp's part of shared memory, 32 rows copied out by one thread
+            if (lane == 0) ptx::bulk_wait_group_read0();     // the last copy has read it
+            __syncwarp();
+            const int64_t n0 = (int64_t)nt * C::TILE_N + g * (128 / H);
+            const bool any = n0 < p.N && m - lane < p.M;      // the warp has something to store
+            if constexpr (GATED) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) acc[i] = silu(acc[i]) * acc[64 + i];
+            } else if (p.bias != nullptr && n0 < p.N) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (n0 + i < p.N)
+                        acc[i] += p.out_bf16 ? load_16bit<true>(p.bias, (size_t)(n0 + i)) : load_16bit<false>(p.bias, (size_t)(n0 + i));
+            }
+            if (!GATED || p.out != nullptr) {
+                // rows of 128 bytes (64 columns), in the order of the 128-byte swizzle
+#pragma unroll
+                for (int c = 0; c < 128 / H; c += 8) {
+                    const uint4 o = p.out_bf16 ? make_uint4(pack2<true>(acc[c], acc[c + 1]), pack2<true>(acc[c + 2], acc[c + 3]),
+                                                            pack2<true>(acc[c + 4], acc[c + 5]), pack2<true>(acc[c + 6], acc[c + 7]))
+                                               : make_uint4(pack2<false>(acc[c], acc[c + 1]), pack2<false>(acc[c + 2], acc[c + 3]),
+                                                            pack2<false>(acc[c + 4], acc[c + 5]), pack2<false>(acc[c + 6], acc[c + 7]));
+                    *reinterpret_cast<uint4*>(out_s + (c >> 6) * 4096 + swz(lane * 128 + (c & 63) * 2, 7)) = o;
+                }
+            } else {
+                // the block's largest: this thread's 64 and those of the same row in the other warpgroup
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) most = max_nan(most, fabsf(acc[i]));     // (past N: products of zeros)
+                const int at = C::MOST + (int)(turn & 1u) * 128 + 4 * lane;
+                *reinterpret_cast<float*>(out_s + at) = most;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(pair_bar(quarter));
+                if (!__all_sync(0xffffffffu, wait(pair_bar(quarter), turn & 1u, DEVICE_TIMEOUT_EPILOGUE))) break;
+                const BlockScale q(max_nan(most, *reinterpret_cast<const float*>(smem + C::OFF_OUT + ((warp - 4) ^ 4) * C::OUT_WARP + at)));
+                if (g == 0 && m < p.M) p.scales[(int64_t)nt * p.M + m] = q.scale;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float* a = acc + c + 4 * j;
+                        o[j] = q.inv == 0.f ? 0u : to_e4m3x4(a[0] * q.inv, a[1] * q.inv, a[2] * q.inv, a[3] * q.inv);
+                    }
+                    *reinterpret_cast<uint4*>(out_s + lane * 64 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && any) {
+                const int y = (int)(m - lane);
+                ptx::tma_store_2d(&p.tmap_out, ptx::smem_u32(out_s), (int)n0, y);
+                if (!GATED && n0 + 64 < p.N) ptx::tma_store_2d(&p.tmap_out, ptx::smem_u32(out_s) + 4096, (int)n0 + 64, y);
+                ptx::bulk_commit_group();
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_group0();
+        __syncwarp();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();      // neither block leaves, or frees tensor memory, while the other may need it
+    ptx::tc_fence_after();
+    if (warp == 2) ptx::tmem_dealloc<2>(tmem, 512);
+}
+
+}  // namespace wq
