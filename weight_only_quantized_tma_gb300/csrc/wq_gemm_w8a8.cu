@@ -134,16 +134,14 @@ struct Wide {
         const Device* d = device();
         if (!d) return cudaErrorInvalidDevice;
         const int64_t tiles_m = (p.M + 255) / 256, tiles_n = (p.N + C::TILE_N - 1) / C::TILE_N;
-        if (tiles_m * tiles_n >= (1LL << 30)) return cudaErrorInvalidValue;
+        if (tiles_m * tiles_n >= (1LL << 30) || tiles_n >= (1LL << 27)) return cudaErrorInvalidValue;
         p.tiles_m = (int)tiles_m;
         p.tiles_n = (int)tiles_n;
-        // the smaller operand's tiles run fastest, so that it stays in L2
-        p.walk_n_fast = p.N * C::H < p.M;
-        p.div_walk = make_fastdiv((uint32_t)(p.walk_n_fast ? tiles_n : tiles_m), (uint32_t)(tiles_m * tiles_n));
+        p.div_group = make_fastdiv((uint32_t)(C::GROUP * tiles_n), (uint32_t)(tiles_m * tiles_n));
         const uint64_t a_dims[2] = {(uint64_t)p.K, (uint64_t)p.M}, a_strides[1] = {(uint64_t)p.K};
         const uint64_t w_dims[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)C::H};
         const uint64_t w_strides[2] = {(uint64_t)p.K, (uint64_t)p.K * p.N};
-        const uint32_t a_box[2] = {128, 128}, w_box[3] = {128, 128 / C::H, 1};
+        const uint32_t a_box[2] = {128, 128}, w_box[3] = {128, 64, 1};
         const bool codes = p.out == nullptr;
         const uint64_t o_dims[2] = {(uint64_t)p.N, (uint64_t)p.M}, o_strides[1] = {(uint64_t)p.N * (codes ? 1 : 2)};
         const uint32_t o_box[2] = {64, 32};

@@ -346,8 +346,7 @@ struct W8A8Params {
     int tiles_m, tiles_n;      // token tiles, weight tiles
     int splits;                // slices of K, one cluster for each tile
     int box_m;                 // token rows of a copy
-    FastDiv div_walk;          // many tokens: tiles in the order of the walk
-    bool walk_n_fast;
+    FastDiv div_group;         // many tokens: tiles of a group of token tiles
     bool gated, out_bf16;
     uint32_t* status;
     long long timeout_ns;

@@ -31,6 +31,7 @@ struct WideCfg {
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TILE_N = GATED ? 128 : 256;            // columns of the output
+    static constexpr int GROUP = 8;             // token tiles that the walk keeps together
     // registers: 168 x 384 at launch = 72 x 128 + 216 x 256
     static constexpr int REGS_ISSUE = 72, REGS_SUM = 216;
     static_assert(SMEM <= 232448, "shared memory");
@@ -83,10 +84,13 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
     ptx::grid_launch_dependents();
 
     const int n_tiles = p.tiles_m * p.tiles_n, first = (int)(blockIdx.x >> 1), step = (int)(gridDim.x >> 1);
+    // GROUP token tiles at a time, theirs fastest: the tiles in flight are about as many of one kind as of the
+    // other, so that they read few panels and write neighbouring columns
     auto tile_at = [&](int t, int& mt, int& nt) {
-        const int q = (int)fastdiv((uint32_t)t, p.div_walk), r = t - q * (int)p.div_walk.d;
-        mt = p.walk_n_fast ? q : r;
-        nt = p.walk_n_fast ? r : q;
+        const int q = (int)fastdiv((uint32_t)t, p.div_group), r = t - q * (int)p.div_group.d;
+        const int high = min(C::GROUP, p.tiles_m - q * C::GROUP);
+        nt = r / high;
+        mt = q * C::GROUP + r - nt * high;
     };
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
@@ -110,9 +114,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                     ptx::mbar_arrive_expect_tx(full(s), C::STAGE);
                     ptx::tma_load_2d(dst, &p.tmap_a, kb * 128, mt * 256 + rank * 128, full(s), pol);
 #pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        ptx::tma_load_3d(dst + 16384 + h * 8192, &p.tmap_w, kb * 128, nt * C::TILE_N + rank * (128 / H), h,
-                                         full(s), pol);
+                    for (int i = 0; i < 2; ++i)    // 64 rows of the gate and of up, or 128 rows
+                        ptx::tma_load_3d(dst + 16384 + i * 8192, &p.tmap_w, kb * 128,
+                                         nt * C::TILE_N + (GATED ? 64 * rank : 128 * rank + 64 * i), GATED ? i : 0, full(s), pol);
                     ++issued;
                     if (++s == STAGES) s = 0, ph ^= 1u;
                 }
@@ -197,27 +201,27 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) return false;
                 ++n;
                 ptx::tc_fence_after();
-                uint32_t v[2][32];
-                ptx::tmem_ld32(base + b * 256, v[0]);
+                uint32_t v[2][16];
+                ptx::tmem_ld16(base + b * 256, v[0]);
                 uint64_t s[H];
 #pragma unroll
                 for (int h = 0; h < H; ++h) s[h] = f2(ra[i] * rw[i][h], ra[i] * rw[i][h]);
                 fetch(i, kb + 2);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     ptx::tmem_wait_ld_of(v[c & 1]);
-                    if (c < 3) {
-                        ptx::tmem_ld32(base + b * 256 + 32 * (c + 1), v[(c + 1) & 1]);
+                    if (c < 7) {
+                        ptx::tmem_ld16(base + b * 256 + 16 * (c + 1), v[(c + 1) & 1]);
                     } else {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_cluster(acc_empty0 + 8u * b);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const int col = 32 * c + j;
+                    for (int j = 0; j < 16; j += 2) {
+                        const int col = 16 * c + j;
                         const float2 r = un2(fma_f2(f2(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1])),
-                                                    s[GATED ? c >> 1 : 0], f2(acc[col], acc[col + 1])));
+                                                    s[GATED ? c >> 2 : 0], f2(acc[col], acc[col + 1])));
                         acc[col] = r.x, acc[col + 1] = r.y;
                     }
                 }
