@@ -20,13 +20,22 @@ template <bool GATED_>
 struct WideCfg {
     static constexpr bool GATED = GATED_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 384;        // warp 0 copies, 1 products, 2 tensor memory, 4-11 sums
-    static constexpr int STAGES = GATED ? 6 : 5;
+    static constexpr int NTHREADS = 384;        // warp 0 copies and scales, 1 products, 2 tensor memory, 4-11 sums
+    static constexpr int STAGES = GATED ? 5 : 4;
     static constexpr int STAGE = 2 * 128 * 128;             // 128 tokens, 128 weight rows
     static constexpr int OUT_WARP = GATED ? 4096 : 8192;    // a warp's part of the output: 32 rows of 128 or 256 bytes
     static constexpr int OFF_OUT = STAGES * STAGE;
     static constexpr int MOST = 2048;           // codes take half of a warp's part; largest magnitudes [2 tiles][32] behind
-    static constexpr int OFF_BAR = OFF_OUT + 8 * OUT_WARP;
+    // Scales of a block of K: 128 tokens', two of the weights.  They are part of the block's stage (its products wait
+    // for them too), so that sums that can be read find their scales without a wait of their own: a wait beside
+    // tensor cores that read shared memory takes about 100 cycles, and loads straight into registers came too late
+    // (8192 x 4096 x 11008: 363 us with a barrier of their own, 356 us with loads two blocks ahead).  A slot is
+    // filled again SCN blocks on, when the products of STAGES blocks before that have ended, for which the sums
+    // two blocks earlier had to be read: nobody reads it any more.
+    static constexpr int SCN = 8;
+    static constexpr int SC_SLOT = 130 * 4 + 8;
+    static constexpr int OFF_SC = OFF_OUT + 8 * OUT_WARP;
+    static constexpr int OFF_BAR = OFF_SC + SCN * SC_SLOT;
     static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;         // full, empty, acc full / empty (2), pairs of warps (4), final
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
@@ -34,12 +43,13 @@ struct WideCfg {
     static constexpr int GROUP = 8;             // token tiles that the walk keeps together
     // registers: 168 x 384 at launch = 72 x 128 + 216 x 256
     static constexpr int REGS_ISSUE = 72, REGS_SUM = 216;
+    static_assert(SCN >= STAGES + 2 && (SCN & (SCN - 1)) == 0 && OFF_BAR % 8 == 0, "scales");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
 template <typename C>
 __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_constant__ W8A8Params p) {
-    constexpr int STAGES = C::STAGES, H = C::H;
+    constexpr int STAGES = C::STAGES, H = C::H, SCN = C::SCN;
     constexpr bool GATED = C::GATED;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -58,7 +68,8 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            ptx::mbar_init(full(s), rank == 0 ? 2 : 1);   // its own copies, and the other block's, passed on
+            // its own copies, its scales, and the other block's of both, passed on
+            ptx::mbar_init(full(s), rank == 0 ? 34 : 33);
             ptx::mbar_init(empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 16);
@@ -92,6 +103,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         nt = r / high;
         mt = q * C::GROUP + r - nt * high;
     };
+    const int64_t wblocks = (p.N + 127) >> 7;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity, uint32_t code) {
         if (ok) ok = bounded_wait<true>(bar, parity, abort_flag, p.status, code, p.timeout_ns);
@@ -100,34 +112,52 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
 
     if (warp < 4) {
         ptx::regs_dec<C::REGS_ISSUE>();
-        if (warp == 0 && lane == 0) {
-            // -------------------------------------------------------- copies
+        if (warp == 0) {
+            // -------------------------------------------------------- copies and scales
             const uint64_t pol = ptx::policy_evict_last();
-            int s = 0;
+            int s = 0, c = 0;
             uint32_t ph = 0;
             long long issued = 0;
             for (int t = first; t < n_tiles && ok; t += step) {
                 int mt, nt;
                 tile_at(t, mt, nt);
-                for (int kb = 0; kb < p.kblocks && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++kb) {
-                    const uint32_t dst = sbase + s * C::STAGE;
-                    ptx::mbar_arrive_expect_tx(full(s), C::STAGE);
-                    ptx::tma_load_2d(dst, &p.tmap_a, kb * 128, mt * 256 + rank * 128, full(s), pol);
+                const int64_t m0 = (int64_t)mt * 256 + rank * 128;
+                const int rows = (int)max((int64_t)0, min((int64_t)128, p.M - m0));
+                const float* sa = p.a_scale + (rows > 0 ? m0 : 0);
+                // lanes 0 and 1: the tile's two blocks of weight rows, or the gate's and up's
+                const int64_t wb = GATED ? (lane & 1) * wblocks + nt : min((int64_t)2 * nt + (lane & 1), wblocks - 1);
+                const float* sw = p.w_scale + wb * p.kblocks;
+                for (int kb = 0; kb < p.kblocks; ++kb) {
+                    if (!__all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER))) break;
+                    if (lane == 0) {
+                        const uint32_t dst = sbase + s * C::STAGE;
+                        ptx::mbar_arrive_expect_tx(full(s), C::STAGE);
+                        ptx::tma_load_2d(dst, &p.tmap_a, kb * 128, (int)m0, full(s), pol);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)    // 64 rows of the gate and of up, or 128 rows
-                        ptx::tma_load_3d(dst + 16384 + i * 8192, &p.tmap_w, kb * 128,
-                                         nt * C::TILE_N + (GATED ? 64 * rank : 128 * rank + 64 * i), GATED ? i : 0, full(s), pol);
+                        for (int i = 0; i < 2; ++i)    // 64 rows of the gate and of up, or 128 rows
+                            ptx::tma_load_3d(dst + 16384 + i * 8192, &p.tmap_w, kb * 128,
+                                             nt * C::TILE_N + (GATED ? 64 * rank : 128 * rank + 64 * i), GATED ? i : 0, full(s), pol);
+                    }
+                    __syncwarp();
+                    const uint32_t sc = sbase + C::OFF_SC + c * C::SC_SLOT;
+#pragma unroll
+                    for (int r = lane; r < 128; r += 32) ptx::cp_async4(sc + 4 * r, sa + (r < rows ? r : 0), r < rows);
+                    if (lane < 2) ptx::cp_async4(sc + 4 * (128 + lane), sw + kb, true);
+                    ptx::cp_async_arrive(full(s));
+                    sa += p.M;
                     ++issued;
                     if (++s == STAGES) s = 0, ph ^= 1u;
+                    if (++c == SCN) c = 0;
                 }
             }
             // every stage released: the commits that arrive here have all landed
             for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
                 if (++s == STAGES) s = 0, ph ^= 1u;
-            if (!ok)
+            if (!ok && lane == 0)
                 for (long long j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
                     if (!drain_wait(full((int)(j % STAGES)), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
                         atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+            ptx::cp_async_wait_all();
         } else if (warp == 1 && lane == 0 && rank == 1) {
             // -------------------------------------------------------- the landing of this block's copies, passed on
             const uint32_t to = ptx::mapa_shared(full(0), 0);
@@ -172,41 +202,25 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         const int g = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + g * 128;
         const uint32_t acc_empty0 = ptx::mapa_shared(acc_empty(0), 0);
-        const int64_t wblocks = (p.N + 127) >> 7;
         uint8_t* out_s = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
         uint32_t n = 0, turn = 0;
         for (int t = first; t < n_tiles && ok; t += step, ++turn) {
-            int mt, nt;
-            tile_at(t, mt, nt);
-            const int64_t m = (int64_t)mt * 256 + rank * 128 + row;
-            // weight scales of this thread's columns: one block of rows, or one of each half
-            const int64_t wb = GATED ? nt : 2 * nt + g;
-            const float* sa = p.a_scale + (m < p.M ? m : 0);
-            const float* sw = p.w_scale + (wb < wblocks ? wb : 0) * p.kblocks;
-            const int64_t up = wblocks * p.kblocks;
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            // scales of this block of K and the next, loaded two blocks ahead
-            float ra[2], rw[2][H];
-            auto fetch = [&](int i, int kb) {
-                if (kb < p.kblocks) {
-                    ra[i] = __ldg(sa + (int64_t)kb * p.M);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) rw[i][h] = __ldg(sw + h * up + kb);
-                }
-            };
-            auto block = [&](int i, int kb) {
-                const int b = n & 1u;
-                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) return false;
-                ++n;
+            for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
+                const uint32_t b = n & 1u;
+                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
                 ptx::tc_fence_after();
                 uint32_t v[2][16];
                 ptx::tmem_ld16(base + b * 256, v[0]);
+                const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + n % SCN * C::SC_SLOT);
                 uint64_t s[H];
 #pragma unroll
-                for (int h = 0; h < H; ++h) s[h] = f2(ra[i] * rw[i][h], ra[i] * rw[i][h]);
-                fetch(i, kb + 2);
+                for (int h = 0; h < H; ++h) {
+                    const float f = sc[row] * sc[128 + (GATED ? h : g)];
+                    s[h] = f2(f, f);
+                }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     ptx::tmem_wait_ld_of(v[c & 1]);
@@ -225,18 +239,14 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                         acc[col] = r.x, acc[col + 1] = r.y;
                     }
                 }
-                return true;
-            };
-            fetch(0, 0);
-            fetch(1, 1);
-            for (int kb = 0; kb < p.kblocks; kb += 2) {
-                if (!block(0, kb)) break;
-                if (kb + 1 < p.kblocks && !block(1, kb + 1)) break;
             }
             if (!ok) break;
             // ---- output: through this warp's part of shared memory, 32 rows copied out by one thread
             if (lane == 0) ptx::bulk_wait_group_read0();     // the last copy has read it
             __syncwarp();
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int64_t m = (int64_t)mt * 256 + rank * 128 + row;
             const int64_t n0 = (int64_t)nt * C::TILE_N + g * (128 / H);
             const bool any = n0 < p.N && m - lane < p.M;      // the warp has something to store
             if constexpr (GATED) {
