@@ -137,6 +137,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
         : "memory");
 }
 
+// A box of a tiled 3D tensor into L2 alone.  Nothing is read from it here, so it may be asked for before the
+// kernel that writes it has ended: L2 is where that kernel's writes arrive as well.
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // Tiled copy shared -> global of one box at (x, y) (x the innermost, a multiple of
 // 16 bytes); elements outside the tensor are not written.  Completion is tracked by
 // the bulk async-group of the issuing thread.
@@ -462,6 +469,14 @@ __device__ __forceinline__ void st_async_v4f32(uint32_t addr, float a, float b, 
 __device__ __forceinline__ void st_async_v2f32(uint32_t addr, float a, float b, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
                  "f"(a), "f"(b), "r"(bar)
+                 : "memory");
+}
+// Untiled copy from this CTA's shared memory to that of a CTA of the cluster (dst and bar from mapa_shared), its
+// bytes completing on the mbarrier there.  Addresses 16-byte aligned, bytes a multiple of 16; the source stays as it
+// is, and this CTA alive, until they have.
+__device__ __forceinline__ void bulk_send(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
 // Split cluster barrier: arrive without ordering (used once, right after barrier

@@ -30,17 +30,18 @@ struct Narrow {
         std::call_once(d.once, [&]() {
             d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-            int blocks = 0;
-            if (d.err == cudaSuccess)
-                d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, C::NTHREADS, C::SMEM);
-            d.clusters[1] = std::max(1, blocks) * sms;
+            // The query counts one block of a kernel with tensor memory for each SM; C::CTAS are resident (304 blocks of
+            // CTAS = 2 ran at once on 152 SMs, in clusters of two as well, 296 in clusters of four), and what the query
+            // leaves over in each part of the GPU then holds clusters too.
+            d.clusters[1] = C::CTAS * sms;
             for (int S = 2; S <= C::SMAX && d.err == cudaSuccess; ++S) {
                 cudaLaunchConfig_t cfg = {};
                 cudaLaunchAttribute attr = {};
                 fill(cfg, &attr, (unsigned)S, S, nullptr);
                 int n = 0;
                 if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) (void)cudaGetLastError(), n = 0;
-                d.clusters[S] = n - (n + 15) / 16;   // (fewer are placed at once than the query reports)
+                if (C::CTAS > 1) n = C::CTAS * n + std::max(0, sms - n * S) / S;
+                d.clusters[S] = n - (n + 31) / 32;   // (fewer are placed at once than the query reports)
             }
         });
         return d.err == cudaSuccess ? &d : nullptr;
@@ -169,14 +170,14 @@ struct Wide {
 cudaError_t launch_w8a8(const W8A8Params& p, int sms, cudaStream_t st) {
     if (p.M >= 256) return p.gated ? Wide<true>::launch(p, st) : Wide<false>::launch(p, st);
     if (p.gated) {
-        if (p.M <= 16) return Narrow<NarrowCfg<16, true, 2, 4, 2>>::launch(p, sms, st);
-        if (p.M <= 32) return Narrow<NarrowCfg<32, true, 2, 2, 2>>::launch(p, sms, st);
-        return Narrow<NarrowCfg<64, true, 3, 4, 1>>::launch(p, sms, st);
+        if (p.M <= 16) return Narrow<NarrowCfg<16, true, 3, 8, 2, true>>::launch(p, sms, st);
+        if (p.M <= 32) return Narrow<NarrowCfg<32, true, 3, 8, 2, true>>::launch(p, sms, st);
+        return Narrow<NarrowCfg<64, true, 4, 8, 1, true>>::launch(p, sms, st);
     }
-    if (p.M <= 16) return Narrow<NarrowCfg<16, false, 4, 8, 2>>::launch(p, sms, st);
-    if (p.M <= 32) return Narrow<NarrowCfg<32, false, 4, 8, 2>>::launch(p, sms, st);
-    if (p.M <= 64) return Narrow<NarrowCfg<64, false, 3, 3, 2>>::launch(p, sms, st);
-    return Narrow<NarrowCfg<128, false, 4, 4, 1>>::launch(p, sms, st);
+    if (p.M <= 16) return Narrow<NarrowCfg<16, false, 4, 8, 2, false>>::launch(p, sms, st);
+    if (p.M <= 32) return Narrow<NarrowCfg<32, false, 5, 8, 2, true>>::launch(p, sms, st);
+    if (p.M <= 64) return Narrow<NarrowCfg<64, false, 4, 8, 2, true>>::launch(p, sms, st);
+    return Narrow<NarrowCfg<128, false, 6, 8, 1, true>>::launch(p, sms, st);
 }
 
 }  // namespace wq

@@ -11,8 +11,9 @@
 // the 128 rows are the output's block.
 //
 // Few tokens are bound by reading the weights: `splits` blocks of threads, one cluster, share a tile's k, so that
-// the grid fills the GPU.  Each then sends its sums to the owners of the columns (tokens in groups of four) by
-// st.async; an owner adds the slices in order and finishes its tokens for all 128 rows.
+// the grid fills the GPU.  Each then lays its sums out in shared memory and sends each owner of columns (tokens in
+// groups of four) its part in one copy; an owner adds the slices in order and finishes its tokens for all 128 rows.
+// (16-byte stores that each count on the owner's barrier took longer than the products: 128 x 4096 x 4096 18.2 us.)
 #pragma once
 
 #include "wq_common.cuh"
@@ -20,26 +21,32 @@
 
 namespace wq {
 
-template <int BN_, bool GATED_, int STAGES_, int SMAX_, int CTAS_>
+// ALIAS: the slices' sums arrive in the stages' memory as well, behind one more cluster barrier.
+template <int BN_, bool GATED_, int STAGES_, int SMAX_, int CTAS_, bool ALIAS_>
 struct NarrowCfg {
     static constexpr int BN = BN_, STAGES = STAGES_, SMAX = SMAX_, CTAS = CTAS_;
-    static constexpr bool GATED = GATED_;
+    static constexpr bool GATED = GATED_, ALIAS = ALIAS_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 224;                    // warps 0-3 sums, 4 copies, 5 products, 6 scales
+    static constexpr int NTHREADS = 192;                    // warps 0-3 sums, 4 copies and scales, 5 products
     static constexpr int W_TILE = 128 * 128;
     static constexpr int STAGE = H * W_TILE + BN * 128;     // weight tiles, then the tokens' rows
-    static constexpr int SCN = 8;                           // slots of scales: BN tokens', then the weights'
+    // Scales of a block of K: BN tokens', then the weights'.  They are part of the block's stage (its products wait
+    // for them too).  A slot is filled again SCN blocks on, when the products of STAGES blocks before that have ended,
+    // for which the sums two blocks earlier had to be read: nobody reads it any more.
+    static constexpr int SCN = STAGES <= 2 ? 4 : 8;
     static constexpr int SC_SLOT = (BN + 4) * 4;
     static constexpr int OFF_SC = STAGES * STAGE;
-    static constexpr int OFF_INBOX = OFF_SC + SCN * SC_SLOT;
     static constexpr int INBOX = SMAX > 1 ? (BN / 4 + SMAX - 1) * 128 * 16 * H : 0;
-    static constexpr int OFF_MOST = OFF_INBOX + INBOX;      // largest magnitudes [4 warps][BN]
+    static constexpr int OUTBOX = SMAX > 1 ? BN / 4 * 128 * 16 * H : 0;      // in the stages
+    static constexpr int OFF_INBOX = ALIAS ? OUTBOX : OFF_SC + SCN * SC_SLOT;
+    static constexpr int OFF_MOST = OFF_SC + SCN * SC_SLOT + (ALIAS ? 0 : INBOX);      // largest magnitudes [4 warps][BN]
     static constexpr int OFF_BAR = OFF_MOST + (GATED ? 4 * BN * 4 : 0);
-    // barriers: full, empty (stages), acc full, acc empty (2), scales full, empty, inbox, final; then TMEM address, abort
-    static constexpr int NBAR = 2 * STAGES + 4 + 2 * SCN + 2;
+    // barriers: full, empty (stages), acc full, acc empty (2), inbox, final; then TMEM address, abort
+    static constexpr int NBAR = 2 * STAGES + 4 + 2;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TMEM_COLS = 2 * H * BN < 32 ? 32 : 2 * H * BN;
+    static_assert(SCN >= STAGES + 2 && OUTBOX + (ALIAS ? INBOX : 0) <= STAGES * STAGE, "scales, inbox");
     static_assert(STAGE % 1024 == 0 && OFF_INBOX % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
     static_assert(TMEM_COLS * CTAS <= 512 && SMEM <= (CTAS == 1 ? 232448 : 115712), "resident blocks");
 };
@@ -56,9 +63,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
     auto acc_empty = [&](int b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-    auto sc_full = [&](int s) { return bar0 + 8u * (2 * STAGES + 4 + s); };
-    auto sc_empty = [&](int s) { return bar0 + 8u * (2 * STAGES + 4 + SCN + s); };
-    const uint32_t inbox_bar = bar0 + 8u * (2 * STAGES + 4 + 2 * SCN), final_bar = inbox_bar + 8u;
+    const uint32_t inbox_bar = bar0 + 8u * (2 * STAGES + 4), final_bar = inbox_bar + 8u;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -75,9 +80,8 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     const int g0 = S > 1 ? rank * per : 0, own = max(0, min(per, groups - g0));
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) ptx::mbar_init(full(s), 1), ptx::mbar_init(empty(s), 1);
+        for (int s = 0; s < STAGES; ++s) ptx::mbar_init(full(s), 33), ptx::mbar_init(empty(s), 1);
         for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 4);
-        for (int s = 0; s < SCN; ++s) ptx::mbar_init(sc_full(s), 32), ptx::mbar_init(sc_empty(s), 4);
         ptx::mbar_init(inbox_bar, 1);
         ptx::mbar_init(final_bar, 1);
         *abort_flag = 0u;
@@ -96,7 +100,11 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     ptx::tc_fence_after();
     if (S > 1) ptx::cluster_arrive_relaxed();
     const uint32_t tmem = *tmem_slot;
-    // every input may come from the kernel before this one
+    // every input may come from the kernel before this one; the first weights are on their way to L2 meanwhile
+    if (warp == 4 && lane < min(n_kb, STAGES)) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) ptx::tma_prefetch_3d(&p.tmap_w, (kb0 + lane) * 128, nt * 128, h);
+    }
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
 
@@ -110,30 +118,41 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     for (int i = 0; i < H * BN; ++i) acc[i] = 0.f;
 
     if (warp == 4) {
-        // ------------------------------------------------------------ copies
-        if (lane == 0) {
-            const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
-            const uint64_t pol_a = ptx::policy_evict_last();
-            const uint32_t bytes = (uint32_t)(H * C::W_TILE + p.box_m * 128);
-            int i = 0, s = 0;
-            uint32_t ph = 0;
-            for (; i < n_kb && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
+        // ------------------------------------------------------------ copies and scales
+        const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
+        const uint64_t pol_a = ptx::policy_evict_last();
+        const uint32_t bytes = (uint32_t)(H * C::W_TILE + p.box_m * 128);
+        const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
+        const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
+        const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
+        int i = 0, s = 0;
+        uint32_t ph = 0;
+        for (; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
+            if (lane == 0) {
                 const uint32_t dst = sbase + s * C::STAGE;
                 ptx::mbar_arrive_expect_tx(full(s), bytes);
 #pragma unroll
                 for (int h = 0; h < H; ++h)
                     ptx::tma_load_3d(dst + h * C::W_TILE, &p.tmap_w, (kb0 + i) * 128, nt * 128, h, full(s), pol_w);
                 ptx::tma_load_2d(dst + H * C::W_TILE, &p.tmap_a, (kb0 + i) * 128, (int)m0, full(s), pol_a);
-                if (++s == STAGES) s = 0, ph ^= 1u;
             }
-            // every stage released: the commits that arrive here have all landed
-            for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
-                if (++s == STAGES) s = 0, ph ^= 1u;
-            if (!ok)   // copies in flight land before the block ends
-                for (int j = max(0, i - STAGES); j < i; ++j)
-                    if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
-                        atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+            __syncwarp();
+            const uint32_t sc = sbase + C::OFF_SC + i % SCN * C::SC_SLOT;
+#pragma unroll
+            for (int c = lane; c < BN; c += 32) ptx::cp_async4(sc + 4 * c, sa + (c < cols ? c : 0), c < cols);
+            if (lane < H) ptx::cp_async4(sc + 4 * (BN + lane), sw + i, true);
+            ptx::cp_async_arrive(full(s));
+            sa += p.M;
+            if (++s == STAGES) s = 0, ph ^= 1u;
         }
+        // every stage released: the commits that arrive here have all landed
+        for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
+            if (++s == STAGES) s = 0, ph ^= 1u;
+        if (!ok && lane == 0)   // copies in flight land before the block ends
+            for (int j = max(0, i - STAGES); j < i; ++j)
+                if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
+                    atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+        ptx::cp_async_wait_all();
         __syncwarp();
     } else if (warp == 5) {
         // ------------------------------------------------------------ products
@@ -165,40 +184,23 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
-        // ------------------------------------------------------------ scales
-        const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
-        const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
-        const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
-        for (int i = 0; i < n_kb; ++i) {
-            const int s = i % SCN;
-            if (!__all_sync(0xffffffffu, wait(sc_empty(s), ((uint32_t)(i / SCN) & 1u) ^ 1u, DEVICE_TIMEOUT_PRODUCER))) break;
-            const uint32_t dst = sbase + C::OFF_SC + s * C::SC_SLOT;
-#pragma unroll
-            for (int c = lane; c < BN; c += 32) ptx::cp_async4(dst + 4 * c, sa + (c < cols ? c : 0), c < cols);
-            if (lane < H) ptx::cp_async4(dst + 4 * (BN + lane), sw + i, true);
-            ptx::cp_async_arrive(sc_full(s));
-            sa += p.M;
-        }
-        ptx::cp_async_wait_all();
     } else {
         // ------------------------------------------------------------ sums
-        constexpr int CH = BN * H >= 32 ? 32 : 16, NC = BN * H / CH;
+        constexpr int CH = BN * H >= 256 || BN * H == 16 ? 16 : 32, NC = BN * H / CH;
         const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
         for (int i = 0; i < n_kb; ++i) {
-            const int b = i & 1, s = i % SCN;
-            wait(sc_full(s), (uint32_t)(i / SCN) & 1u, DEVICE_TIMEOUT_TRANSFORM);
+            const int b = i & 1;
             if (!__all_sync(0xffffffffu, wait(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
             ptx::tc_fence_after();
-            const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + s * C::SC_SLOT);
-            uint64_t sw[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) sw[h] = f2(sc[BN + h], sc[BN + h]);
             uint32_t v[2][CH];
             auto load = [&](int c) {
                 if constexpr (CH == 32) ptx::tmem_ld32(base + b * H * BN + c * CH, v[c & 1]);
                 else ptx::tmem_ld16(base + b * H * BN + c * CH, v[c & 1]);
             };
+            const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + i % SCN * C::SC_SLOT);
+            uint64_t sw[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) sw[h] = f2(sc[BN + h], sc[BN + h]);
             load(0);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
@@ -221,8 +223,6 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
                     acc[col] = r01.x, acc[col + 1] = r01.y, acc[col + 2] = r23.x, acc[col + 3] = r23.y;
                 }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sc_empty(s));
         }
     }
     // From here on every thread runs the same sequence (no early exit before the barriers).
@@ -231,90 +231,104 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     ptx::tc_fence_after();
     if (warp == 5) ptx::tmem_dealloc<1>(tmem, C::TMEM_COLS);
     if (S > 1) ptx::cluster_wait();   // every block of the cluster has initialised its barriers
-    if (warp >= 4) return;
-    ok = *abort_flag == 0u;
-    const int row = threadIdx.x;      // of the tile
-    if (C::SMAX > 1 && S > 1) {
-        if (ok) {
-#pragma unroll
-            for (int j = 0; j < BN / 4; ++j) {
-                if (j < groups) {
-                    const int owner = j / per;
-                    const uint32_t bar = ptx::mapa_shared(inbox_bar, (uint32_t)owner);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        const uint32_t at = sbase + C::OFF_INBOX + (uint32_t)(((rank * H + h) * 128 + row) * per + j - owner * per) * 16u;
-                        const float* a = acc + h * BN + 4 * j;
-                        ptx::st_async_v4f32(ptx::mapa_shared(at, (uint32_t)owner), a[0], a[1], a[2], a[3], bar);
-                    }
-                }
-            }
-        }
-        if (own == 0) return;
-        ok = ok && bounded_wait<true>(inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
-#pragma unroll
-        for (int j = 0; j < BN / 4; ++j) {
-            if (j < own && ok) {
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int q = 0; q < S; ++q) {
-                        const float4 u = *reinterpret_cast<const float4*>(
-                            smem + C::OFF_INBOX + (((q * H + h) * 128 + row) * per + j) * 16);
-                        t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
-                    }
-                    float* a = acc + h * BN + 4 * j;
-                    a[0] = t.x, a[1] = t.y, a[2] = t.z, a[3] = t.w;
-                }
-            }
-        }
-    }
-    // ---- the tokens m_first .. of this block, all rows of the tile
-    const int64_t m_first = m0 + 4 * g0;
-    const int mine = (int)min((int64_t)(4 * own), p.M - m_first);
-    const int64_t n = (int64_t)nt * 128 + row;
-    if (GATED) {
-#pragma unroll
-        for (int c = 0; c < BN; ++c) acc[c] = silu(acc[c]) * acc[(H - 1) * BN + c];
-    }
-    if (p.out != nullptr) {
-        if (ok && n < p.N) {
-            const float bias = !GATED && p.bias != nullptr
-                                   ? (p.out_bf16 ? load_16bit<true>(p.bias, (size_t)n) : load_16bit<false>(p.bias, (size_t)n))
-                                   : 0.f;
-            uint16_t* out = static_cast<uint16_t*>(p.out) + m_first * p.N + n;
-#pragma unroll
-            for (int c = 0; c < BN; ++c)
-                if (c < mine) out[c * p.N] = p.out_bf16 ? to_16bit<true>(acc[c] + bias) : to_16bit<false>(acc[c] + bias);
-        }
+    if (C::ALIAS && S > 1) ptx::cluster_sync();   // and has read its stages
+    if (warp >= 4) {
+        if (S > 1) ptx::cluster_arrive_relaxed(), ptx::cluster_wait();   // (the barrier behind the exchange)
         return;
     }
-    if constexpr (GATED) {
-        float* most = reinterpret_cast<float*>(smem + C::OFF_MOST);
+    ok = *abort_flag == 0u;
+    const int row = threadIdx.x;      // of the tile
+    // From here on sums lie in shared memory, [part][half][group of columns][row], and are worked on in small loops:
+    // code that runs once is bound by its own fetching (128 x 4096 x 4096: 38000 cycles unrolled over the columns in
+    // registers, four times those of the loop over K).
 #pragma unroll
-        for (int c = 0; c < BN; ++c) {
-            if (c < mine) {
-                const float m = warp_most(n < p.N ? acc[c] : 0.f);
-                if (lane == 0) most[warp * BN + c] = m;
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < BN / 4; ++j)
+            *reinterpret_cast<float4*>(smem + ((h * (BN / 4) + j) * 128 + row) * 16) =
+                make_float4(acc[h * BN + 4 * j], acc[h * BN + 4 * j + 1], acc[h * BN + 4 * j + 2], acc[h * BN + 4 * j + 3]);
+    if (S > 1) {
+        // each owner's groups of columns are one piece for each half
+        ptx::fence_proxy_async_smem();
+        ptx::named_barrier_sync(1, 128);
+        if (ok && threadIdx.x < S) {
+            const int owner = threadIdx.x, theirs = min(per, groups - owner * per);
+            const uint32_t bar = ptx::mapa_shared(inbox_bar, (uint32_t)owner);
+            if (theirs > 0)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+                    ptx::bulk_send(ptx::mapa_shared(sbase + C::OFF_INBOX + (uint32_t)((rank * H + h) * per * 2048), (uint32_t)owner),
+                                   sbase + (uint32_t)((h * (BN / 4) + owner * per) * 2048), (uint32_t)(theirs * 2048), bar);
+        }
+        __syncwarp();
+        if (own > 0) {
+            ok = ok && bounded_wait<true>(inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
+            __syncwarp();
+        }
+        // Nobody leaves before all have what was sent to them: what they sent has then been read.
+        ptx::cluster_arrive_relaxed();
+    }
+    // ---- the tokens m_first .. of this block, all rows of the tile
+    const int64_t m_first = m0 + 4 * g0, n = (int64_t)nt * 128 + row;
+    const int mine = (int)min((int64_t)(4 * own), p.M - m_first);
+    uint8_t* parts = smem + (S > 1 ? C::OFF_INBOX : 0) + row * 16;
+    float* most = reinterpret_cast<float*>(smem + C::OFF_MOST);
+    const bool codes = GATED && p.out == nullptr;
+    const float bias = !GATED && p.bias != nullptr && n < p.N
+                           ? (p.out_bf16 ? load_16bit<true>(p.bias, (size_t)n) : load_16bit<false>(p.bias, (size_t)n))
+                           : 0.f;
+#pragma unroll 1
+    for (int j = 0; j < own && ok; ++j) {
+        float4 t[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) t[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int q = 0; q < S; ++q)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float4 u = *reinterpret_cast<const float4*>(parts + ((q * H + h) * per + j) * 2048);
+                t[h].x += u.x, t[h].y += u.y, t[h].z += u.z, t[h].w += u.w;
+            }
+        float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
+        if constexpr (GATED) {
+            v[0] = silu(v[0]) * t[1].x, v[1] = silu(v[1]) * t[1].y, v[2] = silu(v[2]) * t[1].z, v[3] = silu(v[3]) * t[1].w;
+        }
+        if (codes) {
+            *reinterpret_cast<float4*>(parts + j * 2048) = make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float m = warp_most(n < p.N ? v[e] : 0.f);
+                if (lane == 0) most[warp * BN + 4 * j + e] = m;
+            }
+        } else if (n < p.N) {
+            uint16_t* out = static_cast<uint16_t*>(p.out) + (m_first + 4 * j) * p.N + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * j + e < mine)
+                    out[e * p.N] = p.out_bf16 ? to_16bit<true>(v[e] + bias) : to_16bit<false>(v[e] + bias);
+        }
+    }
+    if (codes) {
+        ptx::named_barrier_sync(1, 128);
+#pragma unroll 1
+        for (int j = 0; j < own && ok; ++j) {
+            const float4 t = *reinterpret_cast<const float4*>(parts + j * 2048);
+            const float v[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 4 * j + e;
+                if (c < mine) {
+                    const BlockScale q(max_nan(max_nan(most[c], most[BN + c]), max_nan(most[2 * BN + c], most[3 * BN + c])));
+                    if (n < p.N)
+                        p.codes[(m_first + c) * p.N + n] = q.inv == 0.f ? 0 : (uint8_t)to_e4m3x4(v[e] * q.inv, 0.f, 0.f, 0.f);
+                    if (row == 0) p.scales[(int64_t)nt * p.M + m_first + c] = q.scale;
+                }
             }
         }
-        ptx::named_barrier_sync(1, 128);
-        // codes [token][row] through the (free) stages, so that a token's 128 leave together
-        uint8_t* stage = smem;
-#pragma unroll
-        for (int c = 0; c < BN; ++c) {
-            if (c < mine) {
-                const BlockScale q(max_nan(max_nan(most[c], most[BN + c]), max_nan(most[2 * BN + c], most[3 * BN + c])));
-                stage[c * 128 + row] = q.inv == 0.f ? 0 : (uint8_t)to_e4m3x4(acc[c] * q.inv, 0.f, 0.f, 0.f);
-                if (row == 0 && ok) p.scales[(int64_t)nt * p.M + m_first + c] = q.scale;
-            }
-        }
-        ptx::named_barrier_sync(1, 128);
-        for (int e = row; e < mine * 8 && ok; e += 128) {
-            const int64_t at = (int64_t)nt * 128 + 16 * (e & 7);
-            if (at < p.N)
-                *reinterpret_cast<uint4*>(p.codes + (m_first + (e >> 3)) * p.N + at) = *reinterpret_cast<const uint4*>(stage + 16 * e);
-        }
+    }
+    if (S > 1) {
+        __syncwarp();
+        ptx::cluster_wait();
     }
 }
 
