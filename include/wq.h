@@ -460,7 +460,7 @@ wq_status wq_quantize_fp8(const void* x, int64_t x_stride, wq_dtype dtype, int64
  * A NaN among a token's codes or scales makes that token's outputs NaN, one of a weight row that
  * row's column.  Results do not change from run to run.
  * Requirements: M >= 0, N >= 8, N % 8 == 0, N <= 2^29, 16 <= K <= 2^30, K % 16 == 0, N * K < 2^40,
- * tiles of 16 tokens x 128 rows below 2^28; a, w and out
+ * M / 256 * N / 128 (each rounded up) < 2^30; a, w and out
  * 16-byte aligned, the scales 4-byte, bias 2-byte. */
 wq_status wq_gemm_w8a8_fp8(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
                            const void* bias, int64_t M, int64_t N, int64_t K, wq_dtype dtype, void* out,

@@ -57,7 +57,7 @@ def test_product_refusals(L):
     for kw in (dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(out=None)):
         assert f(**kw) == NULL
     for kw in (dict(M=-1), dict(M=1 << 31), dict(N=0), dict(N=4), dict(N=260), dict(N=(1 << 29) + 8), dict(K=0), dict(K=8),
-               dict(K=264), dict(K=(1 << 30) + 16)):
+               dict(K=264), dict(K=(1 << 30) + 16), dict(N=1 << 20, K=1 << 20), dict(M=1 << 30, N=1 << 16)):
         assert f(**kw) == SHAPE, kw
     assert f(dt=2) == DTYPE
     for kw in (dict(a=P + 8), dict(w=P + 8), dict(out=P + 8), dict(sa=P + 2), dict(sw=P + 1), dict(bias=P + 1)):

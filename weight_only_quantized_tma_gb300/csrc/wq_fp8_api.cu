@@ -64,7 +64,7 @@ wq_status product_call(const uint8_t* a, const float* a_scale, const uint8_t* w,
     const int64_t step = gated ? 16 : 8;
     // (weight rows and k are coordinates of 32-bit tensor maps)
     if (M < 0 || M > kMaxTokens || N < step || N % step != 0 || N > (1LL << 29) || K < 16 || K % 16 != 0 ||
-        K > (1LL << 30) || N * K >= (1LL << 40))
+        K > (1LL << 30) || N * K >= (1LL << 40) || (M + 255) / 256 * ((N + 127) / 128) >= (1LL << 30))
         return WQ_ERR_SHAPE;
     if ((out || !gated) && !type_ok(dtype)) return WQ_ERR_DTYPE;
     if (M == 0) return WQ_OK;

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "wq_w8a8_mid.cuh"
 #include "wq_w8a8_narrow.cuh"
 #include "wq_w8a8_wide.cuh"
 
@@ -12,11 +13,12 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSplits = 8;
 
-// One instantiation: its attributes, and how many clusters of S blocks the device holds at once (asked once for
-// each device).
-template <typename C>
-struct Narrow {
-    static constexpr auto kernel = w8a8_narrow_kernel<C>;
+// One instantiation of the kernels with one tile for each cluster of `splits` blocks: its attributes, and how many
+// clusters of S blocks the device holds at once (asked once for each device).  TM tokens x 128 weight rows (of each
+// half) a tile, BOX_W weight rows a copy.
+template <typename C, void (*KERNEL)(W8A8Params), int TM, int CTAS, int BOX_W>
+struct Split {
+    static constexpr auto kernel = KERNEL;
     struct Device {
         std::once_flag once;
         cudaError_t err = cudaSuccess;
@@ -30,17 +32,17 @@ struct Narrow {
         std::call_once(d.once, [&]() {
             d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
             if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-            // The query counts one block of a kernel with tensor memory for each SM; C::CTAS are resident (304 blocks of
+            // The query counts one block of a kernel with tensor memory for each SM; CTAS are resident (304 blocks of
             // CTAS = 2 ran at once on 152 SMs, in clusters of two as well, 296 in clusters of four), and what the query
             // leaves over in each part of the GPU then holds clusters too.
-            d.clusters[1] = C::CTAS * sms;
+            d.clusters[1] = CTAS * sms;
             for (int S = 2; S <= C::SMAX && d.err == cudaSuccess; ++S) {
                 cudaLaunchConfig_t cfg = {};
                 cudaLaunchAttribute attr = {};
                 fill(cfg, &attr, (unsigned)S, S, nullptr);
                 int n = 0;
                 if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) (void)cudaGetLastError(), n = 0;
-                if (C::CTAS > 1) n = C::CTAS * n + std::max(0, sms - n * S) / S;
+                if (CTAS > 1) n = CTAS * n + std::max(0, sms - n * S) / S;
                 d.clusters[S] = n - (n + 31) / 32;   // (fewer are placed at once than the query reports)
             }
         });
@@ -57,29 +59,37 @@ struct Narrow {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    static cudaError_t launch(W8A8Params p, int sms, cudaStream_t st) {
+    // Slices of K that end soonest, and when, in 10 ns: the rounds of clusters times (`block` for each block of K, 2 us to
+    // start and end), and 1 us for the exchange.  0 slices: the device cannot be asked.
+    struct Plan {
+        int splits;
+        int64_t cost;
+    };
+    static Plan plan(const W8A8Params& p, int sms, int block) {
         const Device* d = device(sms);
-        if (!d) return cudaErrorInvalidDevice;
-        const int64_t tiles_m = (p.M + C::BN - 1) / C::BN, tiles_n = (p.N + 127) / 128, tiles = tiles_m * tiles_n;
-        if (tiles * kMaxSplits >= (1LL << 31)) return cudaErrorInvalidValue;
-        // Slices of K: the rounds of clusters times (blocks of a slice, and 4 blocks' time to start and end),
-        // and 2 blocks' time for the exchange.
-        int S = 1;
-        int64_t best = 0;
+        Plan best{0, 0};
+        if (!d) return best;
+        const int64_t tiles = (p.M + TM - 1) / TM * ((p.N + 127) / 128);
         for (int s = 1; s <= C::SMAX && (s == 1 || p.kblocks >= 2 * s); ++s) {
             if (d->clusters[s] < 1) continue;
             const int64_t rounds = (tiles + d->clusters[s] - 1) / d->clusters[s];
-            const int64_t cost = rounds * ((p.kblocks + s - 1) / s + 4) + (s > 1 ? 2 : 0);
-            if (s == 1 || cost < best) S = s, best = cost;
+            const int64_t cost = rounds * ((p.kblocks + s - 1) / s * block + 200) + (s > 1 ? 100 : 0);
+            if (s == 1 || cost < best.cost) best = Plan{s, cost};
         }
+        return best;
+    }
+    static cudaError_t launch(W8A8Params p, int S, cudaStream_t st) {
+        if (S < 1) return cudaErrorInvalidDevice;
+        const int64_t tiles_m = (p.M + TM - 1) / TM, tiles_n = (p.N + 127) / 128, tiles = tiles_m * tiles_n;
+        if (tiles * kMaxSplits >= (1LL << 31)) return cudaErrorInvalidValue;
         p.tiles_m = (int)tiles_m;
         p.tiles_n = (int)tiles_n;
         p.splits = S;
-        p.box_m = (int)std::min<int64_t>(C::BN, p.M);
+        p.box_m = (int)std::min<int64_t>(TM, p.M);
         const uint64_t a_dims[2] = {(uint64_t)p.K, (uint64_t)p.M}, a_strides[1] = {(uint64_t)p.K};
         const uint64_t w_dims[3] = {(uint64_t)p.K, (uint64_t)p.N, (uint64_t)C::H};
         const uint64_t w_strides[2] = {(uint64_t)p.K, (uint64_t)p.K * p.N};
-        const uint32_t a_box[2] = {128, (uint32_t)p.box_m}, w_box[3] = {128, 128, 1};
+        const uint32_t a_box[2] = {128, (uint32_t)p.box_m}, w_box[3] = {128, BOX_W, 1};
         if (!encode_tensor_map(&p.tmap_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.a, 2, a_dims, a_strides, a_box,
                                CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode_tensor_map(&p.tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w, 3, w_dims, w_strides, w_box,
@@ -95,6 +105,11 @@ struct Narrow {
         return cudaLaunchKernelEx(&cfg, kernel, p);
     }
 };
+
+template <typename C>
+using Narrow = Split<C, w8a8_narrow_kernel<C>, C::BN, C::CTAS, 128>;
+template <bool GATED>
+using Mid = Split<MidCfg<GATED>, w8a8_mid_kernel<MidCfg<GATED>>, 128, 1, 64>;
 
 // Pairs of blocks over tiles of 256 tokens x 256 weight rows.
 template <bool GATED>
@@ -131,6 +146,13 @@ struct Wide {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
+    // as Split's
+    static int64_t cost(const W8A8Params& p, int block) {
+        const Device* d = device();
+        if (!d) return INT64_MAX;
+        const int64_t tiles = (p.M + 255) / 256 * ((p.N + C::TILE_N - 1) / C::TILE_N);
+        return (tiles + d->pairs - 1) / d->pairs * ((int64_t)p.kblocks * block + 200);
+    }
     static cudaError_t launch(W8A8Params p, cudaStream_t st) {
         const Device* d = device();
         if (!d) return cudaErrorInvalidDevice;
@@ -165,19 +187,38 @@ struct Wide {
     }
 };
 
+// Up to 32 tokens weight rows are the tensor cores' M dimension: nothing of a tile is unused but what 16 or 32 exceed
+// the tokens by, and two blocks are resident on each SM.  From there on tokens are, in tiles of a block's own or of a
+// pair's, by which of them ends first.  What a block of K takes is measured (10 ns): 38 in a tile of a block's own
+// (63 gated), 43 (48) in a pair's, which is four times as large (gated twice).  Both measured, in us:
+//   tokens x rows x K           own   pair      tokens x rows x K, gated    own   pair
+//   333 x 4096 x 4096          17.1   19.0      400 x 4096 x 4096          26.6   21.1
+//   512 x 4096 x 4096          17.6   19.0      512 x 6928 x 2560          40.6   26.2
+//   768 x 4096 x 4096          39.9   19.6      777 x 6928 x 2560          60.8   37.5
+//   512 x 12288 x 4096         52.2   35.0
+// (and with weight rows as M in tiles of 64 or 128 tokens: 64 x 4096 x 4096 10.3 against 9.2 of its own, 128 x 4096 x
+// 4096 14.2 against 10.6, 250 x 4096 x 4096 18.8 against 13.6; gated 64 x 11008 x 4096 38.6 against 24.7).
+template <bool GATED>
+cudaError_t launch_many(const W8A8Params& p, int sms, cudaStream_t st) {
+    const typename Mid<GATED>::Plan own = Mid<GATED>::plan(p, sms, GATED ? 63 : 38);
+    if (Wide<GATED>::cost(p, GATED ? 48 : 43) < own.cost) return Wide<GATED>::launch(p, st);
+    return Mid<GATED>::launch(p, own.splits, st);
+}
+template <typename K>
+cudaError_t launch_few(const W8A8Params& p, int sms, cudaStream_t st) {
+    return K::launch(p, K::plan(p, sms, 50).splits, st);
+}
+
 }  // namespace
 
 cudaError_t launch_w8a8(const W8A8Params& p, int sms, cudaStream_t st) {
-    if (p.M >= 256) return p.gated ? Wide<true>::launch(p, st) : Wide<false>::launch(p, st);
+    if (p.M > 32) return p.gated ? launch_many<true>(p, sms, st) : launch_many<false>(p, sms, st);
     if (p.gated) {
-        if (p.M <= 16) return Narrow<NarrowCfg<16, true, 3, 8, 2, true>>::launch(p, sms, st);
-        if (p.M <= 32) return Narrow<NarrowCfg<32, true, 3, 8, 2, true>>::launch(p, sms, st);
-        return Narrow<NarrowCfg<64, true, 4, 8, 1, true>>::launch(p, sms, st);
+        if (p.M <= 16) return launch_few<Narrow<NarrowCfg<16, true, 3, 8, 2, true>>>(p, sms, st);
+        return launch_few<Narrow<NarrowCfg<32, true, 3, 8, 2, true>>>(p, sms, st);
     }
-    if (p.M <= 16) return Narrow<NarrowCfg<16, false, 4, 8, 2, false>>::launch(p, sms, st);
-    if (p.M <= 32) return Narrow<NarrowCfg<32, false, 5, 8, 2, true>>::launch(p, sms, st);
-    if (p.M <= 64) return Narrow<NarrowCfg<64, false, 4, 8, 2, true>>::launch(p, sms, st);
-    return Narrow<NarrowCfg<128, false, 6, 8, 1, true>>::launch(p, sms, st);
+    if (p.M <= 16) return launch_few<Narrow<NarrowCfg<16, false, 4, 8, 2, false>>>(p, sms, st);
+    return launch_few<Narrow<NarrowCfg<32, false, 5, 8, 2, true>>>(p, sms, st);
 }
 
 }  // namespace wq
