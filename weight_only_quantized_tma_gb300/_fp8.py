@@ -11,26 +11,40 @@ import torch
 from ._attn import _DTYPES, _call, _flat, _stream
 
 _E4M3 = torch.float8_e4m3fn
+_F32 = torch.float32
+_empty, _empty_like, _Tensor = torch.empty, torch.empty_like, torch.Tensor
 
 
-def _rows(t, name, dtype=None, shape=None, device=None):
-    """A [T, H] tensor whose rows are contiguous (any stride from row to row); the elements from row to row."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    got = t.shape
-    if len(got) != 2:
-        raise ValueError(f"{name} must be [tokens, values], got {tuple(got)}")
-    if dtype is not None and t.dtype is not dtype:
+# A decode step's calls are bound by the host, so a tensor's common form is tested in one expression and told apart
+# only where that fails (a call of wq_add_rms_norm that makes its outputs: 13.6 us with a check for each property).
+
+def _step(t, name, dtype, shape, device):
+    """The elements from row to row of a [T, H] tensor (any stride) of this type, shape and device."""
+    if not isinstance(t, _Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if shape is not None and got != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(got)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    n, h = got
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]
     step, one = t.stride()
-    if h > 1 and one != 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return step if n > 1 else h
+    return step if shape[0] > 1 else shape[1]
+
+
+def _rows(x):
+    """(elements from row to row, shape, type, its code, device) of 16-bit activations x [T, H]."""
+    if not isinstance(x, _Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if len(shape) != 2:
+        raise ValueError(f"x must be [tokens, values], got {tuple(shape)}")
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"16-bit values must be float16 or bfloat16, got {dtype}")
+    return shape[1] if x.is_contiguous() else _step(x, "x", dtype, shape, dev), shape, dtype, code, dev
 
 
 def _type(dtype) -> int:
@@ -42,46 +56,44 @@ def _type(dtype) -> int:
 
 def _codes(t, name, device=None):
     """A contiguous e4m3 matrix (float8_e4m3fn, or its bytes as uint8)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or (device is not None and t.device != device):
+    if not isinstance(t, _Tensor) or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a tensor on {device if device is not None else 'a CUDA device'}")
     if t.dtype is not _E4M3 and t.dtype is not torch.uint8:
         raise ValueError(f"{name} must have dtype float8_e4m3fn or uint8, got {t.dtype}")
-    if t.dim() != 2 or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous matrix")
-    return t.shape
+    return shape
 
 
 def _pair(codes, scales, T, K, device):
     """The two outputs of 8-bit activations, made where none are given."""
     blocks = -(-K // 128)
     if codes is None:
-        codes = torch.empty((T, K), dtype=_E4M3, device=device)
+        codes = _empty((T, K), dtype=_E4M3, device=device)
     elif _codes(codes, "codes", device) != (T, K):
         raise ValueError(f"codes must have shape {(T, K)}, got {tuple(codes.shape)}")
     if scales is None:
-        scales = torch.empty((blocks, T), dtype=torch.float32, device=device)
+        scales = _empty((blocks, T), dtype=_F32, device=device)
     else:
-        _flat(scales, "scales", torch.float32, (blocks, T), device)
+        _flat(scales, "scales", _F32, (blocks, T), device)
     return codes, scales
 
 
 # ------------------------------------------------------------------ norm, quantiser
 
-def _norm_inputs(x, weight, residual, sum_out):
-    x_step = _rows(x, "x")
-    dtype, dev = x.dtype, x.device
-    code = _type(dtype)
-    _flat(weight, "weight", dtype, (x.shape[1],), dev)
+def _sum_of(residual, sum_out, x, shape, dtype, dev):
+    """(residual's pointer, its step, the sum, the sum's pointer, its step)."""
     if residual is None:
         if sum_out is not None:
             raise ValueError("sum_out without a residual: there is no sum")
-        return x_step, code, dev, None, 0, None, 0
-    r_step = _rows(residual, "residual", dtype, x.shape, dev)
+        return None, 0, None, None, 0
+    step = _step(residual, "residual", dtype, shape, dev)
     if sum_out is None:
-        sum_out, s_step = torch.empty(x.shape, dtype=dtype, device=dev), x.shape[1]
-    else:
-        s_step = _rows(sum_out, "sum_out", dtype, x.shape, dev)
-    return x_step, code, dev, residual.data_ptr(), r_step, sum_out, s_step
+        sum_out = _empty_like(x) if x.is_contiguous() else _empty(shape, dtype=dtype, device=dev)
+        return residual.data_ptr(), step, sum_out, sum_out.data_ptr(), shape[1]
+    s_step = _step(sum_out, "sum_out", dtype, shape, dev)
+    return residual.data_ptr(), step, sum_out, sum_out.data_ptr(), s_step
 
 
 def wq_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None, eps: float = 1e-6,
@@ -90,34 +102,35 @@ def wq_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tenso
 
     out = s * rsqrt(mean(s^2) + eps) * weight of the fp32 sum s; sum is s rounded, the new residual.  sum_out may
     be residual (or x), out may be x (or residual): in place."""
-    x_step, code, dev, r, r_step, total, s_step = _norm_inputs(x, weight, residual, sum_out)
-    T, H = x.shape
+    x_step, shape, dtype, code, dev = _rows(x)
+    T, H = shape
+    _flat(weight, "weight", dtype, (H,), dev)
+    r, r_step, total, s, s_step = _sum_of(residual, sum_out, x, shape, dtype, dev)
     if out is None:
-        out, o_step = torch.empty(x.shape, dtype=x.dtype, device=dev), H
+        out, o_step = _empty_like(x) if x_step == H else _empty(shape, dtype=dtype, device=dev), H
     else:
-        o_step = _rows(out, "out", x.dtype, x.shape, dev)
-    _call("wq_add_rms_norm", dev, x.data_ptr(), x_step, r, r_step, code, T, H, weight.data_ptr(), eps,
-          None if total is None else total.data_ptr(), s_step, out.data_ptr(), o_step, _stream(dev))
+        o_step = _step(out, "out", dtype, shape, dev)
+    _call("wq_add_rms_norm", dev, x.data_ptr(), x_step, r, r_step, code, T, H, weight.data_ptr(), eps, s, s_step,
+          out.data_ptr(), o_step, _stream(dev))
     return out, total
 
 
 def wq_add_rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor = None, eps: float = 1e-6,
                         sum_out: torch.Tensor = None, codes: torch.Tensor = None, scales: torch.Tensor = None):
     """wq_add_rms_norm with its output in 8 bits -> (codes, scales, sum; None without a residual)."""
-    x_step, code, dev, r, r_step, total, s_step = _norm_inputs(x, weight, residual, sum_out)
-    T, H = x.shape
+    x_step, shape, dtype, code, dev = _rows(x)
+    T, H = shape
+    _flat(weight, "weight", dtype, (H,), dev)
+    r, r_step, total, s, s_step = _sum_of(residual, sum_out, x, shape, dtype, dev)
     codes, scales = _pair(codes, scales, T, H, dev)
-    _call("wq_add_rms_norm_fp8", dev, x.data_ptr(), x_step, r, r_step, code, T, H, weight.data_ptr(), eps,
-          None if total is None else total.data_ptr(), s_step, codes.data_ptr(), scales.data_ptr(), _stream(dev))
+    _call("wq_add_rms_norm_fp8", dev, x.data_ptr(), x_step, r, r_step, code, T, H, weight.data_ptr(), eps, s, s_step,
+          codes.data_ptr(), scales.data_ptr(), _stream(dev))
     return codes, scales, total
 
 
 def wq_quantize_fp8(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None):
     """16-bit activations x [T, K] -> (codes float8_e4m3fn [T, K], scales fp32 [ceil(K / 128), T])."""
-    x_step = _rows(x, "x")
-    dev = x.device
-    T, K = x.shape
-    code = _type(x.dtype)
+    x_step, (T, K), _, code, dev = _rows(x)
     codes, scales = _pair(codes, scales, T, K, dev)
     _call("wq_quantize_fp8", dev, x.data_ptr(), x_step, code, T, K, codes.data_ptr(), scales.data_ptr(), _stream(dev))
     return codes, scales

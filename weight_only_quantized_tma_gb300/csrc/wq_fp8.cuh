@@ -6,10 +6,22 @@
 
 namespace wq {
 
+__device__ __forceinline__ float about_reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Larger of both; a NaN in either gives NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -27,14 +39,17 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
 
 // The scale of a block whose largest magnitude is `most`, and what its values are multiplied with.  An
 // infinity or a NaN in the block gives a NaN for the scale (and codes of 0): the block's values are NaN.
-// The product with the nearest reciprocal puts a value within 2^-23 of its quotient, so that only one
-// that close to the middle between two codes can become the other of them.
+// most / 448 is rounded exactly: the product with 1 / 448 and one correction by its exact residual (Markstein's method;
+// where the residual would leave the normal range the scale is the least one).  A value's product with the reciprocal
+// is within 2^-22 of its quotient, so that only one that close to the middle between two codes can become the other
+// of them.
 struct BlockScale {
     float scale, inv;
     __device__ __forceinline__ explicit BlockScale(float most) {
         const bool finite = most <= 3.402823466e38f;
-        scale = finite ? fmaxf(__fdiv_rn(most, 448.0f), 0x1p-96f) : __int_as_float(0x7FC00000);
-        inv = finite ? __frcp_rn(scale) : 0.0f;
+        const float q = most * (1.0f / 448.0f);
+        scale = finite ? fmaxf(fmaf(fmaf(-448.0f, q, most), 1.0f / 448.0f, q), 0x1p-96f) : __int_as_float(0x7FC00000);
+        inv = finite ? about_reciprocal(scale) : 0.0f;
     }
 };
 

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = (1LL << 31) - 1;
 constexpr int64_t kMaxStride = 1LL << 40;
-constexpr int64_t kMaxWidth = 32768;      // of a normed row: 1024 threads x 32 values
+constexpr int64_t kMaxWidth = 32768;      // of a normed row: 512 threads x 64 values
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 wq_status finish_launch(cudaError_t e) { return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA; }

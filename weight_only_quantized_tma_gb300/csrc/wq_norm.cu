@@ -10,29 +10,41 @@
 namespace wq {
 namespace {
 
+// Eight 16-bit values as four pairs of fp32 (one instruction then works on two), and back.
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&x)[4]) {
     const float2 a = unpack2<BF16>(r.x), b = unpack2<BF16>(r.y), c = unpack2<BF16>(r.z), d = unpack2<BF16>(r.w);
-    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y, x[4] = c.x, x[5] = c.y, x[6] = d.x, x[7] = d.y;
+    x[0] = f2(a.x, a.y), x[1] = f2(b.x, b.y), x[2] = f2(c.x, c.y), x[3] = f2(d.x, d.y);
 }
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
+    const float2 a = un2(x[0]), b = un2(x[1]), c = un2(x[2]), d = un2(x[3]);
+    return make_uint4(pack2<BF16>(a.x, a.y), pack2<BF16>(b.x, b.y), pack2<BF16>(c.x, c.y), pack2<BF16>(d.x, d.y));
+}
+
+// 16 bytes that are used once: they take no place in L1 from the weight, which every row of an SM reads.
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
 }
 
 // The largest magnitude of 8 values of each of 16 neighbouring lanes (a block of 128).
-__device__ __forceinline__ float block_most(const float (&y)[8]) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
+__device__ __forceinline__ float block_most(const uint64_t (&y)[4]) {
+    const float2 a = un2(y[0]), b = un2(y[1]), c = un2(y[2]), d = un2(y[3]);
+    float m = max_nan(fabsf(a.x), fabsf(a.y), fabsf(b.x));
+    m = max_nan(m, fabsf(b.y), fabsf(c.x));
+    m = max_nan(m, fabsf(c.y), fabsf(d.x));
+    m = max_nan(m, fabsf(d.y));
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
     return m;
 }
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+__device__ __forceinline__ uint2 codes8(const uint64_t (&y)[4], float inv) {
     if (inv == 0.f) return make_uint2(0u, 0u);   // (a NaN times 0 would be one)
-    return make_uint2(to_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                      to_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+    const uint64_t by = f2(inv, inv);
+    const float2 a = un2(mul_f2(y[0], by)), b = un2(mul_f2(y[1], by)), c = un2(mul_f2(y[2], by)), d = un2(mul_f2(y[3], by));
+    return make_uint2(to_e4m3x4(a.x, a.y, b.x, b.y), to_e4m3x4(c.x, c.y, d.x, d.y));
 }
 
 // rsqrt(mean + eps) from a sum of squares; `again(f)` gives the sum of (f s)^2 where the plain one has
@@ -47,10 +59,13 @@ __device__ __forceinline__ float inverse_rms(float sum, float inv_h, float eps, 
 
 // One row for each group of `blockDim.x` threads (blockDim.y rows in a block; more than one only where a
 // row is one warp).  Thread i holds values 8 (i + c blockDim.x) .. + 7 of chunk c < C, so 16 neighbouring
-// lanes hold one block of 128.
+// lanes hold one block of 128.  Bound by memory from some 100 rows on, as far as rows are on their way: hence the
+// bounds on registers, which keep 1200 to 2000 threads on an SM (4000 x 11008 to 8 bits 41 -> 33 us), and the weight
+// read late.  8192 x 4096 with a residual: 42.6 us (6.3 TB/s), to 8 bits 42 (5.6 TB/s; issue slots 56 % full).  Tried:
+// blocks that stay, rows arriving by bulk copies (43 to 46 us), the next row loaded into registers early (43 to 44).
 template <bool BF16, int C, bool ADD, bool QUANT>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
-    __shared__ float part[2][32];
+__global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 2 : 3) : C == 2 ? (ADD ? 3 : 4) : 4) norm_kernel(const NormParams p) {
+    __shared__ float part[2][16];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
@@ -58,32 +73,42 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
     const bool row = t < p.T;
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + t * p.x_stride;
     const uint16_t* r = static_cast<const uint16_t*>(p.residual) + t * p.r_stride;
-    float s[C][8];
-    uint4 xr[C], rr[C], wr[C];
+    // With a residual the fp32 sums are kept for the output, without one the 16-bit row is (half the registers, so
+    // more rows are on their way in an SM).
+    uint64_t s[C][4];
+    uint4 xr[C], rr[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = 8 * (int)(threadIdx.x + c * blockDim.x);
         const bool in = row && at < p.H;
-        xr[c] = in ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0, 0, 0, 0);
-        if (ADD) rr[c] = in ? *reinterpret_cast<const uint4*>(r + at) : make_uint4(0, 0, 0, 0);
-        wr[c] = at < p.H ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at)) : make_uint4(0, 0, 0, 0);
+        xr[c] = in ? load_once(x + at) : make_uint4(0, 0, 0, 0);
+        if (ADD) rr[c] = in ? load_once(r + at) : make_uint4(0, 0, 0, 0);
     }
-    float sum = 0.f;
+    auto values = [&](int c, uint64_t (&v)[4]) {
+        if (ADD) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = s[c][i];
+        } else {
+            unpack8<BF16>(xr[c], v);
+        }
+    };
+    uint64_t squares = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+        const int at = 8 * (int)(threadIdx.x + c * blockDim.x);
         unpack8<BF16>(xr[c], s[c]);
         if (ADD) {
-            float b[8];
+            uint64_t b[4];
             unpack8<BF16>(rr[c], b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[c][i] += b[i];
-            const int at = 8 * (int)(threadIdx.x + c * blockDim.x);
+            for (int i = 0; i < 4; ++i) s[c][i] = add_f2(s[c][i], b[i]);
             if (row && at < p.H)
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.sum) + t * p.sum_stride + at) = pack8<BF16>(s[c]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += s[c][i] * s[c][i];
+        for (int i = 0; i < 4; ++i) squares = fma_f2(s[c][i], s[c][i], squares);
     }
+    const float sum = un2(squares).x + un2(squares).y;
     // the row's total, the same in each of its threads
     auto total = [&](float v, int turn) {
 #pragma unroll
@@ -96,55 +121,66 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
         return all;
     };
     const float inv = inverse_rms(total(sum, 0), p.inv_h, p.eps, [&](float f) {
-        float v = 0.f;
+        float sq = 0.f;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            uint64_t v[4];
+            values(c, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v += (f * s[c][i]) * (f * s[c][i]);
-        return total(v, 1);   // (the row's threads agree on whether they come here)
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = un2(mul_f2(v[i], f2(f, f)));
+                sq += u.x * u.x + u.y * u.y;
+            }
+        }
+        return total(sq, 1);   // (the row's threads agree on whether they come here)
     });
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = 8 * (int)(threadIdx.x + c * blockDim.x);
-        float w[8];
-        unpack8<BF16>(wr[c], w);
+        uint64_t v[4], w[4];
+        values(c, v);
+        unpack8<BF16>(at < p.H ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at)) : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[c][i] = s[c][i] * inv * w[i];
+        for (int i = 0; i < 4; ++i) v[i] = mul_f2(mul_f2(v[i], f2(inv, inv)), w[i]);
         if (QUANT) {
             // lanes past the row hold zeros (0 * inv * 0, where inv may be infinite: not those)
             if (at >= p.H) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[c][i] = 0.f;
+                for (int i = 0; i < 4; ++i) v[i] = 0;
             }
-            const BlockScale q(block_most(s[c]));
+            const BlockScale q(block_most(v));
             if (row && at < p.H) {
-                *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(s[c], q.inv);
+                *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(v, q.inv);
                 if ((lane & 15) == 0) p.scales[(int64_t)(at >> 7) * p.T + t] = q.scale;
             }
         } else if (row && at < p.H) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + at) = pack8<BF16>(s[c]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + at) = pack8<BF16>(v);
         }
     }
 }
 
-template <bool BF16, int C>
-cudaError_t launch_c(const NormParams& p, int threads, cudaStream_t st) {
-    const int rows = threads == 32 ? 4 : 1;
-    const unsigned grid = (unsigned)((p.T + rows - 1) / rows);
-    const dim3 block(threads, rows);
-    if (p.codes != nullptr)
-        return p.residual != nullptr ? launch_pdl(norm_kernel<BF16, C, true, true>, grid, block, 0, st, p)
-                                     : launch_pdl(norm_kernel<BF16, C, false, true>, grid, block, 0, st, p);
-    return p.residual != nullptr ? launch_pdl(norm_kernel<BF16, C, true, false>, grid, block, 0, st, p)
-                                 : launch_pdl(norm_kernel<BF16, C, false, false>, grid, block, 0, st, p);
+// Threads of a row, 8 C values each.
+int threads_of(int H, int C) { return (H + 256 * C - 1) / (256 * C) * 32; }
+
+template <bool BF16, int C, bool ADD, bool QUANT>
+cudaError_t launch_row_each(const NormParams& p, cudaStream_t st) {
+    const int threads = threads_of(p.H, C), rows = threads == 32 ? 4 : 1;
+    return launch_pdl(norm_kernel<BF16, C, ADD, QUANT>, (unsigned)((p.T + rows - 1) / rows), dim3(threads, rows), 0, st, p);
+}
+
+template <bool BF16, bool ADD, bool QUANT>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
+    if (p.H <= 4096) return launch_row_each<BF16, 1, ADD, QUANT>(p, st);
+    if (p.H <= 8192) return launch_row_each<BF16, 2, ADD, QUANT>(p, st);
+    if (p.H <= 16384) return launch_row_each<BF16, 4, ADD, QUANT>(p, st);
+    return launch_row_each<BF16, 8, ADD, QUANT>(p, st);   // up to 512 threads: H <= 32768
 }
 
 template <bool BF16>
 cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
-    auto threads = [&](int c) { return (int)((p.H + 256 * c - 1) / (256 * c)) * 32; };
-    if (threads(1) <= 512) return launch_c<BF16, 1>(p, threads(1), st);
-    if (threads(2) <= 512) return launch_c<BF16, 2>(p, threads(2), st);
-    return launch_c<BF16, 4>(p, threads(4), st);   // up to 1024 threads: H <= 32768
+    if (p.codes != nullptr)
+        return p.residual != nullptr ? launch_norm<BF16, true, true>(p, st) : launch_norm<BF16, false, true>(p, st);
+    return p.residual != nullptr ? launch_norm<BF16, true, false>(p, st) : launch_norm<BF16, false, false>(p, st);
 }
 
 // 16 tokens for each block of 256 threads: 16 lanes take one token's block of 128, U of them in turn whose
@@ -168,7 +204,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const NormParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int at = (kb0 + u) * 128 + 8 * lane;
-        float y[8];
+        uint64_t y[4];
         unpack8<BF16>(xr[u], y);
         const BlockScale q(block_most(y));
         if (row && at < p.H) {
