@@ -182,3 +182,25 @@ def test_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(caught, want))
+
+
+def test_outputs_over_either_input():
+    """sum over x and out over residual: every value is read before it is written, by the thread that writes it."""
+    x, r, w = _inputs(50, 4096, "f16", True)
+    want, total = wq.wq_add_rms_norm(x, w, residual=r)
+    wq.wq_add_rms_norm(x, w, residual=r, sum_out=x, out=r)
+    assert torch.equal(r, want) and torch.equal(x, total)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows are those of a call of their own."""
+    T, H, n = 530_000, 4096, 200
+    x = torch.empty(T, H, device="cuda", dtype=torch.bfloat16)
+    tail, _, w = _inputs(n, H, "bf16", False)
+    x[:-n].fill_(1.0)
+    x[-n:] = tail
+    out, _ = wq.wq_add_rms_norm(x, w)
+    assert torch.equal(out[-n:], wq.wq_add_rms_norm(tail, w)[0]) and torch.equal(out[0], out[T - n - 1])
+    del out
+    for pair, own in ((wq.wq_quantize_fp8(x), wq.wq_quantize_fp8(tail)), (wq.wq_add_rms_norm_fp8(x, w), wq.wq_add_rms_norm_fp8(tail, w))):
+        assert torch.equal(pair[0][-n:].view(torch.uint8), own[0].view(torch.uint8)) and torch.equal(pair[1][:, -n:], own[1])

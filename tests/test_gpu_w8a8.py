@@ -191,3 +191,63 @@ def test_back_to_back():
     slow = chain(torch.cuda.synchronize)
     for _ in range(20):
         assert all(torch.equal(p, q) for p, q in zip(chain(lambda: None), slow))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 outputs: the last rows are those of a call of their own."""
+    M, N, K, n = 70_000, 32_768, 128, 256    # (the own call's tokens start a tile as they do in the large one)
+    g = _gen(5)
+    w, sw = ref.random_weight(g, N, K)
+    a = torch.ones(M, K, device="cuda").to(ref.E4M3)
+    sa = torch.ones(1, M, device="cuda")
+    first = M // 256 * 256 - n
+    tail, ts = ref.random_pair(g, M - first, K)
+    a.view(torch.uint8)[first:] = tail.view(torch.uint8)
+    sa[:, first:] = ts
+    out = wq.wq_gemm_w8a8_fp8(a, sa, w, sw)
+    _check(out[first:], *ref.product(tail, ts, w, sw), "bf16")
+    assert torch.equal(out[0], out[first - 1])
+    del out
+    codes, scales = wq.wq_gemm_w8a8_fp8_gated(a, sa, torch.cat([w, w]), torch.stack([sw, sw]))
+    ref.check_pair(codes[first:].contiguous(), scales[:, first:].contiguous(), *ref.gated(tail, ts, torch.cat([w, w]), torch.stack([sw, sw])))
+
+
+@pytest.mark.parametrize("M", [3, 40, 900])
+def test_first_call_of_a_process_in_a_capture(M):
+    """What the library asks of the device once is asked outside the stream: a first call may be a captured one."""
+    import subprocess
+    import sys
+    code = f"""
+import torch, weight_only_quantized_tma_gb300 as wq
+E = torch.float8_e4m3fn
+a, w = torch.ones({M}, 256, device="cuda").to(E), torch.ones(512, 256, device="cuda").to(E)
+sa, sw = torch.ones(2, {M}, device="cuda"), torch.ones(4, 2, device="cuda")
+x = torch.ones({M}, 256, device="cuda").half()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = wq.wq_gemm_w8a8_fp8(a, sa, w, sw)
+    codes, scales = wq.wq_gemm_w8a8_fp8_gated(a, sa, w, sw.view(2, 2, 2))
+    y, _ = wq.wq_add_rms_norm(x, x[0].clone())
+    q, s = wq.wq_quantize_fp8(x)
+g.replay()
+torch.cuda.synchronize()
+assert (out == 256).all() and (codes.double() == 448).all() and (scales == 65536 / 448).all()
+assert (y == 1).all() and (q.double() == 448).all() and wq.wq_device_status() == 0
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M", [7, 48, 600])
+def test_padded_tokens_change_nothing(M):
+    """Tokens are independent: those of a batch padded with rubbish get the bits that they get alone."""
+    N, K = 512, 1024
+    a, sa, w, sw = _case(M, N, K)
+    alone = wq.wq_gemm_w8a8_fp8(a, sa, w, sw)
+    a2, sa2 = a.clone(), sa.clone()
+    a2.view(torch.uint8)[M // 2:] = 0x7F
+    sa2[:, M // 2:] = NAN
+    assert torch.equal(wq.wq_gemm_w8a8_fp8(a2, sa2, w, sw)[: M // 2], alone[: M // 2])
