@@ -60,7 +60,12 @@ __device__ __forceinline__ float warp_most(float v) {
     return r;
 }
 
-// g / (1 + exp(-g)): -0 far below (exp overflows to infinity), NaN at minus infinity (0 times it).
-__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// g / (1 + exp(-g)): -0 far below (exp overflows to infinity), NaN at minus infinity (0 times it).  The exponential and
+// the reciprocal are the special function unit's own, whose results below the normal range are zeros.
+__device__ __forceinline__ float silu(float g) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    return g * about_reciprocal(1.0f + e);
+}
 
 }  // namespace wq

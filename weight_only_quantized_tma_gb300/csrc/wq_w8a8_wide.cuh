@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 // the block's largest: this thread's 64 and those of the same row in the other warpgroup
                 float most = 0.f;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) most = max_nan(most, fabsf(acc[i]));     // (past N: products of zeros)
+                for (int i = 0; i < 64; i += 2) most = max_nan(most, fabsf(acc[i]), fabsf(acc[i + 1]));     // (past N: products of zeros)
                 const int at = C::MOST + (int)(turn & 1u) * 128 + 4 * lane;
                 *reinterpret_cast<float*>(out_s + at) = most;
                 __syncwarp();
