@@ -14,7 +14,7 @@ template <bool GATED_>
 struct MidCfg {
     static constexpr bool GATED = GATED_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 384;                    // warp 0 copies and scales, 1 products, 2 tensor memory, 4-11 sums
+    static constexpr int NTHREADS = 384;                    // warp 0 copies and scales, 1 and 3 products, 2 tensor memory, 4-11 sums
     static constexpr int SMAX = GATED ? 1 : 8;              // (both halves' sums of two slices do not fit)
     static constexpr int N = 128 * H;                       // weight rows of a tile
     static constexpr int CT = N / 2;                        // columns of a thread
@@ -28,7 +28,7 @@ struct MidCfg {
     static constexpr int OUTBOX = NG * PITCH * 16;
     static constexpr int INBOX = SMAX > 1 ? NG * (128 + 2 * SMAX) * 16 : 0;
     static constexpr int OFF_BAR = OFF_SC + SCN * SC_SLOT;
-    static constexpr int NBAR = 2 * STAGES + 4 + 2;         // full, empty, acc full / empty (2), inbox, final
+    static constexpr int NBAR = 2 * STAGES + 4 + 3;         // full, empty, acc full / empty (2), inbox, final
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TMEM_COLS = 2 * N;
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
         for (int s = 0; s < STAGES; ++s) ptx::mbar_init(full(s), 33), ptx::mbar_init(empty(s), 1);
         for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 8);
         ptx::mbar_init(inbox_bar, 1);
-        ptx::mbar_init(final_bar, 1);
+        ptx::mbar_init(final_bar, 1), ptx::mbar_init(final_bar + 8u, 1);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
         if (S > 1 && own > 0) ptx::mbar_arrive_expect_tx(inbox_bar, (uint32_t)(S * NG * own * 16));
@@ -140,13 +140,15 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
                     if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
                         atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
             ptx::cp_async_wait_all();
-        } else if (warp == 1 && lane == 0) {
+        } else if ((warp == 1 || warp == 3) && lane == 0) {
             // -------------------------------------------------------- products
+            // Two warps issue in turn, each for one buffer of sums: a block's waits, commits and loop (some 250 cycles)
+            // then lie beside the other warp's products, which the tensor cores only take as fast as they work.
             constexpr uint32_t idesc = ptx::make_idesc_e4m3(128, C::N);
-            int s = 0;
+            const int b = warp >> 1;
+            int s = b;
             uint32_t ph = 0;
-            for (int i = 0; i < n_kb; ++i) {
-                const int b = i & 1;
+            for (int i = b; i < n_kb; i += 2) {
                 if (!wait(full(s), ph, DEVICE_TIMEOUT_MMA) || !wait(acc_empty(b), ((uint32_t)(i >> 1) & 1u) ^ 1u, DEVICE_TIMEOUT_MMA))
                     break;
                 ptx::tc_fence_after();
@@ -156,11 +158,11 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
                     ptx::mma_f8_ss<1>(tmem + b * C::N, a_lo + 2 * k, ptx::kSdescHi, b_lo + 2 * k, ptx::kSdescHi, idesc, k > 0);
                 ptx::mma_commit<1>(acc_full(b));
                 ptx::mma_commit<1>(empty(s));
-                if (++s == STAGES) s = 0, ph ^= 1u;
+                if ((s += 2) >= STAGES) s -= STAGES, ph ^= 1u;
             }
             if (!ok) {
-                ptx::mma_commit<1>(final_bar);
-                if (!drain_wait(final_bar, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+                ptx::mma_commit<1>(final_bar + 8u * b);
+                if (!drain_wait(final_bar + 8u * b, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
             }
         }
         __syncwarp();

@@ -27,7 +27,7 @@ struct NarrowCfg {
     static constexpr int BN = BN_, STAGES = STAGES_, SMAX = SMAX_, CTAS = CTAS_;
     static constexpr bool GATED = GATED_, ALIAS = ALIAS_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 192;                    // warps 0-3 sums, 4 copies and scales, 5 products
+    static constexpr int NTHREADS = 224;                    // warps 0-3 sums, 4 copies and scales, 5 and 6 products
     static constexpr int W_TILE = 128 * 128;
     static constexpr int STAGE = H * W_TILE + BN * 128;     // weight tiles, then the tokens' rows
     // Scales of a block of K: BN tokens', then the weights'.  They are part of the block's stage (its products wait
@@ -42,7 +42,7 @@ struct NarrowCfg {
     static constexpr int OFF_MOST = OFF_SC + SCN * SC_SLOT + (ALIAS ? 0 : INBOX);      // largest magnitudes [4 warps][BN]
     static constexpr int OFF_BAR = OFF_MOST + (GATED ? 4 * BN * 4 : 0);
     // barriers: full, empty (stages), acc full, acc empty (2), inbox, final; then TMEM address, abort
-    static constexpr int NBAR = 2 * STAGES + 4 + 2;
+    static constexpr int NBAR = 2 * STAGES + 4 + 3;
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TMEM_COLS = 2 * H * BN < 32 ? 32 : 2 * H * BN;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         for (int s = 0; s < STAGES; ++s) ptx::mbar_init(full(s), 33), ptx::mbar_init(empty(s), 1);
         for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 4);
         ptx::mbar_init(inbox_bar, 1);
-        ptx::mbar_init(final_bar, 1);
+        ptx::mbar_init(final_bar, 1), ptx::mbar_init(final_bar + 8u, 1);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
         if (S > 1 && own > 0) ptx::mbar_arrive_expect_tx(inbox_bar, (uint32_t)(S * H * 128 * own * 16));
@@ -154,16 +154,17 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
                     atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
         ptx::cp_async_wait_all();
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp >= 5) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
+            // Two warps issue in turn, each for one buffer of sums: a block's waits, commits and loop (some 250 cycles)
+            // then lie beside the other warp's products, which the tensor cores only take as fast as they work.
             constexpr uint32_t idesc = ptx::make_idesc_e4m3(128, BN);
-            int s = 0;
+            const int b = warp - 5;
+            int s = b;
             uint32_t ph = 0;
-            for (int i = 0; i < n_kb; ++i) {
-                const int b = i & 1;
-                if (!wait(acc_empty(b), ((uint32_t)(i >> 1) & 1u) ^ 1u, DEVICE_TIMEOUT_MMA) ||
-                    !wait(full(s), ph, DEVICE_TIMEOUT_MMA))
+            for (int i = b; i < n_kb; i += 2) {
+                if (!wait(acc_empty(b), ((uint32_t)(i >> 1) & 1u) ^ 1u, DEVICE_TIMEOUT_MMA) || !wait(full(s), ph, DEVICE_TIMEOUT_MMA))
                     break;
                 ptx::tc_fence_after();
                 const uint32_t w_lo = ptx::sdesc_lo(sbase + s * C::STAGE);
@@ -176,11 +177,11 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
                                           t_lo + 2 * k, ptx::kSdescHi, idesc, k > 0);
                 ptx::mma_commit<1>(acc_full(b));
                 ptx::mma_commit<1>(empty(s));
-                if (++s == STAGES) s = 0, ph ^= 1u;
+                if ((s += 2) >= STAGES) s -= STAGES, ph ^= 1u;
             }
             if (!ok) {
-                ptx::mma_commit<1>(final_bar);
-                if (!drain_wait(final_bar, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+                ptx::mma_commit<1>(final_bar + 8u * b);
+                if (!drain_wait(final_bar + 8u * b, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
             }
         }
         __syncwarp();

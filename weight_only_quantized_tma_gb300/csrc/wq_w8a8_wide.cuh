@@ -20,7 +20,7 @@ template <bool GATED_>
 struct WideCfg {
     static constexpr bool GATED = GATED_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 384;        // warp 0 copies and scales, 1 products, 2 tensor memory, 4-11 sums
+    static constexpr int NTHREADS = 384;        // warp 0 copies and scales, 1 and 3 products, 2 tensor memory, 4-11 sums
     static constexpr int STAGES = GATED ? 5 : 4;
     static constexpr int STAGE = 2 * 128 * 128;             // 128 tokens, 128 weight rows
     static constexpr int OUT_WARP = GATED ? 4096 : 8192;    // a warp's part of the output: 32 rows of 128 or 256 bytes
@@ -36,7 +36,7 @@ struct WideCfg {
     static constexpr int SC_SLOT = 130 * 4 + 8;
     static constexpr int OFF_SC = OFF_OUT + 8 * OUT_WARP;
     static constexpr int OFF_BAR = OFF_SC + SCN * SC_SLOT;
-    static constexpr int NBAR = 2 * STAGES + 4 + 4 + 1;         // full, empty, acc full / empty (2), pairs of warps (4), final
+    static constexpr int NBAR = 2 * STAGES + 4 + 4 + 2;         // full, empty, acc full / empty (2), pairs of warps (4), final
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TILE_N = GATED ? 128 : 256;            // columns of the output
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         }
         for (int b = 0; b < 2; ++b) ptx::mbar_init(acc_full(b), 1), ptx::mbar_init(acc_empty(b), 16);
         for (int q = 0; q < 4; ++q) ptx::mbar_init(pair_bar(q), 2);
-        ptx::mbar_init(final_bar, 1);
+        ptx::mbar_init(final_bar, 1), ptx::mbar_init(final_bar + 8u, 1);
         *abort_flag = 0u;
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
@@ -168,31 +168,31 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                     ptx::mbar_arrive_cluster(to + 8u * s);
                     if (++s == STAGES) s = 0, ph ^= 1u;
                 }
-        } else if (warp == 1 && lane == 0) {
+        } else if ((warp == 1 || warp == 3) && lane == 0 && rank == 0) {
             // -------------------------------------------------------- products
+            // Two warps issue in turn, each for one buffer of sums: a block's waits, commits and loop (some 250 cycles)
+            // then lie beside the other warp's products, which the tensor cores only take as fast as they work.
             constexpr uint32_t idesc = ptx::make_idesc_e4m3(256, 256);
-            int s = 0;
-            uint32_t ph = 0, n = 0;      // n: blocks of K so far, buffer n % 2
-            for (int t = first; t < n_tiles && ok; t += step)
-                for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
-                    const int b = n & 1u;
-                    if (!wait(acc_empty(b), (n >> 1 & 1u) ^ 1u, DEVICE_TIMEOUT_MMA) || !wait(full(s), ph, DEVICE_TIMEOUT_MMA))
-                        break;
-                    ptx::tc_fence_after();
-                    const uint32_t a_lo = ptx::sdesc_lo(sbase + s * C::STAGE), b_lo = a_lo + (16384 >> 4);
+            const uint32_t b = warp >> 1;
+            const long long all = (long long)((n_tiles - first + step - 1) / step) * p.kblocks;
+            int s = (int)b;
+            uint32_t ph = 0, use = 0;      // use: how often this buffer has been used
+            for (long long n = b; n < all; n += 2, ++use) {
+                if (!wait(full(s), ph, DEVICE_TIMEOUT_MMA) || !wait(acc_empty(b), (use & 1u) ^ 1u, DEVICE_TIMEOUT_MMA)) break;
+                ptx::tc_fence_after();
+                const uint32_t a_lo = ptx::sdesc_lo(sbase + s * C::STAGE), b_lo = a_lo + (16384 >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_f8_ss<2>(tmem + b * 256, a_lo + 2 * k, ptx::kSdescHi, b_lo + 2 * k, ptx::kSdescHi, idesc, k > 0);
-                    ptx::mma_commit_pair(empty(s));
-                    ptx::mma_commit_pair(acc_full(b));
-                    if (++s == STAGES) s = 0, ph ^= 1u;
-                }
+                for (int k = 0; k < 4; ++k)
+                    ptx::mma_f8_ss<2>(tmem + b * 256, a_lo + 2 * k, ptx::kSdescHi, b_lo + 2 * k, ptx::kSdescHi, idesc, k > 0);
+                ptx::mma_commit_pair(acc_full(b));
+                ptx::mma_commit_pair(empty(s));
+                if ((s += 2) >= STAGES) s -= STAGES, ph ^= 1u;
+            }
             // the last arrivals of the other block land before this one may end
-            if (n > 0) wait(acc_empty((n - 1) & 1u), (n - 1) >> 1 & 1u, DEVICE_TIMEOUT_MMA);
-            if (n > 1) wait(acc_empty(n & 1u), (n - 2) >> 1 & 1u, DEVICE_TIMEOUT_MMA);
+            if (use > 0) wait(acc_empty(b), (use - 1) & 1u, DEVICE_TIMEOUT_MMA);
             if (!ok) {
-                ptx::mma_commit<2>(final_bar);
-                if (!drain_wait(final_bar, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+                ptx::mma_commit<2>(final_bar + 8u * b);
+                if (!drain_wait(final_bar + 8u * b, 0, p.timeout_ns)) atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
             }
         }
         __syncwarp();
