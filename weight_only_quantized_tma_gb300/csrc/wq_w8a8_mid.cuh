@@ -14,7 +14,7 @@ template <bool GATED_>
 struct MidCfg {
     static constexpr bool GATED = GATED_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 384;                    // warp 0 copies and scales, 1 and 3 products, 2 tensor memory, 4-11 sums
+    static constexpr int NTHREADS = 384;                    // warp 0 copies, 1 and 3 products, 2 tensor memory and scales, 4-11 sums
     static constexpr int SMAX = GATED ? 1 : 8;              // (both halves' sums of two slices do not fit)
     static constexpr int N = 128 * H;                       // weight rows of a tile
     static constexpr int CT = N / 2;                        // columns of a thread
@@ -104,26 +104,37 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
 
     if (warp < 4) {
         ptx::regs_dec<C::REGS_ISSUE>();
-        if (warp == 0) {
-            // -------------------------------------------------------- copies and scales
+        if (warp == 0 && lane == 0) {
+            // -------------------------------------------------------- copies
             const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
             const uint64_t pol_a = ptx::policy_evict_last();
             const uint32_t bytes = (uint32_t)(C::N * 128 + p.box_m * 128);
+            int i = 0, s = 0;
+            uint32_t ph = 0;
+            for (; i < n_kb && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
+                const uint32_t dst = sbase + s * C::STAGE;
+                ptx::mbar_arrive_expect_tx(full(s), bytes);
+#pragma unroll
+                for (int j = 0; j < C::N / 64; ++j)
+                    ptx::tma_load_3d(dst + 16384 + j * 8192, &p.tmap_w, (kb0 + i) * 128, w_row(j), w_half(j), full(s), pol_w);
+                ptx::tma_load_2d(dst, &p.tmap_a, (kb0 + i) * 128, (int)m0, full(s), pol_a);
+                if (++s == STAGES) s = 0, ph ^= 1u;
+            }
+            // every stage released: the commits that arrive here have all landed
+            for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
+                if (++s == STAGES) s = 0, ph ^= 1u;
+            if (!ok)   // copies in flight land before the block ends
+                for (int j = max(0, i - STAGES); j < i; ++j)
+                    if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
+                        atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+        } else if (warp == 2) {
+            // -------------------------------------------------------- scales
             const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
             const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
             const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
-            int i = 0, s = 0;
+            int s = 0;
             uint32_t ph = 0;
-            for (; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
-                if (lane == 0) {
-                    const uint32_t dst = sbase + s * C::STAGE;
-                    ptx::mbar_arrive_expect_tx(full(s), bytes);
-#pragma unroll
-                    for (int j = 0; j < C::N / 64; ++j)
-                        ptx::tma_load_3d(dst + 16384 + j * 8192, &p.tmap_w, (kb0 + i) * 128, w_row(j), w_half(j), full(s), pol_w);
-                    ptx::tma_load_2d(dst, &p.tmap_a, (kb0 + i) * 128, (int)m0, full(s), pol_a);
-                }
-                __syncwarp();
+            for (int i = 0; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
                 const uint32_t sc = sbase + C::OFF_SC + i % SCN * C::SC_SLOT;
 #pragma unroll
                 for (int r = lane; r < 128; r += 32) ptx::cp_async4(sc + 4 * r, sa + (r < rows ? r : 0), r < rows);
@@ -132,13 +143,6 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
                 sa += p.M;
                 if (++s == STAGES) s = 0, ph ^= 1u;
             }
-            // every stage released: the commits that arrive here have all landed
-            for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
-                if (++s == STAGES) s = 0, ph ^= 1u;
-            if (!ok && lane == 0)   // copies in flight land before the block ends
-                for (int j = max(0, i - STAGES); j < i; ++j)
-                    if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
-                        atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
             ptx::cp_async_wait_all();
         } else if ((warp == 1 || warp == 3) && lane == 0) {
             // -------------------------------------------------------- products

@@ -27,7 +27,7 @@ struct NarrowCfg {
     static constexpr int BN = BN_, STAGES = STAGES_, SMAX = SMAX_, CTAS = CTAS_;
     static constexpr bool GATED = GATED_, ALIAS = ALIAS_;
     static constexpr int H = GATED ? 2 : 1;
-    static constexpr int NTHREADS = 224;                    // warps 0-3 sums, 4 copies and scales, 5 and 6 products
+    static constexpr int NTHREADS = 256;                    // warps 0-3 sums, 4 copies, 5 and 6 products, 7 scales
     static constexpr int W_TILE = 128 * 128;
     static constexpr int STAGE = H * W_TILE + BN * 128;     // weight tiles, then the tokens' rows
     // Scales of a block of K: BN tokens', then the weights'.  They are part of the block's stage (its products wait
@@ -118,25 +118,39 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     for (int i = 0; i < H * BN; ++i) acc[i] = 0.f;
 
     if (warp == 4) {
-        // ------------------------------------------------------------ copies and scales
-        const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
-        const uint64_t pol_a = ptx::policy_evict_last();
-        const uint32_t bytes = (uint32_t)(H * C::W_TILE + p.box_m * 128);
-        const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
-        const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
-        const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
-        int i = 0, s = 0;
-        uint32_t ph = 0;
-        for (; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
-            if (lane == 0) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
+            const uint64_t pol_a = ptx::policy_evict_last();
+            const uint32_t bytes = (uint32_t)(H * C::W_TILE + p.box_m * 128);
+            int i = 0, s = 0;
+            uint32_t ph = 0;
+            for (; i < n_kb && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
                 const uint32_t dst = sbase + s * C::STAGE;
                 ptx::mbar_arrive_expect_tx(full(s), bytes);
 #pragma unroll
                 for (int h = 0; h < H; ++h)
                     ptx::tma_load_3d(dst + h * C::W_TILE, &p.tmap_w, (kb0 + i) * 128, nt * 128, h, full(s), pol_w);
                 ptx::tma_load_2d(dst + H * C::W_TILE, &p.tmap_a, (kb0 + i) * 128, (int)m0, full(s), pol_a);
+                if (++s == STAGES) s = 0, ph ^= 1u;
             }
-            __syncwarp();
+            // every stage released: the commits that arrive here have all landed
+            for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
+                if (++s == STAGES) s = 0, ph ^= 1u;
+            if (!ok)   // copies in flight land before the block ends
+                for (int j = max(0, i - STAGES); j < i; ++j)
+                    if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
+                        atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ------------------------------------------------------------ scales
+        const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
+        const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
+        const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int i = 0; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
             const uint32_t sc = sbase + C::OFF_SC + i % SCN * C::SC_SLOT;
 #pragma unroll
             for (int c = lane; c < BN; c += 32) ptx::cp_async4(sc + 4 * c, sa + (c < cols ? c : 0), c < cols);
@@ -145,15 +159,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
             sa += p.M;
             if (++s == STAGES) s = 0, ph ^= 1u;
         }
-        // every stage released: the commits that arrive here have all landed
-        for (int j = 0; j < STAGES && wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++j)
-            if (++s == STAGES) s = 0, ph ^= 1u;
-        if (!ok && lane == 0)   // copies in flight land before the block ends
-            for (int j = max(0, i - STAGES); j < i; ++j)
-                if (!drain_wait(full(j % STAGES), (uint32_t)(j / STAGES) & 1u, p.timeout_ns))
-                    atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
         ptx::cp_async_wait_all();
-        __syncwarp();
     } else if (warp >= 5) {
         // ------------------------------------------------------------ products
         if (lane == 0) {
