@@ -59,13 +59,13 @@ struct Split {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    // Slices of K that end soonest, and when, in 10 ns: the rounds of clusters times (`block` for each block of K, 2 us to
-    // start and end), and 1 us for the exchange.  0 slices: the device cannot be asked.
+    // Slices of K that end soonest, and when, in 10 ns: the rounds of clusters times (`block` for each block of K and `ends`
+    // to start and end), and 1 us for the exchange.  0 slices: the device cannot be asked.
     struct Plan {
         int splits;
         int64_t cost;
     };
-    static Plan plan(const W8A8Params& p, int sms, int block) {
+    static Plan plan(const W8A8Params& p, int sms, int block, int ends) {
         const Device* d = device(sms);
         Plan best{0, 0};
         if (!d) return best;
@@ -73,7 +73,7 @@ struct Split {
         for (int s = 1; s <= C::SMAX && (s == 1 || p.kblocks >= 2 * s); ++s) {
             if (d->clusters[s] < 1) continue;
             const int64_t rounds = (tiles + d->clusters[s] - 1) / d->clusters[s];
-            const int64_t cost = rounds * ((p.kblocks + s - 1) / s * block + 200) + (s > 1 ? 100 : 0);
+            const int64_t cost = rounds * ((p.kblocks + s - 1) / s * block + ends) + (s > 1 ? 100 : 0);
             if (s == 1 || cost < best.cost) best = Plan{s, cost};
         }
         return best;
@@ -146,12 +146,12 @@ struct Wide {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    // as Split's
+    // When its rounds of tiles have ended, in 10 ns: `block` for each block of K, 2 us for each tile, 3 for the kernel.
     static int64_t cost(const W8A8Params& p, int block) {
         const Device* d = device();
         if (!d) return INT64_MAX;
         const int64_t tiles = (p.M + 255) / 256 * ((p.N + C::TILE_N - 1) / C::TILE_N);
-        return (tiles + d->pairs - 1) / d->pairs * ((int64_t)p.kblocks * block + 200);
+        return (tiles + d->pairs - 1) / d->pairs * ((int64_t)p.kblocks * block + 200) + 300;
     }
     static cudaError_t launch(W8A8Params p, cudaStream_t st) {
         const Device* d = device();
@@ -189,24 +189,24 @@ struct Wide {
 
 // Up to 32 tokens weight rows are the tensor cores' M dimension: nothing of a tile is unused but what 16 or 32 exceed
 // the tokens by, and two blocks are resident on each SM.  From there on tokens are, in tiles of a block's own or of a
-// pair's, by which of them ends first.  What a block of K takes is measured (10 ns): 38 in a tile of a block's own
-// (63 gated), 43 (48) in a pair's, which is four times as large (gated twice).  Both measured, in us:
+// pair's, whichever ends first.  What a block of K takes is measured (10 ns): 33 in a tile of a block's own (62 gated),
+// 42 (44) in a pair's, which is four times as large (gated twice).  Both measured, in us:
 //   tokens x rows x K           own   pair      tokens x rows x K, gated    own   pair
-//   333 x 4096 x 4096          17.1   19.0      400 x 4096 x 4096          26.6   21.1
-//   512 x 4096 x 4096          17.6   19.0      512 x 6928 x 2560          40.6   26.2
-//   768 x 4096 x 4096          39.9   19.6      777 x 6928 x 2560          60.8   37.5
-//   512 x 12288 x 4096         52.2   35.0
-// (and with weight rows as M in tiles of 64 or 128 tokens: 64 x 4096 x 4096 10.3 against 9.2 of its own, 128 x 4096 x
-// 4096 14.2 against 10.6, 250 x 4096 x 4096 18.8 against 13.6; gated 64 x 11008 x 4096 38.6 against 24.7).
+//   333 x 4096 x 4096          14.1   18.4      64 x 11008 x 4096          23.0   35.7
+//   512 x 4096 x 4096          14.7   18.5      250 x 4096 x 4096          22.9   19.7
+//   768 x 4096 x 4096          35.7   19.0      250 x 11008 x 4096         46.9   36.2
+//   333 x 12288 x 4096         29.7   33.6      777 x 6928 x 2560          53.7   36.5
+//   512 x 12288 x 4096         43.7   33.8
+// (Weight rows as M in tiles of 64 or 128 tokens took longer than tokens as M from 33 tokens on, by an eighth to a third.)
 template <bool GATED>
 cudaError_t launch_many(const W8A8Params& p, int sms, cudaStream_t st) {
-    const typename Mid<GATED>::Plan own = Mid<GATED>::plan(p, sms, GATED ? 63 : 38);
-    if (Wide<GATED>::cost(p, GATED ? 48 : 43) < own.cost) return Wide<GATED>::launch(p, st);
+    const typename Mid<GATED>::Plan own = Mid<GATED>::plan(p, sms, GATED ? 62 : 33, 400);
+    if (Wide<GATED>::cost(p, GATED ? 44 : 42) < own.cost) return Wide<GATED>::launch(p, st);
     return Mid<GATED>::launch(p, own.splits, st);
 }
 template <typename K>
 cudaError_t launch_few(const W8A8Params& p, int sms, cudaStream_t st) {
-    return K::launch(p, K::plan(p, sms, 50).splits, st);
+    return K::launch(p, K::plan(p, sms, 50, 200).splits, st);
 }
 
 }  // namespace
