@@ -41,6 +41,9 @@ struct WideCfg {
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TILE_N = GATED ? 128 : 256;            // columns of the output
     static constexpr int GROUP = 8;             // token tiles that the walk keeps together
+    // Columns of the sums that a load reads: 32 leave fewer waits for loads (8192 x 12288 x 4096: 304 -> 302 us), but
+    // the gated kernel, with two factors, then spills inside the loop (8192 x 2048 x 11008, gated: 271 -> 348 us).
+    static constexpr int LOAD = GATED ? 16 : 32;
     // registers: 168 x 384 at launch = 72 x 128 + 216 x 256
     static constexpr int REGS_ISSUE = 72, REGS_SUM = 216;
     static_assert(SCN >= STAGES + 2 && (SCN & (SCN - 1)) == 0 && OFF_BAR % 8 == 0, "scales");
@@ -49,7 +52,7 @@ struct WideCfg {
 
 template <typename C>
 __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_constant__ W8A8Params p) {
-    constexpr int STAGES = C::STAGES, H = C::H, SCN = C::SCN;
+    constexpr int STAGES = C::STAGES, H = C::H, SCN = C::SCN, LOAD = C::LOAD;
     constexpr bool GATED = C::GATED;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -214,15 +217,17 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         uint8_t* out_s = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
         uint32_t n = 0, turn = 0;
         for (int t = first; t < n_tiles && ok; t += step, ++turn) {
-            float acc[128];
+            // Pairs of neighbouring columns, as the packed products take them: as single numbers ten of them were spilled
+            // (8192 x 4096 x 11008, with the wider loads: 259 -> 255 us, 8192 x 2048 x 11008 gated: 270 -> 267 us).
+            uint64_t sum[64];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            for (int i = 0; i < 64; ++i) sum[i] = 0;
             for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
                 const uint32_t b = n & 1u;
                 if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
                 ptx::tc_fence_after();
-                uint32_t v[2][16];
-                ptx::tmem_ld16(base + b * 256, v[0]);
+                uint32_t v[2][LOAD];
+                ptx::tmem_ld(base + b * 256, v[0]);
                 const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + n % SCN * C::SC_SLOT);
                 uint64_t s[H];
 #pragma unroll
@@ -231,25 +236,30 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                     s[h] = f2(f, f);
                 }
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 128 / LOAD; ++c) {
                     ptx::tmem_wait_ld_of(v[c & 1]);
-                    if (c < 7) {
-                        ptx::tmem_ld16(base + b * 256 + 16 * (c + 1), v[(c + 1) & 1]);
+                    if (c < 128 / LOAD - 1) {
+                        ptx::tmem_ld(base + b * 256 + LOAD * (c + 1), v[(c + 1) & 1]);
                     } else {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_cluster(acc_empty0 + 8u * b);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const int col = 16 * c + j;
-                        const float2 r = un2(fma_f2(f2(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1])),
-                                                    s[GATED ? c >> 2 : 0], f2(acc[col], acc[col + 1])));
-                        acc[col] = r.x, acc[col + 1] = r.y;
+                    for (int j = 0; j < LOAD; j += 2) {
+                        const int col = LOAD * c + j;
+                        sum[col / 2] = fma_f2(f2(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1])),
+                                              s[GATED ? col >> 6 : 0], sum[col / 2]);
                     }
                 }
             }
             if (!ok) break;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const float2 r = un2(sum[i]);
+                acc[2 * i] = r.x, acc[2 * i + 1] = r.y;
+            }
             // ---- output: through this warp's part of shared memory, 32 rows copied out by one thread
             if (lane == 0) ptx::bulk_wait_group_read0();     // the last copy has read it
             __syncwarp();
