@@ -26,12 +26,14 @@ struct WideCfg {
     static constexpr int OUT_WARP = GATED ? 4096 : 8192;    // a warp's part of the output: 32 rows of 128 or 256 bytes
     static constexpr int OFF_OUT = STAGES * STAGE;
     static constexpr int MOST = 2048;           // codes take half of a warp's part; largest magnitudes [2 tiles][32] behind
-    // Scales of a block of K: 128 tokens', two of the weights.  They are part of the block's stage (its products wait
-    // for them too), so that sums that can be read find their scales without a wait of their own: a wait beside
-    // tensor cores that read shared memory takes about 100 cycles, and loads straight into registers came too late
-    // (8192 x 4096 x 11008: 363 us with a barrier of their own, 356 us with loads two blocks ahead).  A slot is
-    // filled again SCN blocks on, when the products of STAGES blocks before that have ended, for which the sums
-    // two blocks earlier had to be read: nobody reads it any more.
+    // Scales of a block of K: 128 tokens', two of the weights.  They are part of the stage of the block before (its
+    // products wait for them too; the first block's are with its own), so that sums that can be read find the next
+    // block's scales without a wait of their own, and read them while they wait for its products: beside tensor cores
+    // that read shared memory a wait takes about 100 cycles, a read hardly less (8192 x 4096 x 11008: 363 us with a
+    // barrier of their own, 356 us with loads from memory two blocks ahead, 274 us in the stage; 8192 x 2048 x 11008
+    // gated: 272 us read behind the wait, 265 us before it).  A slot is filled again SCN - 1 blocks on, when the
+    // products of STAGES blocks before that have ended, for which the sums two blocks earlier had to be read, which
+    // is at least the block whose scales these were.
     static constexpr int SCN = 8;
     static constexpr int SC_SLOT = 130 * 4 + 8;
     static constexpr int OFF_SC = OFF_OUT + 8 * OUT_WARP;
@@ -46,7 +48,7 @@ struct WideCfg {
     static constexpr int LOAD = GATED ? 16 : 32;
     // registers: 168 x 384 at launch = 72 x 128 + 216 x 256
     static constexpr int REGS_ISSUE = 72, REGS_SUM = 216;
-    static_assert(SCN >= STAGES + 2 && (SCN & (SCN - 1)) == 0 && OFF_BAR % 8 == 0, "scales");
+    static_assert(SCN >= STAGES + 3 && (SCN & (SCN - 1)) == 0 && OFF_BAR % 8 == 0, "scales");
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -146,28 +148,37 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         } else if (warp == 2) {
             // -------------------------------------------------------- scales
             // (a warp of their own: in the warp of the copies they made it the slowest, 267 -> 257 us for 8192 x 4096 x 11008)
-            int s = 0, c = 0;
+            int t = first, kb = 0, s = 0, c = 0;
             uint32_t ph = 0;
-            for (int t = first; t < n_tiles && ok; t += step) {
-                int mt, nt;
-                tile_at(t, mt, nt);
-                const int64_t m0 = (int64_t)mt * 256 + rank * 128;
-                const int rows = (int)max((int64_t)0, min((int64_t)128, p.M - m0));
-                const float* sa = p.a_scale + (rows > 0 ? m0 : 0);
-                // lanes 0 and 1: the tile's two blocks of weight rows, or the gate's and up's
-                const int64_t wb = GATED ? (lane & 1) * wblocks + nt : min((int64_t)2 * nt + (lane & 1), wblocks - 1);
-                const float* sw = p.w_scale + wb * p.kblocks;
-                for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if (!__all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER))) break;
-                    const uint32_t sc = sbase + C::OFF_SC + c * C::SC_SLOT;
-#pragma unroll
-                    for (int r = lane; r < 128; r += 32) ptx::cp_async4(sc + 4 * r, sa + (r < rows ? r : 0), r < rows);
-                    if (lane < 2) ptx::cp_async4(sc + 4 * (128 + lane), sw + kb, true);
-                    ptx::cp_async_arrive(full(s));
-                    sa += p.M;
-                    if (++s == STAGES) s = 0, ph ^= 1u;
-                    if (++c == SCN) c = 0;
+            int rows = 0;
+            const float *sa = p.a_scale, *sw = p.w_scale;
+            auto copy = [&]() {       // the next block's, if there is one
+                if (t >= n_tiles) return;
+                if (kb == 0) {
+                    int mt, nt;
+                    tile_at(t, mt, nt);
+                    const int64_t m0 = (int64_t)mt * 256 + rank * 128;
+                    rows = (int)max((int64_t)0, min((int64_t)128, p.M - m0));
+                    sa = p.a_scale + (rows > 0 ? m0 : 0);
+                    // lanes 0 and 1: the tile's two blocks of weight rows, or the gate's and up's
+                    const int64_t wb = GATED ? (lane & 1) * wblocks + nt : min((int64_t)2 * nt + (lane & 1), wblocks - 1);
+                    sw = p.w_scale + wb * p.kblocks;
                 }
+                const uint32_t sc = sbase + C::OFF_SC + c * C::SC_SLOT;
+#pragma unroll
+                for (int r = lane; r < 128; r += 32) ptx::cp_async4(sc + 4 * r, sa + (r < rows ? r : 0), r < rows);
+                if (lane < 2) ptx::cp_async4(sc + 4 * (128 + lane), sw + kb, true);
+                sa += p.M;
+                if (++kb == p.kblocks) kb = 0, t += step;
+                if (++c == SCN) c = 0;
+            };
+            const long long all = (long long)((n_tiles - first + step - 1) / step) * p.kblocks;
+            for (long long i = 0; i < all; ++i) {
+                if (!__all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER))) break;
+                if (i == 0) copy();       // the first block's own
+                copy();
+                ptx::cp_async_arrive(full(s));
+                if (++s == STAGES) s = 0, ph ^= 1u;
             }
             ptx::cp_async_wait_all();
         } else if (warp == 1 && lane == 0 && rank == 1) {
@@ -216,6 +227,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         const uint32_t acc_empty0 = ptx::mapa_shared(acc_empty(0), 0);
         uint8_t* out_s = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
         uint32_t n = 0, turn = 0;
+        wait(acc_full(0), 0, DEVICE_TIMEOUT_TRANSFORM);      // the first scales have landed
         for (int t = first; t < n_tiles && ok; t += step, ++turn) {
             // Pairs of neighbouring columns, as the packed products take them: as single numbers ten of them were spilled
             // (8192 x 4096 x 11008, with the wider loads: 259 -> 255 us, 8192 x 2048 x 11008 gated: 270 -> 267 us).
@@ -224,17 +236,17 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
             for (int i = 0; i < 64; ++i) sum[i] = 0;
             for (int kb = 0; kb < p.kblocks; ++kb, ++n) {
                 const uint32_t b = n & 1u;
-                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
-                ptx::tc_fence_after();
-                uint32_t v[2][LOAD];
-                ptx::tmem_ld(base + b * 256, v[0]);
-                const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + n % SCN * C::SC_SLOT);
+                const volatile float* sc = reinterpret_cast<const volatile float*>(smem + C::OFF_SC + n % SCN * C::SC_SLOT);
                 uint64_t s[H];
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
                     const float f = sc[row] * sc[128 + (GATED ? h : g)];
                     s[h] = f2(f, f);
                 }
+                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
+                ptx::tc_fence_after();
+                uint32_t v[2][LOAD];
+                ptx::tmem_ld(base + b * 256, v[0]);
 #pragma unroll
                 for (int c = 0; c < 128 / LOAD; ++c) {
                     ptx::tmem_wait_ld_of(v[c & 1]);
