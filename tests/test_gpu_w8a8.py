@@ -65,6 +65,20 @@ def test_larger_gated(M, F, K):
     ref.check_pair(*wq.wq_gemm_w8a8_fp8_gated(a, sa, w, sw), *ref.gated(a, sa, w, sw))
 
 
+@pytest.mark.parametrize("M,N,K", [(6000, 4096, 128), (6000, 2056, 16), (4500, 4112, 272), (9000, 2064, 1168)])
+def test_many_tiles_of_few_blocks(M, N, K):
+    """Several tiles for each pair of thread blocks, of an odd or even number of blocks of K, down to one: scales and
+    buffers of sums go on from tile to tile."""
+    a, sa, w, sw = _case(M, N, K)
+    _check(wq.wq_gemm_w8a8_fp8(a, sa, w, sw, dtype=torch.float16), *ref.product(a, sa, w, sw), "f16")
+
+
+@pytest.mark.parametrize("M,F,K", [(6000, 2064, 128), (5000, 2816, 304), (9000, 1040, 528)])
+def test_many_gated_tiles_of_few_blocks(M, F, K):
+    a, sa, w, sw = _case(M, F, K, halves=2)
+    ref.check_pair(*wq.wq_gemm_w8a8_fp8_gated(a, sa, w, sw), *ref.gated(a, sa, w, sw))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("M", [5, 100, 700])
 def test_bias(M, dtype):
