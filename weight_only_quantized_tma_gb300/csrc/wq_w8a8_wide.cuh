@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                         atomicOr(p.status, DEVICE_TIMEOUT_DRAIN);
         } else if (warp == 2) {
             // -------------------------------------------------------- scales
-            // (a warp of their own: in the warp of the copies they made it the slowest, 267 -> 257 us for 8192 x 4096 x 11008)
+            // (a warp of their own: in the warp of the copies they made it the slowest, 267 -> 259 us for 8192 x 4096 x 11008)
             int t = first, kb = 0, s = 0, c = 0;
             uint32_t ph = 0;
             int rows = 0;
