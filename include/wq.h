@@ -425,8 +425,10 @@ wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_hea
  * fp32 scales [ceil(K / 128)][T], one for each token and block of 128 values along K (the last
  * block may be shorter); a value is e4m3(code) * scale.  The kernels that make them take
  *     scale = max(max |y| / 448, 2^-96),   code = e4m3(y / scale)
- * of a block's fp32 values y (round to nearest even).  A block that holds an infinity or a NaN
- * gets a NaN for its scale: its values are NaN, and no other block is touched. */
+ * of a block's fp32 values y: both quotients are rounded to fp32, a code to the nearest e4m3
+ * number (ties to the even code), as IEEE division and conversion do.  (Where scale is below 2^-93
+ * the second quotient may be off by its last bit.)  A block that holds an infinity or a NaN
+ * gets a NaN for its scale: its values are NaN (codes 0), and no other block is touched. */
 
 /* Norm of rows with the residual's addition, T rows of H values, in fp32 with one rounding:
  *     s = x + residual,   sum = RN(s),   out = RN(s * rsqrt(mean(s^2) + eps) * weight)

@@ -40,11 +40,8 @@ __device__ __forceinline__ float block_most(const uint64_t (&y)[4]) {
     for (int off = 8; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
     return m;
 }
-__device__ __forceinline__ uint2 codes8(const uint64_t (&y)[4], float inv) {
-    if (inv == 0.f) return make_uint2(0u, 0u);   // (a NaN times 0 would be one)
-    const uint64_t by = f2(inv, inv);
-    const float2 a = un2(mul_f2(y[0], by)), b = un2(mul_f2(y[1], by)), c = un2(mul_f2(y[2], by)), d = un2(mul_f2(y[3], by));
-    return make_uint2(to_e4m3x4(a.x, a.y, b.x, b.y), to_e4m3x4(c.x, c.y, d.x, d.y));
+__device__ __forceinline__ uint2 codes8(const uint64_t (&y)[4], const BlockScale& q) {
+    return make_uint2(q.codes(y[0], y[1]), q.codes(y[2], y[3]));
 }
 
 // rsqrt(mean + eps) from a sum of squares; `again(f)` gives the sum of (f s)^2 where the plain one has
@@ -65,7 +62,7 @@ __device__ __forceinline__ float inverse_rms(float sum, float inv_h, float eps, 
 // blocks that stay, rows arriving by bulk copies (43 to 46 us), the next row loaded into registers early (43 to 44).
 template <bool BF16, int C, bool ADD, bool QUANT>
 __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 2 : 3) : C == 2 ? (ADD ? 3 : 4) : 4) norm_kernel(const NormParams p) {
-    __shared__ float part[2][16];
+    __shared__ __align__(16) float part[2][16];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
@@ -117,7 +114,12 @@ __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 
         if (lane == 0) part[turn][threadIdx.x >> 5] = v;
         __syncthreads();
         float all = 0.f;
-        for (int w = 0; w < warps; ++w) all += part[turn][w];
+#pragma unroll
+        for (int w = 0; w < 16; w += 4) {      // (four in one load: 8192 x 4096 to 8 bits 44.7 -> 43.8 us)
+            if (w >= warps) break;
+            const float4 q = *reinterpret_cast<const float4*>(&part[turn][w]);
+            all += q.x, all += w + 1 < warps ? q.y : 0.f, all += w + 2 < warps ? q.z : 0.f, all += w + 3 < warps ? q.w : 0.f;
+        }
         return all;
     };
     const float inv = inverse_rms(total(sum, 0), p.inv_h, p.eps, [&](float f) {
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 
             }
             const BlockScale q(block_most(v));
             if (row && at < p.H) {
-                *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(v, q.inv);
+                *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(v, q);
                 if ((lane & 15) == 0) p.scales[(int64_t)(at >> 7) * p.T + t] = q.scale;
             }
         } else if (row && at < p.H) {
@@ -186,7 +188,7 @@ cudaError_t launch_norm_t(const NormParams& p, cudaStream_t st) {
 // 16 tokens for each block of 256 threads: 16 lanes take one token's block of 128, U of them in turn whose
 // loads are all issued first.  The scales of 16 tokens are neighbours.
 template <bool BF16, int U>
-__global__ void __launch_bounds__(256) quantize_kernel(const NormParams p) {
+__global__ void __launch_bounds__(256, 6) quantize_kernel(const NormParams p) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int lane = threadIdx.x & 15;
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const NormParams p) {
         unpack8<BF16>(xr[u], y);
         const BlockScale q(block_most(y));
         if (row && at < p.H) {
-            *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(y, q.inv);
+            *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(y, q);
             if (lane == 0) p.scales[(int64_t)(kb0 + u) * p.T + t] = q.scale;
         }
     }

@@ -287,8 +287,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
             // (columns past N are products of zeros)
             const BlockScale q(warp_most(max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])))));
             if (n < p.N)
-                *reinterpret_cast<uint32_t*>(p.codes + m * p.N + n) =
-                    q.inv == 0.f ? 0u : to_e4m3x4(v[0] * q.inv, v[1] * q.inv, v[2] * q.inv, v[3] * q.inv);
+                *reinterpret_cast<uint32_t*>(p.codes + m * p.N + n) = q.codes(f2(v[0], v[1]), f2(v[2], v[3]));
             if (lane == 0) p.scales[(int64_t)nt * p.M + m] = q.scale;
         }
     }

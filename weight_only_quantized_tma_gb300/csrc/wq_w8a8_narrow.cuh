@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
                 if (c < mine) {
                     const BlockScale q(max_nan(max_nan(most[c], most[BN + c]), max_nan(most[2 * BN + c], most[3 * BN + c])));
                     if (n < p.N)
-                        p.codes[(m_first + c) * p.N + n] = q.inv == 0.f ? 0 : (uint8_t)to_e4m3x4(v[e] * q.inv, 0.f, 0.f, 0.f);
+                        p.codes[(m_first + c) * p.N + n] = q.code(v[e]);
                     if (row == 0) p.scales[(int64_t)nt * p.M + m_first + c] = q.scale;
                 }
             }

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float* a = acc + c + 4 * j;
-                        o[j] = q.inv == 0.f ? 0u : to_e4m3x4(a[0] * q.inv, a[1] * q.inv, a[2] * q.inv, a[3] * q.inv);
+                        o[j] = q.codes(f2(a[0], a[1]), f2(a[2], a[3]));
                     }
                     *reinterpret_cast<uint4*>(out_s + lane * 64 + c) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
