@@ -44,14 +44,94 @@ __device__ __forceinline__ uint2 codes8(const uint64_t (&y)[4], const BlockScale
     return make_uint2(q.codes(y[0], y[1]), q.codes(y[2], y[3]));
 }
 
-// rsqrt(mean + eps) from a sum of squares; `again(f)` gives the sum of (f s)^2 where the plain one has
-// left fp32's range (a row of numbers around 2^64 and above, or all of them tiny without an eps that
-// outweighs them).
-template <typename Again>
-__device__ __forceinline__ float inverse_rms(float sum, float inv_h, float eps, Again again) {
-    if (!(sum <= 3.402823466e38f)) return rsqrtf(again(0x1p-72f) * inv_h + eps * 0x1p-144f) * 0x1p-72f;
-    if (sum < 0x1p-90f && eps < 0x1p-80f) return rsqrtf(again(0x1p80f) * inv_h + eps * 0x1p80f * 0x1p80f) * 0x1p80f;
-    return rsqrtf(sum * inv_h + eps);
+// A row's total, the same in each of its threads; `part` is the block's, one for each turn.
+__device__ __forceinline__ float row_total(float v, float* part) {
+    const int warps = (int)(blockDim.x >> 5);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float all = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; w += 4) {      // (four in one load: 8192 x 4096 to 8 bits 44.7 -> 43.8 us)
+        if (w >= warps) break;
+        const float4 q = *reinterpret_cast<const float4*>(part + w);
+        all += q.x, all += w + 1 < warps ? q.y : 0.f, all += w + 2 < warps ? q.z : 0.f, all += w + 3 < warps ? q.w : 0.f;
+    }
+    return all;
+}
+
+// Eight values of row t from `at` on, times inv and the weight, to the output.
+template <bool BF16, bool QUANT>
+__device__ __forceinline__ void finish_values(const NormParams& p, int64_t t, int at, uint64_t (&v)[4], float inv) {
+    const bool in = t < p.T && at < p.H;
+    uint64_t w[4];
+    unpack8<BF16>(at < p.H ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at)) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul_f2(mul_f2(v[i], f2(inv, inv)), w[i]);
+    if (QUANT) {
+        // lanes past the row hold zeros (0 * inv * 0, where inv may be infinite: not those)
+        if (at >= p.H) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = 0;
+        }
+        const BlockScale q(block_most(v));
+        if (in) {
+            *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(v, q);
+            if ((threadIdx.x & 15) == 0) p.scales[(int64_t)(at >> 7) * p.T + t] = q.scale;
+        }
+    } else if (in) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + at) = pack8<BF16>(v);
+    }
+}
+
+// Where a row's sum of squares, or the mean with eps, has left fp32's range (a row of numbers around 2^64 and above, or
+// all of them tiny without an eps that outweighs them) the squares are taken of f s; as the root may be below 2^-126 or
+// past 2^128 itself, the values are multiplied with g first.
+struct Range {
+    bool large;
+    float f, g;
+    __device__ __forceinline__ explicit Range(bool l) : large(l), f(l ? 0x1p-72f : 0x1p80f), g(l ? 0x1p-32f : 0x1p32f) {}
+    __device__ __forceinline__ float square(uint64_t (&v)[4]) const {
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 u = un2(mul_f2(v[i], f2(f, f)));
+            sq += u.x * u.x + u.y * u.y;
+            v[i] = mul_f2(v[i], f2(g, g));
+        }
+        return sq;
+    }
+    // of g s, from the total of squares
+    __device__ __forceinline__ float inverse(float sq, float inv_h, float eps) const {
+        return rsqrtf(sq * inv_h + eps * f * f) * (large ? 0x1p-40f : 0x1p48f);
+    }
+};
+
+// Such a row without a residual, from memory once more: no register of the usual way is held for it.
+template <bool BF16, int C, bool QUANT>
+__device__ __noinline__ void norm_again(const NormParams& p, int64_t t, bool large, float* part) {
+    const Range range(large);
+    const int first = 8 * (int)threadIdx.x, step = 8 * (int)blockDim.x;
+    auto load = [&](int at, uint64_t (&v)[4]) {
+        const uint16_t* x = static_cast<const uint16_t*>(p.x) + t * p.x_stride + at;
+        unpack8<BF16>(t < p.T && at < p.H ? *reinterpret_cast<const uint4*>(x) : make_uint4(0, 0, 0, 0), v);
+        return range.square(v);
+    };
+    float sq = 0.f;
+#pragma unroll 1
+    for (int at = first; at < C * step; at += step) {
+        uint64_t v[4];
+        sq += load(at, v);
+    }
+    const float inv = range.inverse(row_total(sq, part), p.inv_h, p.eps);
+#pragma unroll 1
+    for (int at = first; at < C * step; at += step) {
+        uint64_t v[4];
+        load(at, v);
+        finish_values<BF16, QUANT>(p, t, at, v, inv);
+    }
 }
 
 // One row for each group of `blockDim.x` threads (blockDim.y rows in a block; more than one only where a
@@ -61,11 +141,10 @@ __device__ __forceinline__ float inverse_rms(float sum, float inv_h, float eps, 
 // read late.  8192 x 4096 with a residual: 42.6 us (6.3 TB/s), to 8 bits 42 (5.6 TB/s; issue slots 56 % full).  Tried:
 // blocks that stay, rows arriving by bulk copies (43 to 46 us), the next row loaded into registers early (43 to 44).
 template <bool BF16, int C, bool ADD, bool QUANT>
-__global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 2 : 3) : C == 2 ? (ADD ? 3 : 4) : 4) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 2 : 3) : C == 2 ? (ADD ? 3 : 4) : 4) norm_kernel(const __grid_constant__ NormParams p) {
     __shared__ __align__(16) float part[2][16];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool row = t < p.T;
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + t * p.x_stride;
@@ -81,14 +160,6 @@ __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 
         xr[c] = in ? load_once(x + at) : make_uint4(0, 0, 0, 0);
         if (ADD) rr[c] = in ? load_once(r + at) : make_uint4(0, 0, 0, 0);
     }
-    auto values = [&](int c, uint64_t (&v)[4]) {
-        if (ADD) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = s[c][i];
-        } else {
-            unpack8<BF16>(xr[c], v);
-        }
-    };
     uint64_t squares = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -105,59 +176,21 @@ __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 
 #pragma unroll
         for (int i = 0; i < 4; ++i) squares = fma_f2(s[c][i], s[c][i], squares);
     }
-    const float sum = un2(squares).x + un2(squares).y;
-    // the row's total, the same in each of its threads
-    auto total = [&](float v, int turn) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (warps == 1) return v;
-        if (lane == 0) part[turn][threadIdx.x >> 5] = v;
-        __syncthreads();
-        float all = 0.f;
-#pragma unroll
-        for (int w = 0; w < 16; w += 4) {      // (four in one load: 8192 x 4096 to 8 bits 44.7 -> 43.8 us)
-            if (w >= warps) break;
-            const float4 q = *reinterpret_cast<const float4*>(&part[turn][w]);
-            all += q.x, all += w + 1 < warps ? q.y : 0.f, all += w + 2 < warps ? q.z : 0.f, all += w + 3 < warps ? q.w : 0.f;
-        }
-        return all;
-    };
-    const float inv = inverse_rms(total(sum, 0), p.inv_h, p.eps, [&](float f) {
+    const float sum = row_total(un2(squares).x + un2(squares).y, part[0]), mean = sum * p.inv_h + p.eps;
+    float inv = rsqrtf(mean);
+    const bool large = !(mean <= 3.402823466e38f);
+    if (large || (sum < 0x1p-90f && p.eps < 0x1p-80f)) {      // (the row's threads agree on it)
+        if (!ADD) return norm_again<BF16, C, QUANT>(p, t, large, part[1]);
+        const Range range(large);
         float sq = 0.f;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            uint64_t v[4];
-            values(c, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 u = un2(mul_f2(v[i], f2(f, f)));
-                sq += u.x * u.x + u.y * u.y;
-            }
-        }
-        return total(sq, 1);   // (the row's threads agree on whether they come here)
-    });
+        for (int c = 0; c < C; ++c) sq += range.square(s[c]);
+        inv = range.inverse(row_total(sq, part[1]), p.inv_h, p.eps);
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int at = 8 * (int)(threadIdx.x + c * blockDim.x);
-        uint64_t v[4], w[4];
-        values(c, v);
-        unpack8<BF16>(at < p.H ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.weight) + at)) : make_uint4(0, 0, 0, 0), w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = mul_f2(mul_f2(v[i], f2(inv, inv)), w[i]);
-        if (QUANT) {
-            // lanes past the row hold zeros (0 * inv * 0, where inv may be infinite: not those)
-            if (at >= p.H) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = 0;
-            }
-            const BlockScale q(block_most(v));
-            if (row && at < p.H) {
-                *reinterpret_cast<uint2*>(p.codes + t * p.H + at) = codes8(v, q);
-                if ((lane & 15) == 0) p.scales[(int64_t)(at >> 7) * p.T + t] = q.scale;
-            }
-        } else if (row && at < p.H) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + at) = pack8<BF16>(v);
-        }
+        if (!ADD) unpack8<BF16>(xr[c], s[c]);
+        finish_values<BF16, QUANT>(p, t, 8 * (int)(threadIdx.x + c * blockDim.x), s[c], inv);
     }
 }
 
