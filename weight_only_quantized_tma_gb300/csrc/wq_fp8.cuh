@@ -83,12 +83,18 @@ __device__ __forceinline__ float warp_most(float v) {
     return r;
 }
 
-// g / (1 + exp(-g)): -0 far below (exp overflows to infinity), NaN at minus infinity (0 times it).  The exponential and
-// the reciprocal are the special function unit's own, whose results below the normal range are zeros.
-__device__ __forceinline__ float silu(float g) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    return g * about_reciprocal(1.0f + e);
+// g / (1 + exp(-g)) of two numbers: -0 where exp overflows to infinity, NaN at minus infinity (0 times it).  The exponential
+// and the reciprocal are the special function unit's own: the exponential's argument is off by 2^-24 of itself, the
+// exponential by as much as that is, which at -88 is 2^-18 of the result and nothing beside a rounding to 16 or 8 bits.  Their
+// results below the normal range are zeros, so the reciprocal is taken of a quarter of 1 + exp(-g), which ends at 2^126.
+__device__ __forceinline__ uint64_t silu2(uint64_t g) {
+    const float2 x = un2(mul_f2(g, f2(-1.4426950408889634f, -1.4426950408889634f)));
+    float2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+    const uint64_t quarter = f2(0.25f, 0.25f);
+    const float2 d = un2(fma_f2(f2(e.x, e.y), quarter, quarter));
+    return mul_f2(mul_f2(g, quarter), f2(about_reciprocal(d.x), about_reciprocal(d.y)));
 }
 
 }  // namespace wq

@@ -266,9 +266,13 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 }
             }
             if (!ok) break;
-            float acc[128];
+            if constexpr (GATED) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
+                for (int i = 0; i < 32; ++i) sum[i] = mul_f2(silu2(sum[i]), sum[32 + i]);
+            }
+            float acc[128 / H];
+#pragma unroll
+            for (int i = 0; i < 64 / H; ++i) {
                 const float2 r = un2(sum[i]);
                 acc[2 * i] = r.x, acc[2 * i + 1] = r.y;
             }
@@ -280,12 +284,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
             const int64_t m = (int64_t)mt * 256 + rank * 128 + row;
             const int64_t n0 = (int64_t)nt * C::TILE_N + g * (128 / H);
             const bool any = n0 < p.N && m - lane < p.M;      // the warp has something to store
-            if constexpr (GATED) {
+            if (!GATED && p.bias != nullptr && n0 < p.N) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) acc[i] = silu(acc[i]) * acc[64 + i];
-            } else if (p.bias != nullptr && n0 < p.N) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
+                for (int i = 0; i < 128 / H; ++i)
                     if (n0 + i < p.N)
                         acc[i] += p.out_bf16 ? load_16bit<true>(p.bias, (size_t)(n0 + i)) : load_16bit<false>(p.bias, (size_t)(n0 + i));
             }
