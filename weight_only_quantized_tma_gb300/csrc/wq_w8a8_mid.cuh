@@ -275,9 +275,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
             }
         float v[4] = {t[0].x + bias[0], t[0].y + bias[1], t[0].z + bias[2], t[0].w + bias[3]};
         if constexpr (GATED) {
-            const float2 a = un2(mul_f2(silu2(f2(v[0], v[1])), f2(t[1].x, t[1].y)));
-            const float2 b = un2(mul_f2(silu2(f2(v[2], v[3])), f2(t[1].z, t[1].w)));
-            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+            v[0] = silu(v[0]) * t[1].x, v[1] = silu(v[1]) * t[1].y, v[2] = silu(v[2]) * t[1].z, v[3] = silu(v[3]) * t[1].w;
         }
         const int64_t m = m0 + r0 + r;
         if (!GATED || p.out != nullptr) {
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
             // (columns past N are products of zeros)
             const BlockScale q(warp_most(max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])))));
             if (n < p.N)
-                *reinterpret_cast<uint32_t*>(p.codes + m * p.N + n) = q.codes(f2(v[0], v[1]), f2(v[2], v[3]));
+                *reinterpret_cast<uint32_t*>(p.codes + m * p.N + n) = q.codes(v[0], v[1], v[2], v[3]);
             if (lane == 0) p.scales[(int64_t)nt * p.M + m] = q.scale;
         }
     }

@@ -298,9 +298,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
             }
         float v[4] = {t[0].x, t[0].y, t[0].z, t[0].w};
         if constexpr (GATED) {
-            const float2 a = un2(mul_f2(silu2(f2(v[0], v[1])), f2(t[1].x, t[1].y)));
-            const float2 b = un2(mul_f2(silu2(f2(v[2], v[3])), f2(t[1].z, t[1].w)));
-            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+            v[0] = silu(v[0]) * t[1].x, v[1] = silu(v[1]) * t[1].y, v[2] = silu(v[2]) * t[1].z, v[3] = silu(v[3]) * t[1].w;
         }
         if (codes) {
             *reinterpret_cast<float4*>(parts + j * 2048) = make_float4(v[0], v[1], v[2], v[3]);

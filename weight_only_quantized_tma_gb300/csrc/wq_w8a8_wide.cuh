@@ -266,13 +266,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 }
             }
             if (!ok) break;
-            if constexpr (GATED) {
+            float acc[128];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) sum[i] = mul_f2(silu2(sum[i]), sum[32 + i]);
-            }
-            float acc[128 / H];
-#pragma unroll
-            for (int i = 0; i < 64 / H; ++i) {
+            for (int i = 0; i < 64; ++i) {
                 const float2 r = un2(sum[i]);
                 acc[2 * i] = r.x, acc[2 * i + 1] = r.y;
             }
@@ -284,9 +280,12 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
             const int64_t m = (int64_t)mt * 256 + rank * 128 + row;
             const int64_t n0 = (int64_t)nt * C::TILE_N + g * (128 / H);
             const bool any = n0 < p.N && m - lane < p.M;      // the warp has something to store
-            if (!GATED && p.bias != nullptr && n0 < p.N) {
+            if constexpr (GATED) {
 #pragma unroll
-                for (int i = 0; i < 128 / H; ++i)
+                for (int i = 0; i < 64; ++i) acc[i] = silu(acc[i]) * acc[64 + i];
+            } else if (p.bias != nullptr && n0 < p.N) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
                     if (n0 + i < p.N)
                         acc[i] += p.out_bf16 ? load_16bit<true>(p.bias, (size_t)(n0 + i)) : load_16bit<false>(p.bias, (size_t)(n0 + i));
             }
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float* a = acc + c + 4 * j;
-                        o[j] = q.codes(f2(a[0], a[1]), f2(a[2], a[3]));
+                        o[j] = q.codes(a[0], a[1], a[2], a[3]);
                     }
                     *reinterpret_cast<uint4*>(out_s + lane * 64 + c) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
