@@ -43,6 +43,14 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, vola
     }
 }
 
+// The same for a whole warp, with one answer: a lane that saw the phase complete and one that saw the abort go the same
+// way.  `ok` stays false once it is.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(bool ok, uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          uint32_t* status, uint32_t code, long long timeout_ns) {
+    return __all_sync(0xffffffffu, ok && bounded_wait<CLUSTER>(bar, parity, abort_flag, status, code, timeout_ns));
+}
+
 // Wait used while draining after an abort: ignores the abort flag.
 __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, long long timeout_ns) {
     const uint64_t t0 = ptx::globaltimer();

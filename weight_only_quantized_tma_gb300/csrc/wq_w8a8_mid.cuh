@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
         if (ok) ok = bounded_wait(bar, parity, abort_flag, p.status, code, p.timeout_ns);
         return ok;
     };
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t code) {      // a warp's lanes together
+        return ok = warp_wait(ok, bar, parity, abort_flag, p.status, code, p.timeout_ns);
+    };
 
     if (warp < 4) {
         ptx::regs_dec<C::REGS_ISSUE>();
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
             const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
             int s = 0;
             uint32_t ph = 0;
-            for (int i = 0; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
+            for (int i = 0; i < n_kb && wait_all(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
                 const uint32_t sc = sbase + C::OFF_SC + i % SCN * C::SC_SLOT;
 #pragma unroll
                 for (int r = lane; r < 128; r += 32) ptx::cp_async4(sc + 4 * r, sa + (r < rows ? r : 0), r < rows);
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
         for (int i = 0; i < CT; ++i) acc[i] = 0.f;
         for (int i = 0; i < n_kb; ++i) {
             const int b = i & 1;
-            if (!__all_sync(0xffffffffu, wait(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
+            if (!wait_all(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM)) break;
             ptx::tc_fence_after();
             uint32_t v[2][16];
             ptx::tmem_ld16(base + b * C::N, v[0]);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
         if (S > 1) ptx::cluster_arrive_relaxed(), ptx::cluster_wait();   // the barrier behind the exchange
         return;
     }
-    ok = *abort_flag == 0u;
+    ok = __all_sync(0xffffffffu, *abort_flag == 0u);
     if (S > 1) {
         const int in_pitch = per | 1;
         if (ok)
@@ -245,10 +248,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
                                    ptx::mapa_shared(inbox_bar, (uint32_t)owner));
             }
         __syncwarp();
-        if (own > 0) {
-            ok = ok && bounded_wait<true>(inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
-            __syncwarp();
-        }
+        if (own > 0) ok = warp_wait<true>(ok, inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
         // Nobody leaves before all have what was sent to them: what they sent has then been read.
         ptx::cluster_arrive_relaxed();
     }

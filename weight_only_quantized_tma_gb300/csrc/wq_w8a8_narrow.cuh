@@ -113,6 +113,9 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         if (ok) ok = bounded_wait(bar, parity, abort_flag, p.status, code, p.timeout_ns);
         return ok;
     };
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t code) {      // a warp's lanes together
+        return ok = warp_wait(ok, bar, parity, abort_flag, p.status, code, p.timeout_ns);
+    };
     float acc[H * BN];
 #pragma unroll
     for (int i = 0; i < H * BN; ++i) acc[i] = 0.f;
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
         int s = 0;
         uint32_t ph = 0;
-        for (int i = 0; i < n_kb && __all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)); ++i) {
+        for (int i = 0; i < n_kb && wait_all(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
             const uint32_t sc = sbase + C::OFF_SC + i % SCN * C::SC_SLOT;
 #pragma unroll
             for (int c = lane; c < BN; c += 32) ptx::cp_async4(sc + 4 * c, sa + (c < cols ? c : 0), c < cols);
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
         for (int i = 0; i < n_kb; ++i) {
             const int b = i & 1;
-            if (!__all_sync(0xffffffffu, wait(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
+            if (!wait_all(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM)) break;
             ptx::tc_fence_after();
             uint32_t v[2][CH];
             auto load = [&](int c) {
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         if (S > 1) ptx::cluster_arrive_relaxed(), ptx::cluster_wait();   // (the barrier behind the exchange)
         return;
     }
-    ok = *abort_flag == 0u;
+    ok = __all_sync(0xffffffffu, *abort_flag == 0u);
     const int row = threadIdx.x;      // of the tile
     // From here on sums lie in shared memory, [part][half][group of columns][row], and are worked on in small loops:
     // code that runs once is bound by its own fetching (128 x 4096 x 4096: 38000 cycles unrolled over the columns in
@@ -268,10 +271,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
                                    sbase + (uint32_t)((h * (BN / 4) + owner * per) * 2048), (uint32_t)(theirs * 2048), bar);
         }
         __syncwarp();
-        if (own > 0) {
-            ok = ok && bounded_wait<true>(inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
-            __syncwarp();
-        }
+        if (own > 0) ok = warp_wait<true>(ok, inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
         // Nobody leaves before all have what was sent to them: what they sent has then been read.
         ptx::cluster_arrive_relaxed();
     }
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     }
     if (codes) {
         ptx::named_barrier_sync(1, 128);
+        ok = __all_sync(0xffffffffu, ok && *abort_flag == 0u);     // (another warp may not have its largest magnitudes)
 #pragma unroll 1
         for (int j = 0; j < own && ok; ++j) {
             const float4 t = *reinterpret_cast<const float4*>(parts + j * 2048);

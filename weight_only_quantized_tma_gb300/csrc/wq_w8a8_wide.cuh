@@ -114,6 +114,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         if (ok) ok = bounded_wait<true>(bar, parity, abort_flag, p.status, code, p.timeout_ns);
         return ok;
     };
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t code) {      // a warp's lanes together
+        return ok = warp_wait<true>(ok, bar, parity, abort_flag, p.status, code, p.timeout_ns);
+    };
 
     if (warp < 4) {
         ptx::regs_dec<C::REGS_ISSUE>();
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
             };
             const long long all = (long long)((n_tiles - first + step - 1) / step) * p.kblocks;
             for (long long i = 0; i < all; ++i) {
-                if (!__all_sync(0xffffffffu, wait(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER))) break;
+                if (!wait_all(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER)) break;
                 if (i == 0) copy();       // the first block's own
                 copy();
                 ptx::cp_async_arrive(full(s));
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
         const uint32_t acc_empty0 = ptx::mapa_shared(acc_empty(0), 0);
         uint8_t* out_s = smem + C::OFF_OUT + (warp - 4) * C::OUT_WARP;
         uint32_t n = 0, turn = 0;
-        wait(acc_full(0), 0, DEVICE_TIMEOUT_TRANSFORM);      // the first scales have landed
+        wait_all(acc_full(0), 0, DEVICE_TIMEOUT_TRANSFORM);      // the first scales have landed
         for (int t = first; t < n_tiles && ok; t += step, ++turn) {
             // Pairs of neighbouring columns, as the packed products take them: as single numbers ten of them were spilled
             // (8192 x 4096 x 11008, with the wider loads: 259 -> 255 us, 8192 x 2048 x 11008 gated: 270 -> 267 us).
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                     const float f = sc[row] * sc[128 + (GATED ? h : g)];
                     s[h] = f2(f, f);
                 }
-                if (!__all_sync(0xffffffffu, wait(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM))) break;
+                if (!wait_all(acc_full(b), n >> 1 & 1u, DEVICE_TIMEOUT_TRANSFORM)) break;
                 ptx::tc_fence_after();
                 uint32_t v[2][LOAD];
                 ptx::tmem_ld(base + b * 256, v[0]);
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 *reinterpret_cast<float*>(out_s + at) = most;
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(pair_bar(quarter));
-                if (!__all_sync(0xffffffffu, wait(pair_bar(quarter), turn & 1u, DEVICE_TIMEOUT_EPILOGUE))) break;
+                if (!wait_all(pair_bar(quarter), turn & 1u, DEVICE_TIMEOUT_EPILOGUE)) break;
                 const BlockScale q(max_nan(most, *reinterpret_cast<const float*>(smem + C::OFF_OUT + ((warp - 4) ^ 4) * C::OUT_WARP + at)));
                 if (g == 0 && m < p.M) p.scales[(int64_t)nt * p.M + m] = q.scale;
 #pragma unroll
