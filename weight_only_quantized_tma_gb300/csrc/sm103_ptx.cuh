@@ -476,6 +476,10 @@ __device__ __forceinline__ void st_async_v2f32(uint32_t addr, float a, float b, 
                  "f"(a), "f"(b), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // Untiled copy from this CTA's shared memory to that of a CTA of the cluster (dst and bar from mapa_shared), its
 // bytes completing on the mbarrier there.  Addresses 16-byte aligned, bytes a multiple of 16; the source stays as it
 // is, and this CTA alive, until they have.

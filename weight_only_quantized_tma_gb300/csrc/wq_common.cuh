@@ -60,6 +60,24 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, long l
     return true;
 }
 
+// Blocks of a cluster that send each other copies end together, but one that gave up does not wait for what was sent to
+// it, so nobody would know when copies into it, or out of the senders, have landed.  It tells the others before the
+// cluster's last barrier (a warp; `lost` is the shared::cta address of a word of each block, zero so far) ...
+__device__ __forceinline__ void tell_lost(uint32_t lost, int blocks) {
+    const int lane = threadIdx.x & 31;
+    if (lane < blocks) ptx::st_shared_cluster_u32(ptx::mapa_shared(lost, (uint32_t)lane), 1u);
+    ptx::fence_cluster();
+    __syncwarp();
+}
+// ... and behind it, where all copies have been started, every block then waits for its own, at most as long as a wait may
+// take (not all that it expects were sent), before any of them leaves.
+__device__ __forceinline__ void land_lost(const volatile uint32_t* lost, bool any, uint32_t inbox_bar, long long timeout_ns) {
+    if (*lost == 0u) return;
+    if (any) (void)drain_wait(inbox_bar, 0u, timeout_ns);
+    __syncwarp();
+    ptx::cluster_sync();
+}
+
 template <bool BF16>
 __device__ __forceinline__ void store_out(void* out, size_t idx, float v) {
     if (BF16)

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
     const uint32_t inbox_bar = bar0 + 8u * (2 * STAGES + 4), final_bar = inbox_bar + 8u;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* lost = tmem_slot + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int S = p.splits;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
         ptx::mbar_init(inbox_bar, 1);
         ptx::mbar_init(final_bar, 1), ptx::mbar_init(final_bar + 8u, 1);
         *abort_flag = 0u;
+        *lost = 0u;
         ptx::fence_barrier_init();
         if (S > 1 && own > 0) ptx::mbar_arrive_expect_tx(inbox_bar, (uint32_t)(S * NG * own * 16));
         ptx::fence_proxy_async_smem();
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
             }
         __syncwarp();
         if (own > 0) ok = warp_wait<true>(ok, inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!ok) tell_lost(sbase + C::OFF_MISC + 8u, S);
         // Nobody leaves before all have what was sent to them: what they sent has then been read.
         ptx::cluster_arrive_relaxed();
     }
@@ -294,6 +297,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_mid_kernel(const __grid_c
     if (S > 1) {
         __syncwarp();
         ptx::cluster_wait();
+        land_lost(lost, own > 0, inbox_bar, p.timeout_ns);
     }
 }
 

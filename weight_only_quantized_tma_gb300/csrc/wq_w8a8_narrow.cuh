@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     const uint32_t inbox_bar = bar0 + 8u * (2 * STAGES + 4), final_bar = inbox_bar + 8u;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* lost = tmem_slot + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int S = p.splits;
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         ptx::mbar_init(inbox_bar, 1);
         ptx::mbar_init(final_bar, 1), ptx::mbar_init(final_bar + 8u, 1);
         *abort_flag = 0u;
+        *lost = 0u;
         ptx::fence_barrier_init();
         if (S > 1 && own > 0) ptx::mbar_arrive_expect_tx(inbox_bar, (uint32_t)(S * H * 128 * own * 16));
         ptx::fence_proxy_async_smem();
@@ -272,6 +274,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         }
         __syncwarp();
         if (own > 0) ok = warp_wait<true>(ok, inbox_bar, 0u, abort_flag, p.status, DEVICE_TIMEOUT_EPILOGUE, p.timeout_ns);
+        if (!ok) tell_lost(sbase + C::OFF_MISC + 8u, S);
         // Nobody leaves before all have what was sent to them: what they sent has then been read.
         ptx::cluster_arrive_relaxed();
     }
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     if (S > 1) {
         __syncwarp();
         ptx::cluster_wait();
+        land_lost(lost, own > 0, inbox_bar, p.timeout_ns);
     }
 }
 
