@@ -1,5 +1,5 @@
-// wq_w8a8_narrow.cuh -- product of e4m3 activations and e4m3 weights for few tokens: weight rows are the
-// tensor cores' M dimension, tokens the N dimension.
+// wq_w8a8_narrow.cuh -- product of e4m3 activations and e4m3 weights for up to 32 tokens, which are one tile: weight rows
+// are the tensor cores' M dimension, tokens the N dimension.
 //
 //   acc[n][m] += (a_scale[kb][m] w_scale[n / 128][kb]) * D_kb[n][m],   D_kb = the tensor cores' sum over block kb
 //
@@ -13,7 +13,7 @@
 // Few tokens are bound by reading the weights: `splits` blocks of threads, one cluster, share a tile's k, so that
 // the grid fills the GPU.  Each then lays its sums out in shared memory and sends each owner of columns (tokens in
 // groups of four) its part in one copy; an owner adds the slices in order and finishes its tokens for all 128 rows.
-// (16-byte stores that each count on the owner's barrier took longer than the products: 128 x 4096 x 4096 18.2 us.)
+// (16-byte stores that each count on the owner's barrier took longer than the products.)
 #pragma once
 
 #include "wq_common.cuh"
@@ -32,12 +32,13 @@ struct NarrowCfg {
     static constexpr int STAGE = H * W_TILE + BN * 128;     // weight tiles, then the tokens' rows
     // Scales of a block of K: BN tokens', then the weights'.  They are part of the block's stage (its products wait
     // for them too).  A slot is filled again SCN blocks on, when the products of STAGES blocks before that have ended,
-    // for which the sums two blocks earlier had to be read: nobody reads it any more.
-    static constexpr int SCN = STAGES <= 2 ? 4 : 8;
+    // for which the sums two blocks earlier had to be released, and those of the block before that were finished with:
+    // nobody reads it any more.
+    static constexpr int SCN = 8;
     static constexpr int SC_SLOT = (BN + 4) * 4;
     static constexpr int OFF_SC = STAGES * STAGE;
-    static constexpr int INBOX = SMAX > 1 ? (BN / 4 + SMAX - 1) * 128 * 16 * H : 0;
-    static constexpr int OUTBOX = SMAX > 1 ? BN / 4 * 128 * 16 * H : 0;      // in the stages
+    static constexpr int INBOX = (BN / 4 + SMAX - 1) * 128 * 16 * H;
+    static constexpr int OUTBOX = BN / 4 * 128 * 16 * H;      // in the stages
     static constexpr int OFF_INBOX = ALIAS ? OUTBOX : OFF_SC + SCN * SC_SLOT;
     static constexpr int OFF_MOST = OFF_SC + SCN * SC_SLOT + (ALIAS ? 0 : INBOX);      // largest magnitudes [4 warps][BN]
     static constexpr int OFF_BAR = OFF_MOST + (GATED ? 4 * BN * 4 : 0);
@@ -46,9 +47,9 @@ struct NarrowCfg {
     static constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static constexpr int TMEM_COLS = 2 * H * BN < 32 ? 32 : 2 * H * BN;
-    static_assert(SCN >= STAGES + 2 && OUTBOX + (ALIAS ? INBOX : 0) <= STAGES * STAGE, "scales, inbox");
+    static_assert(SCN >= STAGES + 3 && OUTBOX + (ALIAS ? INBOX : 0) <= STAGES * STAGE, "scales, inbox");
     static_assert(STAGE % 1024 == 0 && OFF_INBOX % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
-    static_assert(TMEM_COLS * CTAS <= 512 && SMEM <= (CTAS == 1 ? 232448 : 115712), "resident blocks");
+    static_assert(TMEM_COLS * CTAS <= 512 && CTAS * (SMEM + 1024) <= 233472, "resident blocks");
 };
 
 template <typename C>
@@ -71,10 +72,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
 
     const int S = p.splits;
     const int rank = S > 1 ? (int)ptx::cluster_ctarank() : 0;
-    const int tile = (int)blockIdx.x / S;
-    const int nt = tile / p.tiles_m, mt = tile - nt * p.tiles_m;      // a weight tile's token tiles are neighbours
-    const int64_t m0 = (int64_t)mt * BN;
-    const int cols = (int)min((int64_t)BN, p.M - m0);
+    const int nt = (int)blockIdx.x / S, cols = (int)p.M;
     const int kb0 = (int)((int64_t)p.kblocks * rank / S), n_kb = (int)((int64_t)p.kblocks * (rank + 1) / S) - kb0;
     // columns in groups of four: this block finishes groups [g0, g0 + own)
     const int groups = (cols + 3) / 4, per = S > 1 ? (groups + S - 1) / S : BN / 4;
@@ -125,7 +123,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     if (warp == 4) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
-            const uint64_t pol_w = p.tiles_m == 1 ? ptx::policy_evict_first() : ptx::policy_evict_last();
+            const uint64_t pol_w = ptx::policy_evict_first();
             const uint64_t pol_a = ptx::policy_evict_last();
             const uint32_t bytes = (uint32_t)(H * C::W_TILE + p.box_m * 128);
             int i = 0, s = 0;
@@ -136,7 +134,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
 #pragma unroll
                 for (int h = 0; h < H; ++h)
                     ptx::tma_load_3d(dst + h * C::W_TILE, &p.tmap_w, (kb0 + i) * 128, nt * 128, h, full(s), pol_w);
-                ptx::tma_load_2d(dst + H * C::W_TILE, &p.tmap_a, (kb0 + i) * 128, (int)m0, full(s), pol_a);
+                ptx::tma_load_2d(dst + H * C::W_TILE, &p.tmap_a, (kb0 + i) * 128, 0, full(s), pol_a);
                 if (++s == STAGES) s = 0, ph ^= 1u;
             }
             // every stage released: the commits that arrive here have all landed
@@ -152,7 +150,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         // ------------------------------------------------------------ scales
         const int64_t wblocks = ((p.N + 127) >> 7) * p.kblocks;
         const float* sw = p.w_scale + (int64_t)nt * p.kblocks + kb0 + (lane < H ? lane * wblocks : 0);
-        const float* sa = p.a_scale + (int64_t)kb0 * p.M + m0;
+        const float* sa = p.a_scale + (int64_t)kb0 * p.M;
         int s = 0;
         uint32_t ph = 0;
         for (int i = 0; i < n_kb && wait_all(empty(s), ph ^ 1u, DEVICE_TIMEOUT_PRODUCER); ++i) {
@@ -198,17 +196,14 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         __syncwarp();
     } else {
         // ------------------------------------------------------------ sums
-        constexpr int CH = BN * H >= 256 || BN * H == 16 ? 16 : 32, NC = BN * H / CH;
+        constexpr int CH = BN * H == 16 ? 16 : 32, NC = BN * H / CH;
         const uint32_t base = tmem + ((uint32_t)(warp * 32) << 16);
         for (int i = 0; i < n_kb; ++i) {
             const int b = i & 1;
             if (!wait_all(acc_full(b), (uint32_t)(i >> 1) & 1u, DEVICE_TIMEOUT_TRANSFORM)) break;
             ptx::tc_fence_after();
             uint32_t v[2][CH];
-            auto load = [&](int c) {
-                if constexpr (CH == 32) ptx::tmem_ld32(base + b * H * BN + c * CH, v[c & 1]);
-                else ptx::tmem_ld16(base + b * H * BN + c * CH, v[c & 1]);
-            };
+            auto load = [&](int c) { ptx::tmem_ld(base + b * H * BN + c * CH, v[c & 1]); };
             const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC + i % SCN * C::SC_SLOT);
             uint64_t sw[H];
 #pragma unroll
@@ -251,8 +246,8 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
     ok = __all_sync(0xffffffffu, *abort_flag == 0u);
     const int row = threadIdx.x;      // of the tile
     // From here on sums lie in shared memory, [part][half][group of columns][row], and are worked on in small loops:
-    // code that runs once is bound by its own fetching (128 x 4096 x 4096: 38000 cycles unrolled over the columns in
-    // registers, four times those of the loop over K).
+    // code that runs once is bound by its own fetching (unrolled over 128 columns in registers it took four times as long
+    // as the loop over 32 blocks of K).
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -279,7 +274,7 @@ __global__ void __launch_bounds__(C::NTHREADS, C::CTAS) w8a8_narrow_kernel(const
         ptx::cluster_arrive_relaxed();
     }
     // ---- the tokens m_first .. of this block, all rows of the tile
-    const int64_t m_first = m0 + 4 * g0, n = (int64_t)nt * 128 + row;
+    const int64_t m_first = 4 * g0, n = (int64_t)nt * 128 + row;
     const int mine = (int)min((int64_t)(4 * own), p.M - m_first);
     uint8_t* parts = smem + (S > 1 ? C::OFF_INBOX : 0) + row * 16;
     float* most = reinterpret_cast<float*>(smem + C::OFF_MOST);
