@@ -434,8 +434,8 @@ wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_hea
  *     s = x + residual,   sum = RN(s),   out = RN(s * rsqrt(mean(s^2) + eps) * weight)
  * (the norm is of s before it is rounded; a NULL residual: s = x, and sum is not written).  The
  * mean holds for every s that fp32 holds.  Strides are elements from row to row.  sum may be
- * residual or x itself, out may be x or residual (same pointer and stride); sum and out differ, and
- * any other overlap is undefined.
+ * residual or x itself, out may be x or residual (same pointer and stride); sum and out differ (one
+ * pointer for both: WQ_ERR_SHAPE), and any other overlap is undefined.
  * Requirements: T >= 0, 8 <= H <= 32768, H % 8 == 0, eps >= 0, strides >= H and multiples of 8;
  * pointers 16-byte aligned. */
 wq_status wq_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
@@ -457,8 +457,9 @@ wq_status wq_quantize_fp8(const void* x, int64_t x_stride, wq_dtype dtype, int64
 /* Product of 8-bit activations and 8-bit weights:
  *     out[m][n] = sum_b a_scale[b][m] w_scale[n / 128][b] sum_{k in block b} a[m][k] w[n][k]  (+ bias[n])
  * a, a_scale: activations [M][K] as above.  w: e4m3 codes [N][K]; w_scale: fp32
- * [ceil(N / 128)][ceil(K / 128)], one for each block of 128 x 128.  Sums of a block and over the
- * blocks are held in fp32; out is 16-bit (dtype) [M][N], rounded once.  bias: NULL or [N] of dtype.
+ * [ceil(N / 128)][ceil(K / 128)], one for each block of 128 x 128.  Products of two scales, sums of
+ * a block and over the blocks are held in fp32 (scales whose product overflows there give infinities
+ * and NaN); out is 16-bit (dtype) [M][N], rounded once.  bias: NULL or [N] of dtype.
  * A NaN among a token's codes or scales makes that token's outputs NaN, one of a weight row that
  * row's column.  Results do not change from run to run.
  * Requirements: M >= 0, N >= 8, N % 8 == 0, N <= 2^29, 16 <= K <= 2^30, K % 16 == 0, N * K < 2^40,
@@ -470,10 +471,10 @@ wq_status wq_gemm_w8a8_fp8(const uint8_t* a, const float* a_scale, const uint8_t
 
 /* First half of a gated feed-forward block:
  *     gate = a . w[0 .. F)^T,  up = a . w[F .. 2F)^T,  h = gate / (1 + exp(-gate)) * up
- * (products as wq_gemm_w8a8_fp8's, h in fp32).  w: [2 F][K]; w_scale: fp32 [2][ceil(F / 128)]
- * [ceil(K / 128)], the blocks of either half counted from its own first row.  Output: codes [M][F]
- * and scales [ceil(F / 128)][M] of h (out NULL, dtype ignored), or out, 16-bit [M][F], rounded once
- * (codes and scales NULL).
+ * (products as wq_gemm_w8a8_fp8's, h in fp32: zero where exp(-gate) overflows there, gates below
+ * -88.7).  w: [2 F][K]; w_scale: fp32 [2][ceil(F / 128)][ceil(K / 128)], the blocks of either half
+ * counted from its own first row.  Output: codes [M][F] and scales [ceil(F / 128)][M] of h (out NULL,
+ * dtype ignored), or out, 16-bit [M][F], rounded once (codes and scales NULL).
  * Requirements: as above with N = F, F % 16 == 0; codes 16-byte aligned. */
 wq_status wq_gemm_w8a8_fp8_gated(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale,
                                  int64_t M, int64_t F, int64_t K, wq_dtype dtype, void* out, uint8_t* codes,

@@ -132,3 +132,12 @@ def test_binding_refusals(machine, monkeypatch):  # noqa: F811
         with pytest.raises(ValueError):
             call()
     assert not machine.calls
+
+
+def test_one_buffer_for_sum_and_output_is_refused(L):
+    def f(s, out, r=P):
+        return L.wq_add_rms_norm(P, 256, r, 256, 0, 4, 256, P, 1e-6, s, 256, out, 256, None)
+    Q = P + 0x10000
+    assert f(Q, Q) == SHAPE and f(P, P) == SHAPE
+    if not torch.cuda.is_available():      # (what is allowed gets as far as the device)
+        assert f(P, Q) not in (SHAPE, NULL, MISALIGNED) and f(Q, P) not in (SHAPE, NULL, MISALIGNED)

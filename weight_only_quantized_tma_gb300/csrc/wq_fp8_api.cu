@@ -36,6 +36,7 @@ wq_status norm_call(const void* x, int64_t x_stride, const void* residual, int64
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(out, 16) ||
         !aligned(codes, 16) || !aligned(scales, 4))
         return WQ_ERR_MISALIGNED;
+    if (residual && !quant && sum == out) return WQ_ERR_SHAPE;      // (each would be the other's)
     DeviceState d{};
     const wq_status st = (wq_status)current_device_state(&d);
     if (st != WQ_OK) return st;
