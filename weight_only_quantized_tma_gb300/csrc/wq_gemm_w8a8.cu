@@ -174,7 +174,7 @@ struct Wide {
                                CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode_tensor_map(&p.tmap_out, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                                codes ? (const void*)p.codes : p.out, 2, o_dims, o_strides, o_box,
-                               codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+                               codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[2] = {};

@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                 if (!wait_all(pair_bar(quarter), turn & 1u, DEVICE_TIMEOUT_EPILOGUE)) break;
                 const BlockScale q(max_nan(most, *reinterpret_cast<const float*>(smem + C::OFF_OUT + ((warp - 4) ^ 4) * C::OUT_WARP + at)));
                 if (g == 0 && m < p.M) p.scales[(int64_t)nt * p.M + m] = q.scale;
+                // rows of 64 bytes, in the order of the 64-byte swizzle (plain rows share banks: 289 -> 284 us for 4096 x
+                // 11008 x 4096)
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) {
                     uint32_t o[4];
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) w8a8_wide_kernel(const __grid_
                         const float* a = acc + c + 4 * j;
                         o[j] = q.codes(a[0], a[1], a[2], a[3]);
                     }
-                    *reinterpret_cast<uint4*>(out_s + lane * 64 + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(out_s + lane * 64 + (c ^ ((lane >> 1 & 3) << 4))) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             ptx::fence_proxy_async_smem();
