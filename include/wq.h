@@ -428,7 +428,8 @@ wq_status wq_attn_kv4_workspace_bytes(const wq_kv4_layout* layout, int32_t q_hea
  * of a block's fp32 values y: both quotients are rounded to fp32, a code to the nearest e4m3
  * number (ties to the even code), as IEEE division and conversion do.  (Where scale is below 2^-93
  * the second quotient may be off by its last bit.)  A block that holds an infinity or a NaN
- * gets a NaN for its scale: its values are NaN (codes 0), and no other block is touched. */
+ * gets a NaN for its scale: its values are NaN (codes 0), and no other block is touched.
+ * Outputs lie over no input, but where that is said. */
 
 /* Norm of rows with the residual's addition, T rows of H values, in fp32 with one rounding:
  *     s = x + residual,   sum = RN(s),   out = RN(s * rsqrt(mean(s^2) + eps) * weight)

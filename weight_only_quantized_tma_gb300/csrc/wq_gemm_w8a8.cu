@@ -192,11 +192,11 @@ struct Wide {
 // pair's, whichever ends first.  What a block of K takes is measured (10 ns): 33 in a tile of a block's own (62 gated),
 // 42 (44) in a pair's, which is four times as large (gated twice).  Both measured, in us:
 //   tokens x rows x K           own   pair      tokens x rows x K, gated    own   pair
-//   333 x 4096 x 4096          14.1   18.4      64 x 11008 x 4096          23.0   35.7
-//   512 x 4096 x 4096          14.7   18.5      250 x 4096 x 4096          22.9   19.7
-//   768 x 4096 x 4096          35.7   19.0      250 x 11008 x 4096         46.9   36.2
-//   333 x 12288 x 4096         29.7   33.6      777 x 6928 x 2560          53.7   36.5
-//   512 x 12288 x 4096         43.7   33.8
+//   333 x 4096 x 4096          14.3   18.9      64 x 11008 x 4096          22.7   34.5
+//   512 x 4096 x 4096          14.9   19.1      250 x 4096 x 4096          22.7   19.0
+//   768 x 4096 x 4096          35.9   19.2      250 x 11008 x 4096         46.8   35.3
+//   333 x 12288 x 4096         29.6   33.6      777 x 6928 x 2560          53.5   34.9
+//   512 x 12288 x 4096         43.7   34.1
 // (Weight rows as M in tiles of 64 or 128 tokens took longer than tokens as M from 33 tokens on, by an eighth to a third.)
 template <bool GATED>
 cudaError_t launch_many(const W8A8Params& p, int sms, cudaStream_t st) {

@@ -137,8 +137,9 @@ __device__ __noinline__ void norm_again(const NormParams& p, int64_t t, bool lar
 // One row for each group of `blockDim.x` threads (blockDim.y rows in a block; more than one only where a
 // row is one warp).  Thread i holds values 8 (i + c blockDim.x) .. + 7 of chunk c < C, so 16 neighbouring
 // lanes hold one block of 128.  Bound by memory from some 100 rows on, as far as rows are on their way: hence the
-// bounds on registers, which keep 1200 to 2000 threads on an SM (4000 x 11008 to 8 bits 41 -> 33 us), and the weight
-// read late.  8192 x 4096 with a residual: 42.6 us (6.3 TB/s), to 8 bits 42 (5.6 TB/s; issue slots 56 % full).  Tried:
+// bounds on registers, which keep 1000 to 2000 threads on an SM (512 for rows past 16384 values with a residual; 4000 x
+// 11008 to 8 bits 41 -> 34 us), and the weight read late.  8192 x 4096 with a residual: 42.1 us (6.4 TB/s), to 8 bits
+// 43.6 (5.4 TB/s; issue slots 72 % full).  The mean is the sum times 1 / H, a rounding more than a division.  Tried:
 // blocks that stay, rows arriving by bulk copies (43 to 46 us), the next row loaded into registers early (43 to 44).
 template <bool BF16, int C, bool ADD, bool QUANT>
 __global__ void __launch_bounds__(512, C == 8 ? (ADD ? 1 : 2) : C == 4 ? (ADD ? 2 : 3) : C == 2 ? (ADD ? 3 : 4) : 4) norm_kernel(const __grid_constant__ NormParams p) {
